@@ -18,4 +18,7 @@ from ._lib import (  # noqa: F401
     gemm_ue8m0,
     bfp8_linear_fp8, bfp8_linear_fp8_workspace_size, linear_workspace, bfp8_gemm_noalloc,
     NOALLOC_SCRATCH_BYTES,
+    KV_MAX_REQUESTS, KV_TILE, KVPlan, attn_paged, attn_paged_workspace, bfp8_attn_paged,
+    bfp8_attn_paged_workspace_size, bfp8_kv_append, bfp8_kv_plan, kv_cache_buffers, kv_plan,
+    kv_plan_buffers,
 )

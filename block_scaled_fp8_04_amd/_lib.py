@@ -8,6 +8,7 @@ no fallback: if the library is missing the call raises.
 """
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -30,12 +31,17 @@ BFP8_ERR_SCRATCH = 8
 # bytes of the device scratch array behind bfp8_gemm_noalloc (include/bfp8.h)
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
+# limits of the paged cache (include/bfp8.h)
+KV_MAX_REQUESTS = 4096
+KV_TILE = 128
+
 EXPORTS = ("bfp8_act_quant", "bfp8_weight_dequant", "bfp8_gemm", "bfp8_gemm_workspace_size",
            "bfp8_gemm_grouped", "bfp8_e4m3_encode_range", "bfp8_bf16_round_range",
            "bfp8_gemm_kernel_name", "bfp8_moe_dispatch_workspace_size", "bfp8_moe_dispatch",
            "bfp8_act_quant_rows", "bfp8_moe_combine", "bfp8_gemm_bf16", "bfp8_gemm_bf16_workspace_size",
            "bfp8_gemm_act_quant", "bfp8_gemm_swiglu_act_quant", "bfp8_act_quant_ue8m0",
            "bfp8_gemm_ue8m0", "bfp8_gemm_ue8m0_workspace_size", "bfp8_linear_fp8_workspace_size", "bfp8_linear_fp8", "bfp8_gemm_noalloc",
+           "bfp8_kv_plan", "bfp8_kv_append", "bfp8_attn_paged", "bfp8_attn_paged_workspace_size",
            "bfp8_status_string", "bfp8_version")
 
 _lib = None
@@ -101,6 +107,17 @@ def library():
     lib.bfp8_gemm_bf16.restype = ctypes.c_int
     lib.bfp8_gemm_bf16_workspace_size.argtypes = [I64, I64, I64]
     lib.bfp8_gemm_bf16_workspace_size.restype = ctypes.c_size_t
+    F32, SZ = ctypes.c_float, ctypes.c_size_t
+    lib.bfp8_kv_plan.argtypes = [P, P, I64, P, I64, P, P, I64, I32, P, P, P, P, P, I64, P, P]
+    lib.bfp8_kv_plan.restype = ctypes.c_int
+    lib.bfp8_kv_append.argtypes = [P, I64, I64, P, I64, I64, P, I64, P, P, P, P, I64, I32, I32, I32,
+                                   I32, P]
+    lib.bfp8_kv_append.restype = ctypes.c_int
+    lib.bfp8_attn_paged.argtypes = [P, I64, I64, P, P, P, P, I64, I32, P, I64, P, P, P, I64, I64, I64,
+                                    I32, I32, I32, I32, F32, P, P, P, SZ, P]
+    lib.bfp8_attn_paged.restype = ctypes.c_int
+    lib.bfp8_attn_paged_workspace_size.argtypes = [I64, I64, I32, I32, I32, I32]
+    lib.bfp8_attn_paged_workspace_size.restype = SZ
     lib.bfp8_status_string.argtypes = [ctypes.c_int]
     lib.bfp8_status_string.restype = ctypes.c_char_p
     lib.bfp8_version.argtypes = []
@@ -438,6 +455,147 @@ def bfp8_moe_combine(expert_out, slot_row, weights, y, stream=None):
         _stream(stream, y.device)))
 
 
+# ------------------------------------------------- attention over the paged e4m3 cache
+
+class KVPlan(NamedTuple):
+    """What bfp8_kv_plan writes for one step (all int32, on the GPU; see include/bfp8.h)."""
+    q_offsets: torch.Tensor       # [R+1] first new token of each request
+    kv_lens: torch.Tensor         # [R]   cached plus new tokens, 0 for an idle or refused request
+    tile_offsets: torch.Tensor    # [R+1] prefix sums of ceil(kv_lens / 128)
+    slot_map: torch.Tensor        # [T]   page * page_size + offset of each new token, or -1
+    positions: torch.Tensor       # [T]   position of each new token in its request, or -1
+    counts: torch.Tensor          # [4]   tokens, free_head after this step, requests kept, pages wanted
+
+
+def kv_plan_buffers(R, T, device) -> KVPlan:
+    """Output arrays of bfp8_kv_plan for R requests and a capacity of T new tokens."""
+    sizes = (R + 1, R, R + 1, T, T, 4)
+    return KVPlan(*(torch.empty(n, dtype=torch.int32, device=device) for n in sizes))
+
+
+def _need_i32(device, *named):
+    for name, t, shape in named:
+        if t.dtype is not torch.int32 or t.device != device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor on the call's GPU")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def bfp8_kv_plan(ctx_lens, new_lens, free_pages, block_table, page_size, plan, free_head=None,
+                 stream=None):
+    """Slots, positions and offsets of a step's new tokens into ``plan`` (kv_plan_buffers), and the
+    pages taken for them into block_table int32 [R, W] (in place).
+
+    ctx_lens, new_lens int32 [R]: cached and new tokens of each request; free_pages int32 [F]:
+    pages that may be taken, of which free_head int32 [1] are already (None: none are)."""
+    dev = ctx_lens.device
+    _need(ctx_lens.is_cuda, "all tensors must be on the GPU")
+    _need(block_table.dim() == 2 and free_pages.dim() == 1, "block_table [R, W], free_pages [F]")
+    R, W = block_table.shape
+    T = plan.slot_map.shape[0]
+    _need_i32(dev, ("ctx_lens", ctx_lens, (R,)), ("new_lens", new_lens, (R,)),
+              ("free_pages", free_pages, None), ("block_table", block_table, None),
+              ("q_offsets", plan.q_offsets, (R + 1,)), ("kv_lens", plan.kv_lens, (R,)),
+              ("tile_offsets", plan.tile_offsets, (R + 1,)), ("slot_map", plan.slot_map, (T,)),
+              ("positions", plan.positions, (T,)), ("counts", plan.counts, (4,)))
+    if free_head is not None:
+        _need_i32(dev, ("free_head", free_head, (1,)))
+    _check("bfp8_kv_plan", library().bfp8_kv_plan(
+        ctx_lens.data_ptr(), new_lens.data_ptr(), R, free_pages.data_ptr(), free_pages.shape[0],
+        free_head.data_ptr() if free_head is not None else None, block_table.data_ptr(), W,
+        page_size, plan.q_offsets.data_ptr(), plan.kv_lens.data_ptr(), plan.tile_offsets.data_ptr(),
+        plan.slot_map.data_ptr(), plan.positions.data_ptr(), T, plan.counts.data_ptr(),
+        _stream(stream, dev)))
+
+
+def kv_cache_buffers(num_pages, heads, page_size, dk, dv, device):
+    """(k_cache, k_scales, v_cache, v_scales) of one layer: codes uint8 [P, H, B, Dk] and
+    [P, H, Dv, B] (values lie token-contiguous), scales fp32 [P, H]."""
+    return (torch.empty(num_pages, heads, page_size, dk, dtype=torch.uint8, device=device),
+            torch.empty(num_pages, heads, dtype=torch.float32, device=device),
+            torch.empty(num_pages, heads, dv, page_size, dtype=torch.uint8, device=device),
+            torch.empty(num_pages, heads, dtype=torch.float32, device=device))
+
+
+def _cache_shape(device, k_cache, k_scales, v_cache, v_scales):
+    """(P, H, B, Dk, Dv) of a layer's cache, checked."""
+    for t in (k_cache, v_cache):
+        if t.dtype is not torch.uint8 and t.dtype is not torch.float8_e4m3fn:
+            raise TypeError(f"expected e4m3 codes (uint8 or float8_e4m3fn), got {t.dtype}")
+    _need(k_cache.dim() == 4 and v_cache.dim() == 4, "k_cache [P, H, B, Dk], v_cache [P, H, Dv, B]")
+    P, H, B, dk = k_cache.shape
+    dv = v_cache.shape[2]
+    _need(v_cache.shape == (P, H, dv, B), "v_cache must be [P, H, Dv, B] next to k_cache [P, H, B, Dk]")
+    _need(k_scales.dtype is torch.float32 and v_scales.dtype is torch.float32 and
+          k_scales.shape == (P, H) and v_scales.shape == (P, H), "scales must be fp32 [P, H]")
+    for t in (k_cache, k_scales, v_cache, v_scales):
+        _need(t.device == device and t.is_contiguous(),
+              "the cache must be contiguous, on the call's GPU")
+    return P, H, B, dk, dv
+
+
+def bfp8_kv_append(k, v, slot_map, k_cache, k_scales, v_cache, v_scales, stream=None):
+    """Quantizes k bf16 [T, H, Dk] and v bf16 [T, H, Dv] (any token and head strides, such as
+    slices of one projection) into the slots of slot_map int32 [T] (in place)."""
+    dev = k.device
+    _need(k.is_cuda, "all tensors must be on the GPU")
+    P, H, B, dk, dv = _cache_shape(dev, k_cache, k_scales, v_cache, v_scales)
+    _need(k.dtype is torch.bfloat16 and v.dtype is torch.bfloat16, "k and v must be bf16")
+    T = slot_map.shape[0]
+    _need(k.shape == (T, H, dk) and v.shape == (T, H, dv), "k must be [T, H, Dk], v [T, H, Dv]")
+    _need(v.device == dev and (T == 0 or (k.stride(2) == 1 and v.stride(2) == 1)),
+          "k and v must be on one GPU, their rows contiguous")
+    _need_i32(dev, ("slot_map", slot_map, (T,)))
+    _check("bfp8_kv_append", library().bfp8_kv_append(
+        k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1),
+        slot_map.data_ptr(), T, k_cache.data_ptr(), k_scales.data_ptr(), v_cache.data_ptr(),
+        v_scales.data_ptr(), P, B, H, dk, dv, _stream(stream, dev)))
+
+
+def bfp8_attn_paged_workspace_size(R, max_new, heads_q, heads_kv, dk, dv) -> int:
+    return int(library().bfp8_attn_paged_workspace_size(int(R), int(max_new), int(heads_q),
+                                                        int(heads_kv), int(dk), int(dv)))
+
+
+def attn_paged_workspace(R, max_new, heads_q, heads_kv, dk, dv, device):
+    """A workspace for bfp8_attn_paged at these sizes."""
+    n = bfp8_attn_paged_workspace_size(R, max_new, heads_q, heads_kv, dk, dv)
+    return torch.empty(max(16, n), dtype=torch.uint8, device=device)
+
+
+def bfp8_attn_paged(q, k_cache, k_scales, v_cache, v_scales, block_table, q_offsets, kv_lens,
+                    tile_offsets, max_new, scale, out, lse=None, workspace=None, stream=None):
+    """out bf16 [T, Hq, Dv] (and lse fp32 [T, Hq]) = causal attention of each request's new tokens,
+    q bf16 [T, Hq, Dk] (any token and head strides), over its pages.  q_offsets, kv_lens and
+    tile_offsets come from bfp8_kv_plan; max_new bounds the requests' new tokens."""
+    dev = q.device
+    _need(q.is_cuda, "all tensors must be on the GPU")
+    P, H, B, dk, dv = _cache_shape(dev, k_cache, k_scales, v_cache, v_scales)
+    _need(q.dtype is torch.bfloat16 and out.dtype is torch.bfloat16, "q and out must be bf16")
+    _need(q.dim() == 3 and q.shape[2] == dk and (q.stride(2) == 1 or q.numel() == 0),
+          "q must be [T, Hq, Dk], rows contiguous")
+    T, Hq, _ = q.shape
+    _need(out.shape == (T, Hq, dv) and out.device == dev and out.is_contiguous(),
+          "out must be a contiguous [T, Hq, Dv] on q's GPU")
+    _need(block_table.dim() == 2, "block_table must be [R, W]")
+    R, W = block_table.shape
+    _need_i32(dev, ("block_table", block_table, None), ("q_offsets", q_offsets, (R + 1,)),
+              ("kv_lens", kv_lens, (R,)), ("tile_offsets", tile_offsets, (R + 1,)))
+    if lse is not None:
+        _need(lse.dtype is torch.float32 and lse.shape == (T, Hq) and lse.device == dev and
+              lse.is_contiguous(), "lse must be a contiguous fp32 [T, Hq] on q's GPU")
+    ws_bytes = 0
+    if workspace is not None:
+        _need(workspace.device == dev and workspace.is_contiguous(), "workspace must be on q's GPU")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _check("bfp8_attn_paged", library().bfp8_attn_paged(
+        q.data_ptr(), q.stride(0), q.stride(1), k_cache.data_ptr(), k_scales.data_ptr(),
+        v_cache.data_ptr(), v_scales.data_ptr(), P, B, block_table.data_ptr(), W,
+        q_offsets.data_ptr(), kv_lens.data_ptr(), tile_offsets.data_ptr(), R, T, max_new, Hq, H, dk,
+        dv, scale, out.data_ptr(), lse.data_ptr() if lse is not None else None,
+        workspace.data_ptr() if workspace is not None else None, ws_bytes, _stream(stream, dev)))
+
+
 # ------------------------------------------------------- allocating conveniences
 
 def act_quant(x, stream=None):
@@ -553,3 +711,24 @@ def moe_experts_fp8(x, topk_idx, weights, w, w_s, expert_lo, stream=None):
     out = torch.empty((cap, N), dtype=torch.bfloat16, device=x.device)
     bfp8_gemm_grouped(q, qs, w, w_s, out, off, stream)
     return moe_combine(out, slot_row, weights, stream)
+
+
+def kv_plan(ctx_lens, new_lens, free_pages, block_table, page_size, num_tokens, free_head=None,
+            stream=None):
+    """bfp8_kv_plan into new arrays; num_tokens is the step's token capacity."""
+    plan = kv_plan_buffers(block_table.shape[0], num_tokens, block_table.device)
+    bfp8_kv_plan(ctx_lens, new_lens, free_pages, block_table, page_size, plan, free_head, stream)
+    return plan
+
+
+def attn_paged(q, cache, block_table, plan, max_new, scale=None, workspace=None, stream=None):
+    """Attention over a layer's cache (kv_cache_buffers) as planned by kv_plan; scale defaults to
+    Dk**-0.5.  Returns out bf16 [T, Hq, Dv]; rows of no request are zero."""
+    T, Hq, dk = q.shape
+    H, dv = cache[0].shape[1], cache[2].shape[2]
+    out = torch.zeros((T, Hq, dv), dtype=torch.bfloat16, device=q.device)
+    if workspace is None:
+        workspace = attn_paged_workspace(block_table.shape[0], max_new, Hq, H, dk, dv, q.device)
+    bfp8_attn_paged(q, *cache, block_table, plan.q_offsets, plan.kv_lens, plan.tile_offsets, max_new,
+                    dk ** -0.5 if scale is None else scale, out, None, workspace, stream)
+    return out

@@ -272,6 +272,137 @@ int bfp8_moe_combine(const void* expert_out_bf16, int64_t rows, const int32_t* s
                                              k, N, (hipStream_t)stream));
 }
 
+static bool kv_page_ok(int32_t page) { return page == 32 || page == 64 || page == 128; }
+static bool kv_dims_ok(int32_t dk, int32_t dv) {
+    return (dk == 64 && dv == 64) || (dk == 128 && dv == 128) || (dk == 192 && dv == 128);
+}
+// slots of the pool and of a table row are 32-bit
+static bool kv_slots_ok(int64_t pages, int32_t page) {
+    return pages >= 0 && pages < ((int64_t)1 << 31) / page;
+}
+
+int bfp8_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int64_t R,
+                 const int32_t* free_pages, int64_t n_free, const int32_t* free_head,
+                 int32_t* block_table, int64_t table_width, int32_t page_size, int32_t* q_offsets,
+                 int32_t* kv_lens, int32_t* tile_offsets, int32_t* slot_map, int32_t* positions,
+                 int64_t T, int32_t* counts, void* stream) {
+    static_assert(BFP8_KV_MAX_REQUESTS == bfp8::kKvMaxRequests && BFP8_KV_TILE == bfp8::kKvTile,
+                  "kv plan limits");
+    const int64_t lim = (int64_t)1 << 31;
+    if (!kv_page_ok(page_size)) return BFP8_ERR_ARG;
+    if (R < 0 || T < 0 || T >= lim || n_free < 0 || n_free >= lim ||
+        !kv_slots_ok(table_width, page_size))
+        return BFP8_ERR_SHAPE;
+    if (R > BFP8_KV_MAX_REQUESTS) return BFP8_ERR_GROUPS;
+    if (!q_offsets || !tile_offsets || !counts) return BFP8_ERR_NULL;
+    if (R > 0 && (!ctx_lens || !new_lens || !kv_lens || (table_width > 0 && !block_table)))
+        return BFP8_ERR_NULL;
+    if ((n_free > 0 && !free_pages) || (T > 0 && (!slot_map || !positions))) return BFP8_ERR_NULL;
+    if (!aligned(ctx_lens, 4) || !aligned(new_lens, 4) || !aligned(free_pages, 4) ||
+        !aligned(free_head, 4) || !aligned(block_table, 4) || !aligned(q_offsets, 4) ||
+        !aligned(kv_lens, 4) || !aligned(tile_offsets, 4) || !aligned(slot_map, 4) ||
+        !aligned(positions, 4) || !aligned(counts, 4))
+        return BFP8_ERR_ALIGN;
+    return from_hip(bfp8::launch_kv_plan(ctx_lens, new_lens, R, free_pages, n_free, free_head,
+                                         block_table, table_width, page_size, q_offsets, kv_lens,
+                                         tile_offsets, slot_map, positions, T, counts,
+                                         (hipStream_t)stream));
+}
+
+int bfp8_kv_append(const void* k_bf16, int64_t k_token_stride, int64_t k_head_stride,
+                   const void* v_bf16, int64_t v_token_stride, int64_t v_head_stride,
+                   const int32_t* slot_map, int64_t T, void* k_cache, float* k_scales,
+                   void* v_cache, float* v_scales, int64_t num_pages, int32_t page_size,
+                   int32_t heads, int32_t dk, int32_t dv, void* stream) {
+    if (!kv_page_ok(page_size)) return BFP8_ERR_ARG;
+    if (T < 0 || T >= ((int64_t)1 << 31) || heads < 1 || heads > 65535 || !kv_dims_ok(dk, dv) ||
+        !kv_slots_ok(num_pages, page_size) || k_token_stride < 0 || k_head_stride < 0 ||
+        v_token_stride < 0 || v_head_stride < 0)
+        return BFP8_ERR_SHAPE;
+    if (T == 0 || num_pages == 0) return BFP8_OK;
+    if (!k_bf16 || !v_bf16 || !slot_map || !k_cache || !k_scales || !v_cache || !v_scales)
+        return BFP8_ERR_NULL;
+    if (!aligned(k_bf16, 2) || !aligned(v_bf16, 2) || !aligned(slot_map, 4) ||
+        !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scales, 4) ||
+        !aligned(v_scales, 4))
+        return BFP8_ERR_ALIGN;
+    return from_hip(bfp8::launch_kv_append(k_bf16, k_token_stride, k_head_stride, v_bf16,
+                                           v_token_stride, v_head_stride, slot_map, T, k_cache,
+                                           k_scales, v_cache, v_scales, num_pages, page_size,
+                                           heads, dk, dv, (hipStream_t)stream));
+}
+
+// Sizes of an attention call that its workspace depends on.
+static bool attn_sizes_ok(int64_t R, int64_t max_new, int32_t heads_q, int32_t heads_kv, int32_t dk,
+                          int32_t dv) {
+    return R >= 0 && max_new >= 0 && heads_kv >= 1 && heads_q >= heads_kv &&
+           heads_q % heads_kv == 0 && heads_q <= 65535 &&
+           max_new < ((int64_t)1 << 31) / heads_q && kv_dims_ok(dk, dv);
+}
+
+size_t bfp8_attn_paged_workspace_size(int64_t R, int64_t max_new, int32_t heads_q,
+                                      int32_t heads_kv, int32_t dk, int32_t dv) {
+    if (!attn_sizes_ok(R, max_new, heads_q, heads_kv, dk, dv) || R == 0 || max_new == 0 ||
+        R > BFP8_KV_MAX_REQUESTS)
+        return 0;
+    return bfp8::attn_paged_workspace_bytes(R, max_new, heads_q, heads_kv, dk, dv);
+}
+
+int bfp8_attn_paged(const void* q_bf16, int64_t q_token_stride, int64_t q_head_stride,
+                    const void* k_cache, const float* k_scales, const void* v_cache,
+                    const float* v_scales, int64_t num_pages, int32_t page_size,
+                    const int32_t* block_table, int64_t table_width, const int32_t* q_offsets,
+                    const int32_t* kv_lens, const int32_t* tile_offsets, int64_t R, int64_t T,
+                    int64_t max_new, int32_t heads_q, int32_t heads_kv, int32_t dk, int32_t dv,
+                    float scale, void* out_bf16, float* lse, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+    if (!kv_page_ok(page_size) || !(scale - scale == 0.0f)) return BFP8_ERR_ARG;
+    if (!attn_sizes_ok(R, max_new, heads_q, heads_kv, dk, dv) || T < 0 ||
+        T >= ((int64_t)1 << 31) || q_token_stride < 0 || q_head_stride < 0 ||
+        !kv_slots_ok(num_pages, page_size) || !kv_slots_ok(table_width, page_size))
+        return BFP8_ERR_SHAPE;
+    if (R > BFP8_KV_MAX_REQUESTS) return BFP8_ERR_GROUPS;
+    if (R == 0 || T == 0) return BFP8_OK;
+    if (max_new < 1) return BFP8_ERR_SHAPE;
+    if (!q_bf16 || !q_offsets || !kv_lens || !tile_offsets || !out_bf16) return BFP8_ERR_NULL;
+    if (num_pages > 0 && table_width > 0 &&
+        (!k_cache || !k_scales || !v_cache || !v_scales || !block_table))
+        return BFP8_ERR_NULL;
+    if (!aligned(q_bf16, 2) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(k_scales, 4) || !aligned(v_scales, 4) || !aligned(block_table, 4) ||
+        !aligned(q_offsets, 4) || !aligned(kv_lens, 4) || !aligned(tile_offsets, 4) ||
+        !aligned(out_bf16, 16) || !aligned(lse, 4) || !aligned(workspace, 16))
+        return BFP8_ERR_ALIGN;
+    if (workspace && workspace_bytes < bfp8::attn_paged_workspace_bytes(R, max_new, heads_q,
+                                                                        heads_kv, dk, dv))
+        return BFP8_ERR_WORKSPACE;
+    bfp8::AttnArgs a;
+    a.q = (const uint16_t*)q_bf16;
+    a.q_ts = q_token_stride;
+    a.q_hs = q_head_stride;
+    a.k_cache = (const uint8_t*)k_cache;
+    a.k_scales = k_scales;
+    a.v_cache = (const uint8_t*)v_cache;
+    a.v_scales = v_scales;
+    a.pages = num_pages;
+    a.block_table = block_table;
+    a.width = num_pages > 0 ? table_width : 0;      // no pool: no request sees a token
+    a.q_offsets = q_offsets;
+    a.kv_lens = kv_lens;
+    a.tile_offsets = tile_offsets;
+    a.R = (int)R;
+    a.heads_q = heads_q;
+    a.heads_kv = heads_kv;
+    a.log_b = __builtin_ctz(page_size);
+    a.T = T;
+    a.max_new = max_new;
+    a.scale = scale;
+    a.out = (uint16_t*)out_bf16;
+    a.lse = lse;
+    a.ws = (float*)workspace;
+    return from_hip(bfp8::launch_attn_paged(a, dk, dv, (hipStream_t)stream));
+}
+
 const char* bfp8_gemm_kernel_name(int64_t M, int64_t N, int64_t K) {
     if (M <= 0 || N <= 0 || K <= 0 || K % BFP8_BLOCK != 0) return "none";
     return bfp8::gemm_config_name(bfp8::gemm_config(M, N, K));

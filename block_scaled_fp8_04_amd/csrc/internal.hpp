@@ -85,4 +85,44 @@ hipError_t launch_moe_combine(const void* out, int64_t rows_cap, const int32_t* 
                               const float* weight, void* y, int64_t T, int32_t k, int64_t N,
                               hipStream_t stream);
 
+// Requests of one step, and tokens per tile of the plan's tile offsets (kv_cache.hip,
+// attn_paged.hip).
+constexpr int kKvMaxRequests = 4096;
+constexpr int kKvTile = 128;
+hipError_t launch_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int64_t R,
+                          const int32_t* free_pages, int64_t n_free, const int32_t* free_head,
+                          int32_t* block_table, int64_t width, int32_t page, int32_t* q_offsets,
+                          int32_t* kv_lens, int32_t* tile_offsets, int32_t* slot_map,
+                          int32_t* positions, int64_t T, int32_t* counts, hipStream_t stream);
+hipError_t launch_kv_append(const void* k, int64_t k_ts, int64_t k_hs, const void* v, int64_t v_ts,
+                            int64_t v_hs, const int32_t* slot_map, int64_t T, void* k_cache,
+                            float* k_scales, void* v_cache, float* v_scales, int64_t pages,
+                            int32_t page, int32_t heads, int32_t dk, int32_t dv,
+                            hipStream_t stream);
+
+// Arguments of one paged-attention call (validated by the ABI layer).
+struct AttnArgs {
+    const uint16_t* q;
+    int64_t q_ts, q_hs;
+    const uint8_t* k_cache;
+    const float* k_scales;
+    const uint8_t* v_cache;
+    const float* v_scales;
+    int64_t pages;
+    const int32_t* block_table;
+    int64_t width;
+    const int32_t* q_offsets;
+    const int32_t* kv_lens;
+    const int32_t* tile_offsets;
+    int R, heads_q, heads_kv, log_b;
+    int64_t T, max_new;
+    float scale;
+    uint16_t* out;
+    float* lse;
+    float* ws;
+};
+size_t attn_paged_workspace_bytes(int64_t R, int64_t max_new, int32_t heads_q, int32_t heads_kv,
+                                  int32_t dk, int32_t dv);
+hipError_t launch_attn_paged(const AttnArgs& a, int32_t dk, int32_t dv, hipStream_t stream);
+
 }  // namespace bfp8

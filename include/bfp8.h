@@ -348,6 +348,149 @@ int bfp8_moe_combine(const void* expert_out_bf16, int64_t rows, const int32_t* s
                      const float* weights, void* y_bf16, int64_t T, int32_t k, int64_t N,
                      void* stream);
 
+/* ----------------------------------------------------------------------
+ * Attention over a paged cache held in e4m3, next to the fp8 linear path: a
+ * serving step plans its pages on the GPU (bfp8_kv_plan), quantizes the new
+ * tokens' keys and values into the cache (bfp8_kv_append) and attends over
+ * it (bfp8_attn_paged), with no host synchronization in between.
+ *
+ * The cache of one layer is a pool of num_pages pages of B = page_size tokens
+ * (32, 64 or 128) with H KV heads:
+ *   k_cache  : e4m3 [num_pages, H, B, Dk]     k_scales : fp32 [num_pages, H]
+ *   v_cache  : e4m3 [num_pages, H, Dv, B]     v_scales : fp32 [num_pages, H]
+ * Values are stored token-contiguous, the order in which the second matrix
+ * product of attention reads them.  A scale is a power of two, one per page
+ * and head, stored as fp32: value = e4m3(code) * scale.  A slot is a token's
+ * place in the pool, page * B + offset.  Bytes of a page behind its last
+ * token, and pages that no request holds, may hold anything, NaN included.
+ * ---------------------------------------------------------------------- */
+
+/* most requests of one step */
+#define BFP8_KV_MAX_REQUESTS 4096
+/* tokens per tile of tile_offsets */
+#define BFP8_KV_TILE 128
+
+/* Block tables and slot maps of one step, from its request lengths.
+ * Request r has ctx_lens[r] tokens in its pages and brings new_lens[r] more
+ * (0 for an idle slot).  Its row of block_table names its pages in order.
+ * Pages it lacks are taken from free_pages, in request order, and entered in
+ * its row.
+ *   ctx_lens, new_lens : DEVICE int32 [R]
+ *   free_pages   : DEVICE int32 [n_free] pages that may be taken
+ *   free_head    : DEVICE int32 [1], how many of free_pages are taken already
+ *                  (e.g. counts + 1 of the step before); NULL means 0
+ *   block_table  : DEVICE int32 [R, table_width], entries of the newly taken
+ *                  pages are written, no other
+ *   q_offsets    : DEVICE int32 [R+1] output: first new token of each request
+ *                  in the step's token order (prefix sums of new_lens)
+ *   kv_lens      : DEVICE int32 [R] output: ctx + new, 0 for an idle or
+ *                  refused request
+ *   tile_offsets : DEVICE int32 [R+1] output: prefix sums of ceil(kv_lens/128)
+ *   slot_map     : DEVICE int32 [T] output: slot of each new token, -1 for a
+ *                  refused request's and for the tokens past q_offsets[R]
+ *   positions    : DEVICE int32 [T] output: the token's position in its
+ *                  request, -1 where slot_map is
+ *   counts       : DEVICE int32 [4] output: tokens (q_offsets[R]), the new
+ *                  free_head, requests not refused, pages wanted
+ * T is the step's token capacity, at least the sum of new_lens (more for a
+ * padded, captured step).  A request is refused when a length is negative,
+ * when its pages would pass table_width, its tokens T, or the pages wanted up
+ * to and including it exceed those left; one that wants no page is never
+ * refused for lack of pages.  A refused request takes no page, its kv_len is
+ * 0, its tokens keep their place in the token order (up to T).
+ * Every output array is distinct from the inputs.  Deterministic.
+ * Errors: BFP8_ERR_SHAPE if R < 0, T < 0, n_free < 0, table_width < 0,
+ * T >= 2^31, n_free >= 2^31 or table_width * page_size >= 2^31;
+ * BFP8_ERR_GROUPS if R > BFP8_KV_MAX_REQUESTS; BFP8_ERR_ARG if page_size is
+ * not 32, 64 or 128; BFP8_ERR_NULL; BFP8_ERR_ALIGN (4 bytes).  R == 0 still
+ * writes offsets, counts and the token arrays. */
+int bfp8_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int64_t R,
+                 const int32_t* free_pages, int64_t n_free, const int32_t* free_head,
+                 int32_t* block_table, int64_t table_width, int32_t page_size, int32_t* q_offsets,
+                 int32_t* kv_lens, int32_t* tile_offsets, int32_t* slot_map, int32_t* positions,
+                 int64_t T, int32_t* counts, void* stream);
+
+/* Quantizes the step's keys and values into their slots.  For each page and
+ * head that the map touches, with x the new tokens' elements there:
+ *     s = 2^ceil(log2( max(amax |x|, 1e-4f) / 448 ))     (as bfp8_act_quant_ue8m0)
+ *     if the page held tokens before the first new one: s = max(s, old scale)
+ *     code = e4m3_rne_saturating(x / s)
+ * and where s grew, the older tokens' codes become e4m3_rne(value * old / s):
+ * exact unless the value falls below the format's normal range.
+ * A page's tokens in front of its first new slot count as older tokens; a page
+ * written from its offset 0 on starts afresh.  Bytes behind the last new token
+ * are not touched.
+ * A key element that is not finite is stored as NaN (0x7F) and left out of the
+ * maximum.  Values are stored finite: a value element that is not finite is
+ * stored as 0 and its token's key as NaN throughout, so that every query that
+ * sees the token gets NaN and no other query does.
+ *   k_bf16   : bf16, element (t, h, d) at t * k_token_stride + h * k_head_stride + d
+ *   v_bf16   : bf16, likewise (strides in elements, at least 0)
+ *   slot_map : DEVICE int32 [T]; a slot outside [0, num_pages * page_size) is
+ *              skipped.  The new slots of one page follow each other in the map
+ *              (with fewer than 64 skipped ones between two of them) and ascend
+ *              by one, as bfp8_kv_plan writes them; where they do not, that
+ *              page's contents are unspecified.
+ *   k_cache, v_cache : 16-byte aligned; k_scales, v_scales : 4-byte aligned
+ * 16-byte loads are used where a pointer is 16-byte aligned and its strides
+ * are multiples of 8, 2-byte loads otherwise.
+ * Errors: BFP8_ERR_SHAPE if T < 0, T >= 2^31, num_pages < 0, heads < 1, heads > 65535, a
+ * stride is negative, num_pages * page_size >= 2^31, or (Dk, Dv) is none of
+ * (64, 64), (128, 128), (192, 128); BFP8_ERR_ARG if page_size is not 32, 64 or
+ * 128; BFP8_ERR_NULL; BFP8_ERR_ALIGN. */
+int bfp8_kv_append(const void* k_bf16, int64_t k_token_stride, int64_t k_head_stride,
+                   const void* v_bf16, int64_t v_token_stride, int64_t v_head_stride,
+                   const int32_t* slot_map, int64_t T, void* k_cache, float* k_scales,
+                   void* v_cache, float* v_scales, int64_t num_pages, int32_t page_size,
+                   int32_t heads, int32_t dk, int32_t dv, void* stream);
+
+/* Attention of each request's new tokens over its pages.  Query i of request r
+ * (n = q_offsets[r+1] - q_offsets[r] of them) stands at position
+ * kv_lens[r] - n + i and sees the tokens up to and including it; query head j
+ * reads KV head j / (heads_q / heads_kv):
+ *     out = bf16_rne( sum_t p_t v_t / sum_t p_t ),  p_t = exp(scale * q . k_t - max)
+ *     lse = log sum_t exp(scale * q . k_t)                       (natural log)
+ * A row that sees nothing (kv_len 0, or a position below 0) gets zeros, and
+ * -infinity.  Codes are widened exactly to bf16 for the matrix cores; p enters
+ * them as two bf16 terms (sixteen significant bits), logits, sums and
+ * statistics are fp32.
+ *   q_bf16   : bf16, element (t, j, d) at t * q_token_stride + j * q_head_stride
+ *              + d (strides in elements), rows 0 .. T-1
+ *   block_table : DEVICE int32 [R, table_width]; entries up to kv_len are read,
+ *              clamped into the pool
+ *   q_offsets, tile_offsets : DEVICE int32 [R+1], kv_lens : DEVICE int32 [R],
+ *              as bfp8_kv_plan writes them (any values stay inside the buffers)
+ *   max_new  : host upper bound of the requests' new tokens; rows of a request
+ *              past it are not written
+ *   out_bf16 : bf16 [T, heads_q, Dv], 16-byte aligned; rows of no request are
+ *              not written
+ *   lse      : fp32 [T, heads_q], or NULL
+ *   workspace: DEVICE, at least bfp8_attn_paged_workspace_size(...) bytes,
+ *              16-byte aligned, any contents: partial results of token ranges;
+ *              NULL lets every row's tokens be walked in one piece
+ * Values stored in a visible page are finite codes, as bfp8_kv_append writes
+ * them.  Deterministic.
+ * Errors: BFP8_ERR_SHAPE if a size is negative, T >= 2^31, max_new < 1 (with R, T > 0),
+ * heads_kv < 1, heads_q is no positive multiple of heads_kv, heads_q > 65535,
+ * max_new * heads_q >= 2^31, num_pages or table_width times page_size >= 2^31,
+ * or the head widths are none of bfp8_kv_append's; BFP8_ERR_GROUPS if R >
+ * BFP8_KV_MAX_REQUESTS; BFP8_ERR_ARG for a page_size as above or a scale that
+ * is not finite; BFP8_ERR_NULL; BFP8_ERR_ALIGN; BFP8_ERR_WORKSPACE. */
+int bfp8_attn_paged(const void* q_bf16, int64_t q_token_stride, int64_t q_head_stride,
+                    const void* k_cache, const float* k_scales, const void* v_cache,
+                    const float* v_scales, int64_t num_pages, int32_t page_size,
+                    const int32_t* block_table, int64_t table_width, const int32_t* q_offsets,
+                    const int32_t* kv_lens, const int32_t* tile_offsets, int64_t R, int64_t T,
+                    int64_t max_new, int32_t heads_q, int32_t heads_kv, int32_t dk, int32_t dv,
+                    float scale, void* out_bf16, float* lse, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace bfp8_attn_paged uses for these sizes (a multiple of 16; 0
+ * for sizes it would refuse or that it never splits).  Pure host function (planned for the
+ * 256 CUs of MI355X). */
+size_t bfp8_attn_paged_workspace_size(int64_t R, int64_t max_new, int32_t heads_q,
+                                      int32_t heads_kv, int32_t dk, int32_t dv);
+
 /* Test helper: encodes the 2^32 float32 bit patterns first .. first+count-1
  * to e4m3 codes with the same device routine act_quant uses (variant 0), or
  * with the alternative routine (variant 1), into out[count] (device).
