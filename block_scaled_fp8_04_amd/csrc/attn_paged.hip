@@ -28,6 +28,7 @@ namespace bfp8 {
 constexpr int kAttnThreads = 256;
 constexpr int kAttnWaves = kAttnThreads / 64;
 constexpr int kCols = 16;                     // query columns of a wave
+constexpr int kSplitMaxCols = 64;             // most query columns of a split item
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -54,132 +55,303 @@ __device__ __forceinline__ void split8(const float (&p)[8], bf8v& hi, bf8v& lo) 
     }
 }
 
-// 32 elements of a bf16 query row (negated for a negative scale); p == nullptr: zeros.
-__device__ __forceinline__ void load_q32(const uint16_t* p, bool vec, bool negate, bf8v (&q)[4]) {
+// Eight elements of a bf16 query row (negated for a negative scale).
+__device__ __forceinline__ bf8v load_q8(const uint16_t* p, bool vec, bool negate) {
+    uint4 x;
+    if (vec) {
+        x = *(const uint4*)p;
+    } else {
+        uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (p != nullptr) {
-            if (vec) {
-                x = ((const uint4*)p)[i];
-            } else {
-                uint32_t w[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[j] = (uint32_t)p[8 * i + 2 * j] | ((uint32_t)p[8 * i + 2 * j + 1] << 16);
-                x = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            const uint32_t f = negate ? 0x80008000u : 0u;
-            x = make_uint4(x.x ^ f, x.y ^ f, x.z ^ f, x.w ^ f);
-        }
-        q[i] = __builtin_bit_cast(bf8v, x);
+        for (int j = 0; j < 4; ++j) w[j] = (uint32_t)p[2 * j] | ((uint32_t)p[2 * j + 1] << 16);
+        x = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    const uint32_t f = negate ? 0x80008000u : 0u;
+    return __builtin_bit_cast(bf8v, make_uint4(x.x ^ f, x.y ^ f, x.z ^ f, x.w ^ f));
 }
 
-// One wave's attention of kCols query columns over 128-token tiles
-// tile0, tile0 + step, ... < tile1 of one request and KV head.
-template <int DK, int DV>
+// Reads through the scalar cache (uniform addresses): page numbers and scales.
+typedef const __attribute__((address_space(4))) int32_t* scalar_i32;
+typedef const __attribute__((address_space(4))) float* scalar_f32;
+
+// A value that is the same in all lanes, in scalar registers (where the compiler cannot see it).
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+    return (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)x) |
+           (int64_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32;
+}
+
+// What an item's columns are: shared by the three kernels.  kUniform: r is the same for the wave,
+// and so is then all of this, in scalar registers.
+struct Item {
+    int64_t q0;
+    int n, cols, kv_len, G;
+    template <bool kUniform>
+    static __device__ __forceinline__ int32_t at(const int32_t* p, int i) {
+        return kUniform ? ((scalar_i32)(uintptr_t)p)[i] : p[i];
+    }
+    template <bool kUniform>
+    static __device__ __forceinline__ Item of(const AttnArgs& a, int r) {
+        Item it;
+        it.G = a.heads_q / a.heads_kv;
+        it.q0 = min(max((int64_t)at<kUniform>(a.q_offsets, r), (int64_t)0), a.T);
+        const int64_t q1 = min(max((int64_t)at<kUniform>(a.q_offsets, r + 1), it.q0), a.T);
+        it.n = (int)(q1 - it.q0);
+        it.cols = (int)min((int64_t)it.n, a.max_new) * it.G;
+        it.kv_len = (int)min(max((int64_t)at<kUniform>(a.kv_lens, r), (int64_t)0), a.width << a.log_b);
+        return it;
+    }
+    // tokens that column c sees
+    __device__ __forceinline__ int limit(int c) const {
+        return min(kv_len, max(kv_len - n + c / G + 1, 0));
+    }
+    __device__ __forceinline__ const uint16_t* row(const AttnArgs& a, int h, int c) const {
+        return a.q + (q0 + c / G) * a.q_ts + (int64_t)(h * G + c % G) * a.q_hs;
+    }
+};
+
+__device__ __forceinline__ bool q_vec(const AttnArgs& a) {
+    return ((uintptr_t)a.q % 16) == 0 && ((a.q_ts | a.q_hs) % 8) == 0;
+}
+__device__ __forceinline__ float exp2_scale(const AttnArgs& a) {
+    return fmaxf(__builtin_fabsf(a.scale) * kLog2e, 0x1p-126f);     // -inf times 0 is NaN
+}
+
+// A run of tiles of one item that a workgroup walks; its waves take every fourth one.
+struct Segment {
+    int r, h, ct;
+    int t0, t1;                                      // tiles of TT tokens
+    int whole;                                       // the item's only run
+};
+
+// One wave's attention of kCols query columns over TT-token tiles, page size B.
+//
+// Each wave brings its own tiles to LDS, by loads that bypass the registers, and reads them
+// back as fragments; nothing is shared between waves, so there is no barrier in the loop.  A
+// fragment's lanes take sixteen different rows, and read straight from memory that way every
+// 16 bytes are an access of their own: 3.8 instead of 5.2 TB/s (64 requests, 180k tokens, 8
+// heads of 128).  The next tile's keys are requested when this tile's have been multiplied,
+// its values when this tile's have: one of the two is always on its way while the wave
+// computes, and the keys also while the waves of a finished item are joined.  The loads are
+// non-temporal (without the hint 4.8 TB/s).
+//
+// Lane group g = lane / 16 holds tokens TT / 4 * g .. of a tile.  In LDS a row's 16-byte
+// chunks are permuted (by exclusive or with k_swz, v_swz of the row), so that the sixteen
+// rows that lanes read together lie in different banks.
+template <int DK, int DV, int B, int TT>
 struct AttnWave {
-    static constexpr int KS = (DK + 127) / 128;      // 128-wide steps of the first product
+    static constexpr int LT = TT / 4;                // tokens per lane group
+    static constexpr int KT = TT / 16;               // 16-row tiles of S^T
+    static constexpr int PM = TT / 32;               // matrix instructions per 16 rows of O^T
+    static constexpr int KF = DK / 32;               // matrix instructions per 16 keys
     static constexpr int DT = DV / 16;               // 16-row tiles of O^T
-    bf8v q[KS][4];                                   // lane group g: dims 128 s + 32 g ..
+    static constexpr int NP = TT > B ? TT / B : 1;   // pages of a tile
+    static constexpr int VB = TT > B ? B : TT;       // bytes of a value row in one page
+    static constexpr int K_BYTES = TT * DK, V_BYTES = TT * DV;
+    static constexpr int NK = K_BYTES / 1024, NV = V_BYTES / 1024;      // loads per tile
+    static_assert(kCols * DV * 4 <= V_BYTES, "results fit the wave's values");
+
+    bf8v q[KF];                                      // lane group g: dims DK / 4 * g + 8 i ..
     v4f o[DT];
     float m, l;                                      // l: this lane's tokens only
+    int entry[NP];                                   // table entries of the tile after the next
+    int64_t page[NP];                                // page * heads + head of the tile loaded last
+    float ks[NP], vs[NP];                            // and its scales
+
+    // bits 4 .. of a chunk's place that depend on the row
+    static __device__ __forceinline__ int k_swz(int token) {
+        const int x = token / LT & 3;
+        return DK == 128 ? ((token >> 1 & 1) | x << 1) << 4 : x << 4;
+    }
+    static __device__ __forceinline__ int v_swz(int d) {
+        return (VB == 128 ? d >> 1 & 7 : VB == 64 ? d >> 2 & 3 : d >> 3 & 1) << 4;
+    }
 
     // column `lane & 15` is this query row (NULL: an unused column)
     __device__ __forceinline__ void load_q(const uint16_t* row, bool vec, bool negate, int g) {
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
-            load_q32(row != nullptr && 128 * s + 32 * g < DK ? row + 128 * s + 32 * g : nullptr, vec,
-                     negate, q[s]);
+        for (int i = 0; i < KF; ++i)
+            q[i] = row ? load_q8(row + DK / 4 * g + 8 * i, vec, negate) : bf8v{0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[d] = v4f{0.f, 0.f, 0.f, 0.f};
         m = neg_inf();
         l = 0.f;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) entry[p] = 0;
     }
 
-    __device__ __forceinline__ void walk(const AttnArgs& a, int r, int h, int tile0, int tile1,
-                                         int step, int kv_len, int limit, int free_limit, float c) {
-        // limit: this column sees tokens below it; free_limit: every column sees those below
-        if (tile0 >= tile1) return;
-        const int lane = threadIdx.x & 63, g = lane >> 4, lr = lane & 15;
-        const int log_b = a.log_b, B = 1 << log_b;
-        const int last = (kv_len - 1) >> log_b;                 // last page that is read
-        const int32_t* const table = a.block_table + (int64_t)r * a.width;
-        // this lane's K rows are tokens ktok + 4 t, its P^T and V^T elements tokens 32 g + j
-        const int ktok = 32 * (lr >> 2) + (lr & 3);
-        const auto page_of = [&](int token) {
-            const int j = min(token >> log_b, last);
-            return min(max((int64_t)table[j], (int64_t)0), a.pages - 1) * a.heads_kv + h;
-        };
-        for (int tile = tile0; tile < tile1; tile += step) {
-            const int base = tile * kKvTile;
-            const int64_t kp = page_of(base + ktok), vp = page_of(base + 32 * g);
-            const float ke = a.k_scales[kp], ve = a.v_scales[vp];
-            const uint8_t* const kb = a.k_cache + kp * ((int64_t)B * DK) +
-                                      ((base + ktok) & (B - 1)) * DK + 32 * g;
-            const uint8_t* const vb = a.v_cache + vp * ((int64_t)B * DV) + lr * B + (32 * g & (B - 1));
-            v4f s[8];
+    __device__ __forceinline__ void read_table(const AttnArgs& a, int r, int tile, int kv_len) {
+        const scalar_i32 table = (scalar_i32)(uintptr_t)(a.block_table + r * a.width);
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                s[t] = v4f{0.f, 0.f, 0.f, 0.f};
+        for (int p = 0; p < NP; ++p)
+            entry[p] = table[max(min((tile * TT + p * B) / B, (kv_len - 1) / B), 0)];
+    }
+    __device__ __forceinline__ void find_pages(const AttnArgs& a, int h) {
+        const scalar_f32 k_scales = (scalar_f32)(uintptr_t)a.k_scales;
+        const scalar_f32 v_scales = (scalar_f32)(uintptr_t)a.v_scales;
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    v8i kf = {0, 0, 0, 0, 0, 0, 0, 0};
-                    if (128 * ks + 128 <= DK || 128 * ks + 32 * g < DK) {
-                        const uint4* p = (const uint4*)(kb + 4 * t * DK + 128 * ks);
-                        kf = frag_from(p[0], p[1]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        s[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            widen8(kf[2 * i], kf[2 * i + 1], ke), q[ks][i], s[t], 0, 0, 0);
-                }
-            }
-            v8i vf[DT];
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                const uint4* p = (const uint4*)(vb + 16 * d * B);
-                vf[d] = frag_from(p[0], p[1]);
-            }
-            if (base + kKvTile > free_limit) {
-                const int seen = limit - base - 32 * g;         // this lane's tokens: the first `seen`
-#pragma unroll
-                for (int t = 0; t < 8; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (4 * t + i >= seen) s[t][i] = neg_inf();
-                // bytes behind the last token may hold anything: 0 * NaN is NaN
-                if (base + kKvTile > kv_len) {
-                    const int live = kv_len - base - 32 * g;
-#pragma unroll
-                    for (int w = 0; w < 8; ++w) {
-                        const int nb = min(max(live - 4 * w, 0), 4);
-                        const int mask = nb == 4 ? -1 : (1 << (8 * nb)) - 1;
-#pragma unroll
-                        for (int d = 0; d < DT; ++d) vf[d][w] &= mask;
-                    }
-                }
-            }
-            bf8v ph[4], pl[4];
-            softmax(s, c, ph, pl);
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bf8v x = widen8(vf[d][2 * i], vf[d][2 * i + 1], ve);
-                    o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, ph[i], o[d], 0, 0, 0);
-                    o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, pl[i], o[d], 0, 0, 0);
-                }
+        for (int p = 0; p < NP; ++p) {
+            page[p] = min(max((int64_t)entry[p], (int64_t)0), a.pages - 1) * a.heads_kv + h;
+            ks[p] = k_scales[page[p]];
+            vs[p] = v_scales[page[p]];
         }
+    }
+    // real: otherwise the loads are out of their resource's range and read nothing
+    __device__ __forceinline__ void load_k(const AttnArgs& a, uint8_t* lds_k, int tile, bool real) {
+        const int lane = threadIdx.x & 63;
+        const int row = lane / (DK / 16), at = lane % (DK / 16);
+        const int in_page = TT < B ? tile * TT & (B - 1) : 0;
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+            const int p = i * 1024 / DK / B;                    // all of a load's rows are in one page
+            const __amdgpu_buffer_rsrc_t src =
+                make_rsrc(a.k_cache + uniform(page[p]) * ((int64_t)B * DK), real ? (uint64_t)B * DK : 0);
+            int voff;
+            if constexpr (DK == 192) {
+                const int x = i % 3 * 64 + lane;                // 16 rows are three loads
+                voff = ((x / 12) * 192 + x % 12 * 16) ^ (i / 3 * 16 / LT & 3) << 4;
+            } else {
+                voff = (row * DK + at * 16) ^ k_swz(i * (1024 / DK) + row);
+            }
+            const int from = (DK == 192 ? i / 3 * 3072 : i * 1024) - p * B * DK + in_page * DK;
+            buf_lds16_nt(src, voff, from, lds_k + i * 1024);
+        }
+    }
+    __device__ __forceinline__ void load_v(const AttnArgs& a, uint8_t* lds_v, int tile) {
+        constexpr int PER = DV * VB / 1024, RI = 1024 / VB;     // loads per page, rows per load
+        const int lane = threadIdx.x & 63;
+        const int row = lane / (VB / 16), at = lane % (VB / 16);
+        const int in_page = TT < B ? tile * TT & (B - 1) : 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int p = i / PER;
+            const __amdgpu_buffer_rsrc_t src =
+                make_rsrc(a.v_cache + uniform(page[p]) * ((int64_t)B * DV), (uint64_t)B * DV);
+            const int voff = row * B + (at * 16 ^ v_swz(i * RI + row));
+            buf_lds16_nt(src, voff, i % PER * RI * B + in_page, lds_v + i * 1024);
+        }
+    }
+    static __device__ __forceinline__ float pick(const float (&x)[NP], int token) {
+        float y = x[0];                                         // the scale of a lane's tokens
+#pragma unroll
+        for (int p = 1; p < NP; ++p)
+            if (token / B == p) y = x[p];
+        return y;
+    }
+
+    // This wave's tiles of segment s.  lds_k, lds_v: its LDS bytes, of two arrays (so that reads of
+    // the one are seen not to wait for loads into the other).  limit: this column sees tokens
+    // below it; free_limit: every column sees those below.  next (NULL: none) is the segment
+    // after this one, in which the wave's first tile is n0 < next->t1: its keys are requested here.
+    // ready: the first tile's keys were requested by the walk before.  Everything but limit is
+    // uniform.
+    __device__ __forceinline__ void walk(const AttnArgs& a, uint8_t* lds_k, uint8_t* lds_v,
+                                         const Segment& s, int t0, int kv_len, int limit,
+                                         int free_limit, float c, bool ready, bool has_next,
+                                         const Segment& next, int n0, int n_kv_len) {
+        const int lane = threadIdx.x & 63, g = lane >> 4, lr = lane & 15;
+        const int t1 = __builtin_amdgcn_readfirstlane(s.t1);
+        t0 = __builtin_amdgcn_readfirstlane(t0);
+        n0 = __builtin_amdgcn_readfirstlane(n0);
+        // fragments: this lane's K rows are tokens ktok + 4 t, its V rows lr + 16 d
+        const int ktok = LT * (lr >> 2) + (lr & 3);
+        const uint8_t* kf[DK / 64];
+#pragma unroll
+        for (int x = 0; x < DK / 64; ++x)
+            kf[x] = lds_k + ktok * DK + ((DK / 64 * g + x) * 16 ^ k_swz(ktok));
+        const uint8_t* vf[LT / 16];
+#pragma unroll
+        for (int y = 0; y < LT / 16; ++y) {
+            const int tok = LT * g + 16 * y;
+            vf[y] = lds_v + tok / VB * (DV * VB) + lr * VB + (tok % VB ^ v_swz(lr));
+        }
+        if (!ready) {
+            read_table(a, s.r, t0, kv_len);
+            find_pages(a, s.h);
+            load_k(a, lds_k, t0, true);
+        }
+        load_v(a, lds_v, t0);
+        const auto read_after = [&](int tile) {                 // the entry of the tile after `tile`
+            if (tile + kAttnWaves < t1) read_table(a, s.r, tile + kAttnWaves, kv_len);
+            else if (has_next) read_table(a, next.r, n0, n_kv_len);
+        };
+        read_after(t0);
+        // one tile; kMore: this wave has another one in the segment
+        const auto tile_step = [&](auto more, int tile) {
+            constexpr bool kMore = decltype(more)::value != 0;
+            const int base = tile * TT;
+            wait_vmcnt<NV>();                                   // this tile's keys have landed
+            __builtin_amdgcn_sched_barrier(0);
+            const float ke = pick(ks, LT * (lr >> 2)), ve = pick(vs, LT * g);
+            v4f x[KT];
+#pragma unroll
+            for (int t = 0; t < KT; ++t) x[t] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < DK / 64; ++i) {
+#pragma unroll
+                for (int t = 0; t < KT; ++t) {
+                    const uint4 w = *(const uint4*)(kf[i] + 4 * t * DK);
+                    x[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8((int)w.x, (int)w.y, ke), q[2 * i],
+                                                                   x[t], 0, 0, 0);
+                    x[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8((int)w.z, (int)w.w, ke),
+                                                                   q[2 * i + 1], x[t], 0, 0, 0);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            // the next tile's keys; with none left, loads that read nothing: a branch around them
+            // would make the waits below cover the shorter path, which is too much
+            find_pages(a, kMore ? s.h : next.h);
+            load_k(a, lds_k, kMore ? tile + kAttnWaves : n0, kMore || has_next);
+            if constexpr (kMore) read_after(tile + kAttnWaves);
+            __builtin_amdgcn_sched_barrier(0);
+            uint32_t mask[LT / 4];
+#pragma unroll
+            for (int w = 0; w < LT / 4; ++w) mask[w] = 0xFFFFFFFFu;
+            if (base + TT > free_limit) {
+                const int seen = limit - base - LT * g;         // this lane's tokens: the first `seen`
+#pragma unroll
+                for (int t = 0; t < KT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (4 * t + i >= seen) x[t][i] = neg_inf();
+                // bytes behind the last token may hold anything: 0 * NaN is NaN
+                const int live = kv_len - base - LT * g;
+#pragma unroll
+                for (int w = 0; w < LT / 4; ++w) {
+                    const int n = min(max(live - 4 * w, 0), 4);
+                    mask[w] = n == 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1;
+                }
+            }
+            bf8v ph[PM], pl[PM];
+            softmax(x, c, ph, pl);
+            wait_vmcnt<NK>();                                   // this tile's values have landed
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int y = 0; y < LT / 16; ++y)
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    const uint4 w = *(const uint4*)(vf[y] + 16 * d * VB);
+                    const bf8v x0 = widen8((int)(w.x & mask[4 * y]), (int)(w.y & mask[4 * y + 1]), ve);
+                    o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x0, ph[2 * y], o[d], 0, 0, 0);
+                    o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x0, pl[2 * y], o[d], 0, 0, 0);
+                    const bf8v x1 = widen8((int)(w.z & mask[4 * y + 2]), (int)(w.w & mask[4 * y + 3]), ve);
+                    o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x1, ph[2 * y + 1], o[d], 0, 0, 0);
+                    o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x1, pl[2 * y + 1], o[d], 0, 0, 0);
+                }
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (kMore) load_v(a, lds_v, tile + kAttnWaves);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        int tile = t0;
+        for (; tile + kAttnWaves < t1; tile += kAttnWaves) tile_step(StageId<1>{}, tile);
+        tile_step(StageId<0>{}, tile);
     }
 
     // S^T of one tile to P^T, with this lane's tokens 8 i .. 8 i + 7 in ph[i] (rounded) and pl[i]
     // (the remainder); rescales o and l to the new running maximum.
-    __device__ __forceinline__ void softmax(v4f (&s)[8], float c, bf8v (&ph)[4], bf8v (&pl)[4]) {
+    __device__ __forceinline__ void softmax(v4f (&s)[KT], float c, bf8v (&ph)[PM], bf8v (&pl)[PM]) {
         float mx = s[0][0];
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
+        for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[t][i]);
         mx = fmaxf(mx, __shfl_xor(mx, 16));
@@ -189,13 +361,13 @@ struct AttnWave {
         // that the largest keeps p = 1
         if (__any(__builtin_fabsf(m_new) > 4194304.f && m_new != neg_inf())) {
 #pragma unroll
-            for (int t = 0; t < 8; ++t) s[t] *= c;
+            for (int t = 0; t < KT; ++t) s[t] *= c;
             c = 1.f;
         }
         const float sub = m_new == neg_inf() ? 0.f : -m_new;    // nothing seen yet: every p is 0
         float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < PM; ++i) {
             float p[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -215,46 +387,63 @@ struct AttnWave {
     }
 };
 
-// Joins the four waves' results of one 16-column item in LDS.  Every wave ends up knowing
-// the column's (m, l); lane (column, dims) results are left in `part` as
-// sum over waves of O 2^(m_w - m), [kCols][DV] fp32 spread over the threads: thread x owns
-// column x / 16, dims 4 (x % 16) + 64 j.
-template <int DK, int DV>
-__device__ __forceinline__ void join_waves(AttnWave<DK, DV>& w, float* lds_o, float* lds_ml,
-                                           float (&part)[DV / 16], float& m, float& l) {
-    constexpr int ROW = DV + 4;
+// Joins the four waves' results of one 16-column item in their bytes of lds_v (the keys' bytes
+// may be receiving the next item's): first m and l, then each wave's O times 2^(m_w - m), its
+// four-dim groups permuted by the column against bank conflicts.  Thread x gets column x / 16,
+// dims 4 (x % 16) + 64 j of the sum, in wave order, and that column's m and l.
+// Barrier behind finished LDS accesses, leaving the loads that are on their way alone.
+__device__ __forceinline__ void barrier_ds() {
+    __builtin_amdgcn_s_waitcnt(0xC07F);                         // lgkmcnt(0)
+    barrier_lds();
+}
+
+template <class W, int DV>
+__device__ __forceinline__ void join_waves(const W& w, uint8_t* lds_v, float (&part)[DV / 16], float& m,
+                                           float& l) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, col = lane & 15;
     float ll = w.l + __shfl_xor(w.l, 16);
     ll += __shfl_xor(ll, 32);
-    __syncthreads();                                            // the last item's reads
+    float* const mine = (float*)(lds_v + wave * W::V_BYTES);
     if (g == 0) {
-        lds_ml[wave * kCols + col] = w.m;
-        lds_ml[(kAttnWaves + wave) * kCols + col] = ll;
+        mine[col] = w.m;
+        mine[kCols + col] = ll;
     }
-#pragma unroll
-    for (int d = 0; d < DV / 16; ++d)
-        *(v4f*)(lds_o + (wave * kCols + col) * ROW + 16 * d + 4 * g) = w.o[d];
-    __syncthreads();
-    const int oc = tid >> 4, od = (tid & 15) * 4;
+    barrier_ds();
+    const int oc = tid >> 4;
+    float mw[kAttnWaves], m_col = neg_inf();
     m = neg_inf();
 #pragma unroll
-    for (int x = 0; x < kAttnWaves; ++x) m = fmaxf(m, lds_ml[x * kCols + oc]);
+    for (int x = 0; x < kAttnWaves; ++x) {
+        const float* const theirs = (const float*)(lds_v + x * W::V_BYTES);
+        mw[x] = theirs[oc];
+        m = fmaxf(m, mw[x]);
+        m_col = fmaxf(m_col, theirs[col]);
+    }
     l = 0.f;
+#pragma unroll
+    for (int x = 0; x < kAttnWaves; ++x) {
+        const float lw = ((const float*)(lds_v + x * W::V_BYTES))[kCols + oc];
+        if (mw[x] != neg_inf() || lw != 0.f) l = __builtin_fmaf(lw, __builtin_amdgcn_exp2f(mw[x] - m), l);
+    }
+    barrier_ds();
+    // a wave that saw nothing in the column has zeros there
+    const float f = w.m == neg_inf() ? 1.f : __builtin_amdgcn_exp2f(w.m - m_col);
+#pragma unroll
+    for (int d = 0; d < DV / 16; ++d) *(v4f*)(mine + col * DV + ((4 * d + g) ^ col) * 4) = w.o[d] * f;
+    barrier_ds();
 #pragma unroll
     for (int j = 0; j < DV / 16; ++j) part[j] = 0.f;
 #pragma unroll
     for (int x = 0; x < kAttnWaves; ++x) {
-        const float mw = lds_ml[x * kCols + oc];
-        if (mw == neg_inf() && lds_ml[(kAttnWaves + x) * kCols + oc] == 0.f) continue;
-        const float f = __builtin_amdgcn_exp2f(mw - m);
-        l = __builtin_fmaf(lds_ml[(kAttnWaves + x) * kCols + oc], f, l);
+        const float* const theirs = (const float*)(lds_v + x * W::V_BYTES);
 #pragma unroll
         for (int j = 0; j < DV / 64; ++j) {
-            const v4f v = *(const v4f*)(lds_o + (x * kCols + oc) * ROW + od + 64 * j);
+            const v4f v = *(const v4f*)(theirs + oc * DV + (((tid & 15) + 16 * j) ^ oc) * 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) part[4 * j + i] = __builtin_fmaf(v[i], f, part[4 * j + i]);
+            for (int i = 0; i < 4; ++i) part[4 * j + i] += v[i];
         }
     }
+    barrier_ds();                                            // before the next item's values
 }
 
 template <int DV>
@@ -272,49 +461,291 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, int64_t row, int he
         a.lse[row * a.heads_q + head] = l == 0.f ? neg_inf() : (m + __builtin_log2f(l)) * kLn2;
 }
 
+// Few query columns (a decode step, drafts): the 128-token tiles of all items, an item being
+// (request, KV head, 16 columns), form one row of units that the workgroups divide evenly, so
+// that ragged lengths and few long caches load the chip alike.  A workgroup walks its units
+// item by item; an item that lies within one workgroup is finished there, the others leave
+// partial sums (at most two of them per workgroup: its first and its last item) that
+// attn_join_kernel adds in token order.
+constexpr int kSplitMinUnits = kAttnWaves;    // tiles per workgroup, at least one for each wave
+
+struct SplitPlan {
+    int64_t units;      // tiles of all items
+    int64_t per;        // tiles per workgroup
+};
+
+__device__ __forceinline__ SplitPlan split_plan(const AttnArgs& a, int col_tiles, int groups) {
+    const int64_t units = (int64_t)max(a.tile_offsets[a.R], 0) * a.heads_kv * col_tiles;
+    return {units, max((units + groups - 1) / groups, (int64_t)kSplitMinUnits)};
+}
+
 // One workgroup per (request, KV head, 16 query columns): its waves take every fourth tile.
-template <int DK, int DV>
-__global__ __launch_bounds__(kAttnThreads, 1) void attn_item_kernel(AttnArgs a, int col_tiles) {
-    __shared__ float lds_o[kAttnWaves * kCols * (DV + 4)];
-    __shared__ float lds_ml[2 * kAttnWaves * kCols];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+template <int DK, int DV, int B, int TT>
+__global__ __launch_bounds__(kAttnThreads) void attn_item_kernel(AttnArgs a, int col_tiles) {
+    using W = AttnWave<DK, DV, B, TT>;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds_k[kAttnWaves * W::K_BYTES];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds_v[kAttnWaves * W::V_BYTES];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     int64_t item = blockIdx.x;
     const int ct = (int)(item % col_tiles);
     item /= col_tiles;
-    const int h = (int)(item % a.heads_kv), r = (int)(item / a.heads_kv);
-    const int G = a.heads_q / a.heads_kv;
-    const int64_t q0 = min(max((int64_t)a.q_offsets[r], (int64_t)0), a.T);
-    const int64_t q1 = min(max((int64_t)a.q_offsets[r + 1], q0), a.T);
-    const int n = (int)(q1 - q0);
-    const int cols = (int)min((int64_t)n, a.max_new) * G;
-    if (ct * kCols >= cols) return;
-    const int kv_len = (int)min(max((int64_t)a.kv_lens[r], (int64_t)0), a.width << a.log_b);
-
-    const auto col_limit = [&](int c) { return min(kv_len, max(kv_len - n + c / G + 1, 0)); };
-    const int col = ct * kCols + (lane & 15), g = lane >> 4;
-    const bool used = col < cols;
-    const bool vec = ((uintptr_t)a.q % 16) == 0 && ((a.q_ts | a.q_hs) % 8) == 0;
-    AttnWave<DK, DV> w;
-    w.load_q(used ? a.q + (q0 + col / G) * a.q_ts + (int64_t)(h * G + col % G) * a.q_hs : nullptr, vec,
-             a.scale < 0.f, g);
-    const int last_col = min(ct * kCols + kCols, cols) - 1;
-    const int tiles = (col_limit(last_col) + kKvTile - 1) / kKvTile;
-    w.walk(a, r, h, wave, tiles, kAttnWaves, kv_len, used ? col_limit(col) : 0, col_limit(ct * kCols),
-           fmaxf(__builtin_fabsf(a.scale) * kLog2e, 0x1p-126f));     // -inf times 0 is NaN
+    const int h = (int)(item % a.heads_kv);
+    const Item it = Item::of<true>(a, (int)(item / a.heads_kv));
+    if (ct * kCols >= it.cols) return;
+    const int col = ct * kCols + (lane & 15);
+    const bool used = col < it.cols;
+    W w;
+    w.load_q(used ? it.row(a, h, col) : nullptr, q_vec(a), a.scale < 0.f, lane >> 4);
+    Segment seg;
+    seg.r = (int)(item / a.heads_kv);
+    seg.h = h;
+    seg.ct = ct;
+    seg.t0 = 0;
+    seg.t1 = (it.limit(min(ct * kCols + kCols, it.cols) - 1) + TT - 1) / TT;
+    seg.whole = 1;
+    if (wave < seg.t1)
+        w.walk(a, lds_k + wave * W::K_BYTES, lds_v + wave * W::V_BYTES, seg, wave, it.kv_len,
+               used ? it.limit(col) : 0, it.limit(ct * kCols), exp2_scale(a), false, false, seg, 0, 0);
     float part[DV / 16], m, l;
-    join_waves<DK, DV>(w, lds_o, lds_ml, part, m, l);
+    join_waves<W, DV>(w, lds_v, part, m, l);
     const int oc = ct * kCols + (tid >> 4);
-    if (oc < cols) store_row<DV>(a, q0 + oc / G, h * G + oc % G, (tid & 15) * 4, part, m, l);
+    if (oc < it.cols)
+        store_row<DV>(a, it.q0 + oc / it.G, h * it.G + oc % it.G, (tid & 15) * 4, part, m, l);
+    wait_vmcnt<0>();                                            // no load outlives its LDS
 }
 
-size_t attn_paged_workspace_bytes(int64_t, int64_t, int32_t, int32_t, int32_t, int32_t) { return 0; }
+template <int DK, int DV, int B, int TT>
+__global__ __launch_bounds__(kAttnThreads) void attn_split_kernel(AttnArgs a, int col_tiles) {
+    using W = AttnWave<DK, DV, B, TT>;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds_k[kAttnWaves * W::K_BYTES];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds_v[kAttnWaves * W::V_BYTES];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const SplitPlan sp = split_plan(a, col_tiles, gridDim.x);
+    int64_t u = (int64_t)blockIdx.x * uniform(sp.per);
+    const int64_t end = min(u + uniform(sp.per), uniform(sp.units));
+    if (u >= end) return;
+    const int64_t items = (int64_t)a.heads_kv * col_tiles;   // of one request
+    // the request of the first unit: how many offsets lie at or below it, counted by 64 lanes on
+    // every 64th offset and then on the 64 behind the last of those
+    static_assert(kKvMaxRequests <= 64 * 64, "two steps");
+    const int64_t ut = uniform(u / items);
+    const int lo64 = __popcll(__ballot(lane * 64 < a.R && a.tile_offsets[min(lane * 64, a.R)] <= ut)) - 1;
+    const int at = max(lo64, 0) * 64 + lane;
+    const int lo = max(lo64, 0) * 64 +
+                   max(__popcll(__ballot(at < a.R && a.tile_offsets[min(at, a.R)] <= ut)) - 1, 0);
+    const scalar_i32 offs = (scalar_i32)(uintptr_t)a.tile_offsets;
+    int r = __builtin_amdgcn_readfirstlane(lo);
+    // the workgroup's next run of tiles, from unit u on
+    const auto advance = [&](Segment& s) {
+        for (; r < a.R && u < end; ++r) {
+            const int64_t f = offs[r];
+            const int nt = (int)min(max((int64_t)offs[r + 1] - f, (int64_t)0), (int64_t)1 << 24);
+            const int64_t local = max(u - f * items, (int64_t)0);
+            if (nt <= 0 || local >= (int64_t)nt * items) continue;
+            const int item = __builtin_amdgcn_readfirstlane((int)(local / nt));
+            const int tile0 = (int)(local - (int64_t)item * nt);
+            const int count = (int)min((int64_t)(nt - tile0), end - u);
+            u += count;
+            s.r = r;
+            s.h = __builtin_amdgcn_readfirstlane(item / col_tiles);
+            s.ct = item - s.h * col_tiles;
+            s.t0 = tile0 * (kKvTile / TT);
+            s.t1 = (tile0 + count) * (kKvTile / TT);
+            s.whole = count == nt;
+            return true;
+        }
+        return false;
+    };
+    bool first = true, ready = false;
+    int64_t page[W::NP] = {};                                  // of the keys that are on their way
+    float ks[W::NP] = {}, vs[W::NP] = {};
+    Segment cur, next;
+    bool valid = advance(cur);
+    Item it = Item::of<true>(a, valid ? cur.r : 0);
+    while (valid) {
+        next = cur;                                             // defined, and inside the pool, if there is none
+        const bool has = advance(next);
+        const Item nit = Item::of<true>(a, has ? next.r : 0);
+        W w;
+        const int col = cur.ct * kCols + (lane & 15);
+        const bool used = col < it.cols;
+        if (cur.ct * kCols < it.cols) {
+            cur.t1 = min(cur.t1, (it.kv_len + TT - 1) / TT);
+            const int n1 = next.ct * kCols < nit.cols ? min(next.t1, (nit.kv_len + TT - 1) / TT) : 0;
+            const bool chain = has && next.t0 + wave < n1;
+            w.load_q(used ? it.row(a, cur.h, col) : nullptr, q_vec(a), a.scale < 0.f, lane >> 4);
+            if (cur.t0 + wave < cur.t1) {
+#pragma unroll
+                for (int p = 0; p < W::NP; ++p) {
+                    w.page[p] = page[p];
+                    w.ks[p] = ks[p];
+                    w.vs[p] = vs[p];
+                }
+                w.walk(a, lds_k + wave * W::K_BYTES, lds_v + wave * W::V_BYTES, cur, cur.t0 + wave,
+                       it.kv_len, used ? it.limit(col) : 0, it.limit(cur.ct * kCols), exp2_scale(a), ready,
+                       chain, next, next.t0 + wave, nit.kv_len);
+#pragma unroll
+                for (int p = 0; p < W::NP; ++p) {
+                    page[p] = w.page[p];
+                    ks[p] = w.ks[p];
+                    vs[p] = w.vs[p];
+                }
+                ready = chain;
+            }
+            float part[DV / 16], m, l;
+            join_waves<W, DV>(w, lds_v, part, m, l);
+            const int x = tid >> 4, oc = cur.ct * kCols + x, od = (tid & 15) * 4;
+            if (oc < it.cols) {
+                if (cur.whole) {
+                    store_row<DV>(a, it.q0 + oc / it.G, cur.h * it.G + oc % it.G, od, part, m, l);
+                } else {
+                    const int64_t slot = ((int64_t)blockIdx.x * 2 + (first ? 0 : 1)) * kCols + x;
+                    float* const ws = a.ws + slot * DV + od;
+#pragma unroll
+                    for (int j = 0; j < DV / 64; ++j)
+                        *(v4f*)(ws + 64 * j) = v4f{part[4 * j], part[4 * j + 1], part[4 * j + 2],
+                                                   part[4 * j + 3]};
+                    if (od == 0) {
+                        float* const ml = a.ws + (int64_t)gridDim.x * 2 * kCols * DV + slot * 2;
+                        ml[0] = m;
+                        ml[1] = l;
+                    }
+                }
+            }
+        }
+        first = false;
+        cur = next;
+        it = nit;
+        valid = has;
+    }
+    wait_vmcnt<0>();                                            // no load outlives its LDS
+}
+
+// Adds the partial sums of the workgroups that shared an item, one row (item column) by STRANDS
+// strands of DV / 4 lanes each: every strand takes its workgroups in token order, then the strands
+// are added in order.  Rows of a request without tokens get their zeros here.
+//
+// Where items are many, an item has few parts and two strands (128 wide: one wave) take a row;
+// where they are few, a workgroup of eight strands does.
+template <int DV, int STRANDS>
+__global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int col_tiles,
+                                                                 int groups, int max_cols) {
+    constexpr int L = DV / 4, ROWS = kAttnThreads / (L * STRANDS);
+    __shared__ float red[kAttnThreads / L][DV + 4];
+    __shared__ float red_l[kAttnThreads / L];
+    const int tid = threadIdx.x, strand = tid / L % STRANDS, d4 = tid % L * 4;
+    int64_t x = (int64_t)blockIdx.x * ROWS + tid / (L * STRANDS);
+    const int col = (int)(x % max_cols);
+    x /= max_cols;
+    const int h = (int)(x % a.heads_kv);
+    const int r = (int)min(x / a.heads_kv, (int64_t)a.R - 1);
+    const Item it = Item::of<false>(a, r);
+    const bool live = x / a.heads_kv < a.R && col < it.cols;
+    const int ct = col / kCols;
+    const int64_t items = (int64_t)a.heads_kv * col_tiles;
+    const int64_t t0 = max(a.tile_offsets[r], 0), nt = (int64_t)a.tile_offsets[r + 1] - t0;
+    const int64_t row = it.q0 + col / it.G;
+    const int head = h * it.G + col % it.G;
+    const SplitPlan sp = split_plan(a, col_tiles, groups);
+    const int64_t begin = t0 * items + ((int64_t)h * col_tiles + ct) * nt;
+    const int wa = (int)min(begin / sp.per, (int64_t)groups);
+    const int wb = (int)min((begin + nt - 1) / sp.per, (int64_t)groups - 1);
+    const bool joins = live && nt > 0 && wa < wb;               // else finished by one workgroup
+    const auto slot_of = [&](int w) {
+        return ((int64_t)w * 2 + (w * sp.per >= begin ? 0 : 1)) * kCols + col % kCols;
+    };
+    const float* const ml = a.ws + (int64_t)groups * 2 * kCols * DV;
+    float m = neg_inf(), l = 0.f;
+    v4f acc = {0.f, 0.f, 0.f, 0.f};
+    if (joins) {
+        // the row's lanes (64, or all 256 of the workgroup's waves alike) look at every part's m
+        for (int w = wa + (tid & 63); w <= wb; w += 64) m = fmaxf(m, ml[slot_of(w) * 2]);
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+    if (joins) {
+#pragma unroll 4
+        for (int w = wa + strand; w <= wb; w += STRANDS) {
+            const int64_t slot = slot_of(w);
+            const float mw = ml[slot * 2], lw = ml[slot * 2 + 1];
+            const v4f v = *(const v4f*)(a.ws + slot * DV + d4);
+            const bool saw = mw != neg_inf() || lw != 0.f;      // otherwise its sums are zeros
+            const float f = saw ? __builtin_amdgcn_exp2f(mw - m) : 0.f;
+            l = __builtin_fmaf(lw, f, l);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(v[i], f, acc[i]);
+        }
+    }
+    const int mine = tid / L;
+    *(v4f*)&red[mine][d4] = acc;
+    if (tid % L == 0) red_l[mine] = l;
+    __syncthreads();
+    if (strand != 0 || !live) return;
+    uint16_t* const out = a.out + (row * a.heads_q + head) * DV + d4;
+    if (nt <= 0) {
+        *(uint2*)out = make_uint2(0, 0);
+        if (a.lse && d4 == 0) a.lse[row * a.heads_q + head] = neg_inf();
+    } else if (joins) {
+#pragma unroll
+        for (int i = 1; i < STRANDS; ++i) {
+            l += red_l[mine + i];
+            acc += *(const v4f*)&red[mine + i][d4];
+        }
+        const float rl = l == 0.f ? 0.f : 1.0f / l;
+        *(uint2*)out =
+            make_uint2(pack_bf16x2(acc[0] * rl, acc[1] * rl), pack_bf16x2(acc[2] * rl, acc[3] * rl));
+        if (a.lse && d4 == 0)
+            a.lse[row * a.heads_q + head] = l == 0.f ? neg_inf() : (m + __builtin_log2f(l)) * kLn2;
+    }
+}
+
+// Tile of a wave, and workgroups of a split launch: as many as the CUs hold at once (16 KB of
+// LDS a wave at 128/128, 20 at 192/128: two workgroups; four at 64/64).
+constexpr int kSplitTile = 64;
+static int split_groups(int dk) { return dk == 64 ? 1024 : 512; }
+static bool splits(int64_t max_new, int32_t heads_q, int32_t heads_kv) {
+    return max_new * (heads_q / heads_kv) <= kSplitMaxCols;
+}
+
+size_t attn_paged_workspace_bytes(int64_t, int64_t max_new, int32_t heads_q, int32_t heads_kv,
+                                  int32_t dk, int32_t dv) {
+    if (!splits(max_new, heads_q, heads_kv)) return 0;
+    return (size_t)split_groups(dk) * 2 * kCols * (dv + 2) * sizeof(float);
+}
+
+template <int DK, int DV, int B>
+static hipError_t attn_launch(const AttnArgs& a, hipStream_t stream) {
+    constexpr int TT = kSplitTile;
+    const int max_cols = (int)(a.max_new * (a.heads_q / a.heads_kv));
+    const int64_t col_tiles = (max_cols + kCols - 1) / kCols;
+    if (a.ws && splits(a.max_new, a.heads_q, a.heads_kv)) {
+        const int groups = split_groups(DK);
+        attn_split_kernel<DK, DV, B, TT><<<dim3(groups), dim3(kAttnThreads), 0, stream>>>(a, (int)col_tiles);
+        const int64_t items = (int64_t)a.R * a.heads_kv * col_tiles;
+        const int64_t rows = (int64_t)a.R * a.heads_kv * max_cols;
+        // parts per item, about groups / items + 1
+        constexpr int FEW = 256 / DV;                           // a wave's strands
+        if (items * 4 >= groups) {
+            attn_join_kernel<DV, FEW><<<dim3((unsigned)((rows + 3) / 4)), dim3(kAttnThreads), 0, stream>>>(
+                a, (int)col_tiles, groups, max_cols);
+        } else {
+            attn_join_kernel<DV, 4 * FEW><<<dim3((unsigned)rows), dim3(kAttnThreads), 0, stream>>>(
+                a, (int)col_tiles, groups, max_cols);
+        }
+        return hipGetLastError();
+    }
+    const int64_t items = (int64_t)a.R * a.heads_kv * col_tiles;
+    attn_item_kernel<DK, DV, B, TT><<<dim3((unsigned)items), dim3(kAttnThreads), 0, stream>>>(a, (int)col_tiles);
+    return hipGetLastError();
+}
 
 template <int DK, int DV>
 static hipError_t attn_launch(const AttnArgs& a, hipStream_t stream) {
-    const int64_t col_tiles = (a.max_new * (a.heads_q / a.heads_kv) + kCols - 1) / kCols;
-    const int64_t items = (int64_t)a.R * a.heads_kv * col_tiles;
-    attn_item_kernel<DK, DV><<<dim3((unsigned)items), dim3(kAttnThreads), 0, stream>>>(a, (int)col_tiles);
-    return hipGetLastError();
+    return a.log_b == 5   ? attn_launch<DK, DV, 32>(a, stream)
+           : a.log_b == 6 ? attn_launch<DK, DV, 64>(a, stream)
+                          : attn_launch<DK, DV, 128>(a, stream);
 }
 
 hipError_t launch_attn_paged(const AttnArgs& a, int32_t dk, int32_t dv, hipStream_t stream) {
