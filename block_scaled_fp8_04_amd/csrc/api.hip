@@ -400,6 +400,7 @@ int bfp8_attn_paged(const void* q_bf16, int64_t q_token_stride, int64_t q_head_s
     a.out = (uint16_t*)out_bf16;
     a.lse = lse;
     a.ws = (float*)workspace;
+    a.ws_bytes = workspace ? workspace_bytes : 0;
     return from_hip(bfp8::launch_attn_paged(a, dk, dv, (hipStream_t)stream));
 }
 

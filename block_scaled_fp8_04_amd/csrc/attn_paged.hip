@@ -19,6 +19,8 @@
 // e4m3 terms loses what lies 2^-22 below a tile's largest.  Logits, maxima,
 // norms and sums are fp32.  Running maxima are rounded up to integers (in units of log 2),
 // so that rescaling by 2^(old - new) is exact.
+#include <algorithm>
+
 #include "device_codec.hpp"
 #include "internal.hpp"
 #include "tile_common.hpp"
@@ -701,6 +703,409 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int
     }
 }
 
+// ---------------------------------------------------------------- many query columns
+//
+// Prompts and chunks: a workgroup takes 32 columns a wave of one request and KV head and walks
+// the tokens they see.  The products and the softmax beside them bound this, so the codes are
+// widened once per workgroup on their way into LDS, keys to bf16 with their scale, values to f16
+// without it, and every wave reads its fragments from there.
+//
+// p enters its product as one f16 term (eleven bits).  Its range is kept by the value page's
+// scale 2^e: with m' the running maximum of x + e over the tokens (x the logit in units of log
+// 2, m' rounded up to an integer), p' = 2^(x + e - m' + 15) lies in (0, 2^15], is exact to
+// 2^-11 down to 2^-29 of the largest weighted token and to 2^-40 of it below that.  O sums p'
+// times the codes, l sums p' 2^-e: their quotient is the result.
+//
+// A step forms the logits of 32 tokens, does the softmax of the 32 before and adds the values of
+// the 32 before those: three independent streams, written out so that each matrix instruction
+// is followed by the vector work that fits beside it (a softmax element takes 26 of its 32
+// cycles) and by the LDS read of a fragment three instructions on.  S^T's rows are the tokens
+// with bits 2 and 3 exchanged, which makes its registers the second product's operand as they
+// stand.
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef _Float16 h8v __attribute__((ext_vector_type(8)));
+typedef _Float16 h2v __attribute__((ext_vector_type(2)));
+
+constexpr int kBlockTile = 64;                // tokens in LDS at a time
+constexpr int kBlockSlots = 512;              // workgroups that a split launch aims at
+constexpr int kBlockMaxSplits = 16;
+
+__device__ __forceinline__ h8v widen8h(uint32_t w0, uint32_t w1) {
+    const h2v a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w0, 1.f, false);
+    const h2v b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w0, 1.f, true);
+    const h2v c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w1, 1.f, false);
+    const h2v d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w1, 1.f, true);
+    return h8v{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// x of the two halves of the wave: their maximum, their sum
+__device__ __forceinline__ float half_max(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+template <int DK, int DV, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, int blocks, int splits) {
+    constexpr int CB = 32 * WAVES, NT = 64 * WAVES;  // columns and threads of a workgroup
+    constexpr int KS = DK / 16, DT = DV / 32;        // steps of the products, 32-row tiles of O^T
+    constexpr int K_CHUNKS = kBlockTile * DK / 16, V_CHUNKS = kBlockTile * DV / 16;
+    constexpr int KCH = (K_CHUNKS + NT - 1) / NT, VCH = (V_CHUNKS + NT - 1) / NT;
+    constexpr int K_ROW = DK * 2, V_ROW = kBlockTile * 2;
+    constexpr int K_BUF = kBlockTile * K_ROW, V_BUF = DV * V_ROW;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds_k[2 * K_BUF];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds_v[2 * V_BUF];
+    const int tid = threadIdx.x, lane = tid & 63, hh = lane >> 5, lr = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int G = a.heads_q / a.heads_kv;
+
+    // block b of the launch: request r's blocks start at q_offsets[r] * G / CB + r, where there
+    // is room for all of them; the last ones, which see the most tokens, go first
+    int idx = blockIdx.x;
+    const int z = idx % splits;
+    idx /= splits;
+    const int h = idx % a.heads_kv, b = blocks - 1 - idx / a.heads_kv;
+    const auto start_of = [&](int r) {
+        return (int64_t)min(max((int64_t)a.q_offsets[r], (int64_t)0), a.T) * G / CB + r;
+    };
+    int r = 0;
+    {
+        const int hi = __popcll(__ballot(lane * 64 < a.R && start_of(min(lane * 64, a.R)) <= b)) - 1;
+        const int at = max(hi, 0) * 64 + lane;
+        r = max(hi, 0) * 64 +
+            max(__popcll(__ballot(at < a.R && start_of(min(at, a.R)) <= b)) - 1, 0);
+        r = __builtin_amdgcn_readfirstlane(r);
+    }
+    const Item it = Item::of<true>(a, r);
+    const int c0 = __builtin_amdgcn_readfirstlane((int)min(b - start_of(r), (int64_t)1 << 22)) * CB;
+    if (c0 < 0 || c0 >= it.cols) return;
+    const int c1 = min(c0 + CB, it.cols) - 1;                   // last column
+    const int seen_by_all = it.limit(c0), seen = it.limit(c1);
+    const int tiles = (seen + kBlockTile - 1) / kBlockTile;
+    const int t_first = (int)((int64_t)tiles * z / splits), t_end = (int)((int64_t)tiles * (z + 1) / splits);
+    const int n = t_end - t_first;
+    const int kv_len = it.kv_len, last = max(kv_len - 1, 0) >> a.log_b, B = 1 << a.log_b;
+    const scalar_i32 table = (scalar_i32)(uintptr_t)(a.block_table + r * a.width);
+    const scalar_f32 k_scales = (scalar_f32)(uintptr_t)a.k_scales;
+    const scalar_i32 v_scales = (scalar_i32)(uintptr_t)a.v_scales;
+    const float c = exp2_scale(a);
+
+    // this lane's column
+    const int col = c0 + wave * 32 + lr;
+    const bool used = col < it.cols;
+    const int limit = used ? it.limit(col) : 0;
+    bf8v q[KS];
+    {
+        const uint16_t* const row = it.row(a, h, used ? col : c0);
+        const bool vec = q_vec(a), negate = a.scale < 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) q[ks] = load_q8(row + 16 * ks + 8 * hh, vec, negate);
+    }
+    v16f o[DT];
+    float m = neg_inf(), l = 0.f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+
+    if (n > 0) {
+        // staging: global codes of one tile in registers, widened into LDS later
+        uint4 kr[KCH], vr[VCH];
+        float ks_r[2];                                           // scales of kr's two 32-token groups
+        const auto page_of = [&](int token) {
+            return min(max((int64_t)table[min(token >> a.log_b, last)], (int64_t)0), a.pages - 1) * a.heads_kv + h;
+        };
+        const auto load_k = [&](int tile) {
+            const int base = min(tile, t_end - 1) * kBlockTile;
+            const int64_t p0 = page_of(base), p1 = page_of(base + 32);
+            ks_r[0] = k_scales[p0];
+            ks_r[1] = k_scales[p1];
+#pragma unroll
+            for (int e = 0; e < KCH; ++e) {
+                const int x = e * NT + tid, token = x / (DK / 16), at = x % (DK / 16);
+                const uint8_t* const page = a.k_cache + (token < 32 ? p0 : p1) * ((int64_t)B * DK);
+                if (K_CHUNKS % NT == 0 || x < K_CHUNKS)
+                    kr[e] = *(const uint4*)(page + ((base + token) & (B - 1)) * DK + 16 * at);
+            }
+        };
+        const auto load_v = [&](int tile) {
+            const int base = min(tile, t_end - 1) * kBlockTile;
+            const int64_t p0 = page_of(base), p1 = page_of(base + 32);
+#pragma unroll
+            for (int e = 0; e < VCH; ++e) {
+                const int x = e * NT + tid, d = x >> 2, token = (x & 3) * 16;
+                const uint8_t* const page = a.v_cache + (token < 32 ? p0 : p1) * ((int64_t)B * DV);
+                if (V_CHUNKS % NT == 0 || x < V_CHUNKS)
+                    vr[e] = *(const uint4*)(page + d * B + ((base + token) & (B - 1)));
+            }
+        };
+        // a row's 16-byte chunks are permuted so that the rows that lanes read together lie in
+        // different banks
+        const auto k_swz = [](int row) { return DK == 128 ? (row & 15) : (row >> 1 & 7); };
+        const auto store_k = [&](int buf) {
+#pragma unroll
+            for (int e = 0; e < KCH; ++e) {
+                const int x = e * NT + tid, token = x / (DK / 16), at = x % (DK / 16);
+                if (K_CHUNKS % NT != 0 && x >= K_CHUNKS) break;
+                const float s = token < 32 ? ks_r[0] : ks_r[1];
+                uint8_t* const to = lds_k + buf * K_BUF + token * K_ROW;
+                *(bf8v*)(to + ((2 * at) ^ k_swz(token)) * 16) = widen8((int)kr[e].x, (int)kr[e].y, s);
+                *(bf8v*)(to + ((2 * at + 1) ^ k_swz(token)) * 16) = widen8((int)kr[e].z, (int)kr[e].w, s);
+            }
+        };
+        const auto store_v = [&](int tile, int buf) {
+            const int live = kv_len - min(tile, t_end - 1) * kBlockTile;
+#pragma unroll
+            for (int e = 0; e < VCH; ++e) {
+                const int x = e * NT + tid, d = x >> 2, token = (x & 3) * 16;
+                if (V_CHUNKS % NT != 0 && x >= V_CHUNKS) break;
+                uint32_t w[4] = {vr[e].x, vr[e].y, vr[e].z, vr[e].w};
+                if (live < kBlockTile) {
+                    // bytes behind the last token may hold anything: 0 * NaN is NaN
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int k = min(max(live - token - 4 * y, 0), 4);
+                        w[y] &= k == 4 ? 0xFFFFFFFFu : (1u << (8 * k)) - 1;
+                    }
+                }
+                const int f = d >> 1 & 7;
+                uint8_t* const to = lds_v + buf * V_BUF + d * V_ROW;
+                *(h8v*)(to + (((x & 3) * 2) ^ f) * 16) = widen8h(w[0], w[1]);
+                *(h8v*)(to + (((x & 3) * 2 + 1) ^ f) * 16) = widen8h(w[2], w[3]);
+            }
+        };
+        // fragment places: K rows are tokens with bits 2 and 3 exchanged, V rows are lr + 32 d
+        const int krow = (lr & 0x13) | (lr & 4) << 1 | (lr & 8) >> 1;
+        int kat[KS], vat[4];
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) kat[ks] = krow * K_ROW + (((2 * ks) ^ (k_swz(krow) ^ hh)) * 16);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) vat[x] = lr * V_ROW + (((2 * x) ^ ((lr >> 1 & 7) ^ hh)) * 16);
+
+        v16f s;
+        uint4 p[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        float top;                                               // maximum of s
+        // one step: softmax of subtile j, logits of j + 1 (half KSUB of buffer KBUF) and their
+        // maximum, values of j - 1 (half VSUB of buffer VBUF)
+        constexpr int NM = KS + 2 * DT;                          // matrix instructions
+        constexpr int AHEAD = 3;
+        const auto step = [&](int j, auto kbuf_, auto ksub_, auto vbuf_, auto vsub_) __attribute__((always_inline)) {
+            constexpr int KBUF = decltype(kbuf_)::value, KSUB = decltype(ksub_)::value;
+            constexpr int VBUF = decltype(vbuf_)::value, VSUB = decltype(vsub_)::value;
+            uint4 ring[AHEAD + 1];
+            const auto read = [&](auto y_) __attribute__((always_inline)) {
+                constexpr int Y = decltype(y_)::value;
+                if constexpr (Y < KS)
+                    ring[Y % (AHEAD + 1)] = *(const uint4*)(lds_k + kat[Y] + KBUF * K_BUF + KSUB * 32 * K_ROW);
+                else if constexpr (Y < NM)
+                    ring[Y % (AHEAD + 1)] = *(const uint4*)(lds_v + vat[2 * VSUB + (Y - KS) / DT] + VBUF * V_BUF +
+                                                           (Y - KS) % DT * 32 * V_ROW);
+            };
+            read(StageId<0>{});
+            read(StageId<1>{});
+            read(StageId<2>{});
+            const int base = t_first * kBlockTile + 32 * j;
+            if (base + 32 > seen_by_all) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (base + 16 * (i >> 3) + 8 * hh + (i & 7) >= limit) s[i] = neg_inf();
+                top = s[0];
+#pragma unroll
+                for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+            }
+            const int e = (int)((uint32_t)v_scales[page_of(base)] >> 23) - 127;
+            const float m_new = fmaxf(m, __builtin_ceilf(half_max(top) * c) + (float)e);
+            const float alpha = m == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(m - m_new);
+            const float add = m_new == neg_inf() ? 0.f : (float)(e + 15) - m_new;
+            const bool grew = __any(m_new != m);
+            float cc = c;
+            if (__any(__builtin_fabsf(m_new) > 4194304.f && m_new != neg_inf())) {      // see AttnWave::softmax
+                asm volatile("" ::: "memory");                   // a branch: it is hardly ever taken
+                s *= c;
+                cc = 1.f;
+            }
+            m = m_new;
+            v16f next;
+            float sum[2] = {0.f, 0.f}, y_last = 0.f;
+            uint32_t w[8];
+            __builtin_amdgcn_sched_barrier(0);
+            const auto slot = [&](auto y_) __attribute__((always_inline)) {
+                constexpr int Y = decltype(y_)::value;
+                read(StageId<Y + AHEAD>{});
+                const uint4 f = ring[Y % (AHEAD + 1)];
+                if constexpr (Y < KS) {
+                    if constexpr (Y == 0) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) next[i] = 0.f;
+                    }
+                    next = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8v, f), q[Y], next, 0, 0, 0);
+                } else {
+                    constexpr int U = (Y - KS) / DT, D = (Y - KS) % DT;
+                    o[D] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8v, f),
+                                                                  __builtin_bit_cast(h8v, p[U]), o[D], 0, 0, 0);
+                }
+                // this slot's softmax elements
+#pragma unroll
+                for (int i = 16 * Y / NM; i < 16 * (Y + 1) / NM; ++i) {
+                    const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], cc, add));
+                    sum[i & 1] += y;
+                    if (i & 1) {
+                        w[i >> 1] = __builtin_bit_cast(uint32_t, h2v{(_Float16)y_last, (_Float16)y});
+                        asm volatile("" : "+v"(w[i >> 1]), "+v"(sum[0]), "+v"(sum[1]));  // computed here
+                    }
+                    y_last = y;
+                }
+                // and of the next step's maximum, once its logits are there
+                if constexpr (Y > KS) {
+                    constexpr int N = 2 * DT - 1, X = Y - KS - 1;
+                    if constexpr (X == 0) top = next[0];
+#pragma unroll
+                    for (int i = 16 * X / N; i < 16 * (X + 1) / N; ++i) top = fmaxf(top, next[i]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            slot(StageId<0>{}); slot(StageId<1>{}); slot(StageId<2>{}); slot(StageId<3>{});
+            slot(StageId<4>{}); slot(StageId<5>{}); slot(StageId<6>{}); slot(StageId<7>{});
+            if constexpr (NM > 8) {
+                slot(StageId<8>{}); slot(StageId<9>{}); slot(StageId<10>{}); slot(StageId<11>{});
+                slot(StageId<12>{}); slot(StageId<13>{}); slot(StageId<14>{}); slot(StageId<15>{});
+            }
+            if constexpr (NM > 16) {
+                slot(StageId<16>{}); slot(StageId<17>{}); slot(StageId<18>{}); slot(StageId<19>{});
+            }
+            l = __builtin_fmaf(sum[0] + sum[1], __uint_as_float((uint32_t)(127 - e) << 23), l * alpha);
+            p[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            p[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            s = next;
+            if (grew) {                                          // O holds the values up to j - 1
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[d] *= alpha;
+            }
+        };
+        static_assert(NM == 8 || NM == 16 || NM == 20, "slots written out");
+
+        load_k(t_first);
+        load_v(t_first);
+        store_k(0);
+        store_v(t_first, 0);
+        load_k(t_first + 1);
+        store_k(1);
+        // the values "before the first" meet p = 0: zeros, since LDS may hold anything
+        for (int x = tid; x < V_BUF / 16; x += NT) ((uint4*)(lds_v + V_BUF))[x] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+        load_k(t_first + 2);
+        load_v(t_first + 1);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+            s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*(const bf8v*)(lds_k + kat[ks]), q[ks], s, 0, 0, 0);
+        top = s[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+        // tile i: buffers i & 1.  Between its two steps every wave is done with the keys of tile i
+        // and the values of tile i - 1, and their buffers take those of i + 2 and i + 1
+        const auto tile_pair = [&](int i, auto par) __attribute__((always_inline)) {
+            constexpr int P = decltype(par)::value;
+            step(2 * i, StageId<P>{}, StageId<1>{}, StageId<1 - P>{}, StageId<1>{});
+            __syncthreads();
+            store_k(P);
+            store_v(t_first + i + 1, 1 - P);
+            load_k(t_first + i + 3);
+            load_v(t_first + i + 2);
+            step(2 * i + 1, StageId<1 - P>{}, StageId<0>{}, StageId<P>{}, StageId<0>{});
+        };
+        for (int i = 0; i < n; i += 2) {
+            tile_pair(i, StageId<0>{});
+            if (i + 1 < n) tile_pair(i + 1, StageId<1>{});
+        }
+        const uint8_t* const at = lds_v + (n - 1 & 1) * V_BUF;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const h8v*)(at + vat[2 + u] + d * 32 * V_ROW),
+                                                              __builtin_bit_cast(h8v, p[u]), o[d], 0, 0, 0);
+    }
+
+    // results: lane half hh holds dims 32 d + 8 (i / 4) + 4 hh + i % 4 of its column
+    const float ll = half_sum(l) * 0x1p-15f;
+    if (!used) return;
+    if (splits == 1) {
+        const float rl = ll == 0.f ? 0.f : 0x1p-15f / ll;
+        const int64_t row = it.q0 + col / G;
+        const int head = h * G + col % G;
+        uint16_t* const out = a.out + (row * a.heads_q + head) * DV + 4 * hh;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                *(uint2*)(out + 32 * d + 8 * y) =
+                    make_uint2(pack_bf16x2(o[d][4 * y] * rl, o[d][4 * y + 1] * rl),
+                               pack_bf16x2(o[d][4 * y + 2] * rl, o[d][4 * y + 3] * rl));
+        if (a.lse && hh == 0)
+            a.lse[row * a.heads_q + head] = ll == 0.f ? neg_inf() : (m + __builtin_log2f(ll)) * kLn2;
+    } else {
+        const int64_t slot = (int64_t)blockIdx.x * CB + wave * 32 + lr;
+        float* const ws = a.ws + slot * DV + 4 * hh;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                *(v4f*)(ws + 32 * d + 8 * y) =
+                    v4f{o[d][4 * y], o[d][4 * y + 1], o[d][4 * y + 2], o[d][4 * y + 3]} * 0x1p-15f;
+        if (hh == 0) {
+            float* const ml = a.ws + (int64_t)gridDim.x * CB * DV + slot * 2;
+            ml[0] = m;
+            ml[1] = ll;
+        }
+    }
+}
+
+// Adds the parts of a split launch, in token order: one row per DV / 4 lanes.
+template <int DV, int WAVES>
+__global__ __launch_bounds__(kAttnThreads) void attn_block_join_kernel(AttnArgs a, int blocks, int splits) {
+    constexpr int CB = 32 * WAVES, L = DV / 4, ROWS = kAttnThreads / L;
+    const int tid = threadIdx.x, d4 = tid % L * 4;
+    const int G = a.heads_q / a.heads_kv;
+    const int64_t row = (int64_t)blockIdx.x * ROWS + tid / L;   // of T * heads_q
+    const int64_t t = row / a.heads_q;
+    const int head = (int)(row % a.heads_q), h = head / G;
+    if (t >= a.T) return;
+    int lo = 0, hi = a.R;                                      // the request of token t
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.q_offsets[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    const Item it = Item::of<false>(a, lo);
+    const int64_t col = (t - it.q0) * G + head % G;
+    if (t < it.q0 || col >= it.cols) return;
+    const int b = (int)(it.q0 * G / CB + lo + col / CB);
+    const int64_t first = ((int64_t)(blocks - 1 - b) * a.heads_kv + h) * splits;
+    const float* const ml = a.ws + (int64_t)blocks * a.heads_kv * splits * CB * DV;
+    float m = neg_inf();
+    for (int z = 0; z < splits; ++z) m = fmaxf(m, ml[((first + z) * CB + col % CB) * 2]);
+    v4f acc = {0.f, 0.f, 0.f, 0.f};
+    float l = 0.f;
+    for (int z = 0; z < splits; ++z) {
+        const int64_t slot = (first + z) * CB + col % CB;
+        const float mw = ml[slot * 2], lw = ml[slot * 2 + 1];
+        const float f = mw != neg_inf() || lw != 0.f ? __builtin_amdgcn_exp2f(mw - m) : 0.f;
+        const v4f v = *(const v4f*)(a.ws + slot * DV + d4);
+        l = __builtin_fmaf(lw, f, l);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(v[i], f, acc[i]);
+    }
+    const float rl = l == 0.f ? 0.f : 1.0f / l;
+    *(uint2*)(a.out + (t * a.heads_q + head) * DV + d4) =
+        make_uint2(pack_bf16x2(acc[0] * rl, acc[1] * rl), pack_bf16x2(acc[2] * rl, acc[3] * rl));
+    if (a.lse && d4 == 0) a.lse[t * a.heads_q + head] = l == 0.f ? neg_inf() : (m + __builtin_log2f(l)) * kLn2;
+}
+
 // Tile of a wave, and workgroups of a split launch: as many as the CUs hold at once (16 KB of
 // LDS a wave at 128/128, 20 at 192/128: two workgroups; four at 64/64).
 constexpr int kSplitTile = 64;
@@ -709,43 +1114,83 @@ static bool splits(int64_t max_new, int32_t heads_q, int32_t heads_kv) {
     return max_new * (heads_q / heads_kv) <= kSplitMaxCols;
 }
 
-size_t attn_paged_workspace_bytes(int64_t, int64_t max_new, int32_t heads_q, int32_t heads_kv,
+// How a launch of many columns divides: eight waves a workgroup, or four where that leaves CUs
+// idle, and the tokens of a block over several workgroups where even those are few.
+struct BlockPlan {
+    int waves;
+    int64_t blocks, splits;                          // per KV head; parts of each
+};
+static BlockPlan block_plan(int64_t T, int64_t R, int heads_q, int heads_kv) {
+    const int64_t G = heads_q / heads_kv;
+    BlockPlan p{8, T * G / 256 + R, 1};
+    if (p.blocks * heads_kv < 256) {
+        p.waves = 4;
+        p.blocks = T * G / 128 + R;
+        const int64_t n = p.blocks * heads_kv;
+        p.splits = n * 2 <= kBlockSlots ? kBlockSlots / n : 1;
+        if (p.splits > kBlockMaxSplits) p.splits = kBlockMaxSplits;
+    }
+    return p;
+}
+
+size_t attn_paged_workspace_bytes(int64_t R, int64_t max_new, int32_t heads_q, int32_t heads_kv,
                                   int32_t dk, int32_t dv) {
-    if (!splits(max_new, heads_q, heads_kv)) return 0;
-    return (size_t)split_groups(dk) * 2 * kCols * (dv + 2) * sizeof(float);
+    if (splits(max_new, heads_q, heads_kv))
+        return (size_t)split_groups(dk) * 2 * kCols * (dv + 2) * sizeof(float);
+    // any number of tokens up to R * max_new: at most kBlockSlots parts of 128 columns
+    const BlockPlan p = block_plan(R * max_new, R, heads_q, heads_kv);
+    const int64_t most = p.waves == 4 ? p.blocks * heads_kv * kBlockMaxSplits : kBlockSlots;
+    return (size_t)(most < kBlockSlots ? most : kBlockSlots) * 128 * (dv + 2) * sizeof(float);
 }
 
 template <int DK, int DV, int B>
-static hipError_t attn_launch(const AttnArgs& a, hipStream_t stream) {
-    constexpr int TT = kSplitTile;
+static hipError_t split_launch(const AttnArgs& a, hipStream_t stream) {
     const int max_cols = (int)(a.max_new * (a.heads_q / a.heads_kv));
     const int64_t col_tiles = (max_cols + kCols - 1) / kCols;
-    if (a.ws && splits(a.max_new, a.heads_q, a.heads_kv)) {
-        const int groups = split_groups(DK);
-        attn_split_kernel<DK, DV, B, TT><<<dim3(groups), dim3(kAttnThreads), 0, stream>>>(a, (int)col_tiles);
-        const int64_t items = (int64_t)a.R * a.heads_kv * col_tiles;
-        const int64_t rows = (int64_t)a.R * a.heads_kv * max_cols;
-        // parts per item, about groups / items + 1
-        constexpr int FEW = 256 / DV;                           // a wave's strands
-        if (items * 4 >= groups) {
-            attn_join_kernel<DV, FEW><<<dim3((unsigned)((rows + 3) / 4)), dim3(kAttnThreads), 0, stream>>>(
-                a, (int)col_tiles, groups, max_cols);
-        } else {
-            attn_join_kernel<DV, 4 * FEW><<<dim3((unsigned)rows), dim3(kAttnThreads), 0, stream>>>(
-                a, (int)col_tiles, groups, max_cols);
-        }
+    const int64_t items = (int64_t)a.R * a.heads_kv * col_tiles;
+    if (!a.ws) {
+        attn_item_kernel<DK, DV, B, kSplitTile>
+            <<<dim3((unsigned)items), dim3(kAttnThreads), 0, stream>>>(a, (int)col_tiles);
         return hipGetLastError();
     }
-    const int64_t items = (int64_t)a.R * a.heads_kv * col_tiles;
-    attn_item_kernel<DK, DV, B, TT><<<dim3((unsigned)items), dim3(kAttnThreads), 0, stream>>>(a, (int)col_tiles);
+    const int groups = split_groups(DK);
+    attn_split_kernel<DK, DV, B, kSplitTile><<<dim3(groups), dim3(kAttnThreads), 0, stream>>>(a, (int)col_tiles);
+    const int64_t rows = (int64_t)a.R * a.heads_kv * max_cols;
+    // parts per item, about groups / items + 1
+    constexpr int FEW = 256 / DV;                               // a wave's strands
+    if (items * 4 >= groups) {
+        attn_join_kernel<DV, FEW><<<dim3((unsigned)((rows + 3) / 4)), dim3(kAttnThreads), 0, stream>>>(
+            a, (int)col_tiles, groups, max_cols);
+    } else {
+        attn_join_kernel<DV, 4 * FEW><<<dim3((unsigned)rows), dim3(kAttnThreads), 0, stream>>>(
+            a, (int)col_tiles, groups, max_cols);
+    }
+    return hipGetLastError();
+}
+
+template <int DK, int DV, int WAVES>
+static hipError_t block_launch(const AttnArgs& a, const BlockPlan& p, hipStream_t stream) {
+    // as many parts as the workspace holds
+    const int64_t hold = a.ws ? (int64_t)(a.ws_bytes / (32 * WAVES * (DV + 2) * sizeof(float))) : 0;
+    const int64_t splits = std::max<int64_t>(1, std::min(p.splits, hold / (p.blocks * a.heads_kv)));
+    const unsigned grid = (unsigned)(p.blocks * a.heads_kv * splits);
+    attn_block_kernel<DK, DV, WAVES><<<dim3(grid), dim3(64 * WAVES), 0, stream>>>(a, (int)p.blocks, (int)splits);
+    if (splits > 1) {
+        const int64_t rows = a.T * a.heads_q, per = kAttnThreads / (DV / 4);
+        attn_block_join_kernel<DV, WAVES><<<dim3((unsigned)((rows + per - 1) / per)), dim3(kAttnThreads), 0, stream>>>(
+            a, (int)p.blocks, (int)splits);
+    }
     return hipGetLastError();
 }
 
 template <int DK, int DV>
 static hipError_t attn_launch(const AttnArgs& a, hipStream_t stream) {
-    return a.log_b == 5   ? attn_launch<DK, DV, 32>(a, stream)
-           : a.log_b == 6 ? attn_launch<DK, DV, 64>(a, stream)
-                          : attn_launch<DK, DV, 128>(a, stream);
+    if (splits(a.max_new, a.heads_q, a.heads_kv))
+        return a.log_b == 5   ? split_launch<DK, DV, 32>(a, stream)
+               : a.log_b == 6 ? split_launch<DK, DV, 64>(a, stream)
+                              : split_launch<DK, DV, 128>(a, stream);
+    const BlockPlan p = block_plan(a.T, a.R, a.heads_q, a.heads_kv);
+    return p.waves == 4 ? block_launch<DK, DV, 4>(a, p, stream) : block_launch<DK, DV, 8>(a, p, stream);
 }
 
 hipError_t launch_attn_paged(const AttnArgs& a, int32_t dk, int32_t dv, hipStream_t stream) {

@@ -120,6 +120,7 @@ struct AttnArgs {
     uint16_t* out;
     float* lse;
     float* ws;
+    size_t ws_bytes;
 };
 size_t attn_paged_workspace_bytes(int64_t R, int64_t max_new, int32_t heads_q, int32_t heads_kv,
                                   int32_t dk, int32_t dv);
