@@ -711,10 +711,12 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int
 // without it, and every wave reads its fragments from there.
 //
 // p enters its product as one f16 term (eleven bits).  Its range is kept by the value page's
-// scale 2^e: with m' the running maximum of x + e over the tokens (x the logit in units of log
-// 2, m' rounded up to an integer), p' = 2^(x + e - m' + 15) lies in (0, 2^15], is exact to
-// 2^-11 down to 2^-29 of the largest weighted token and to 2^-40 of it below that.  O sums p'
-// times the codes, l sums p' 2^-e: their quotient is the result.
+// scale 2^e: with m' within kSlack of the running maximum of x + e over the tokens (x the logit
+// in units of log 2), p' = 2^(x + e - m' + 15 - kSlack) lies in (0, 2^15], is exact to 2^-11
+// down to 2^-21 of the largest weighted token and to 2^-32 of it below that.  O sums p' times
+// the codes, l sums p' 2^-e: their quotient is the result.  The slack is there because a
+// maximum over 32 columns that is followed at once moves in every second step (2048 tokens
+// over 32k), and O has to be rescaled each time.
 //
 // A step forms the logits of 32 tokens, does the softmax of the 32 before and adds the values of
 // the 32 before those: three independent streams, written out so that each matrix instruction
@@ -729,6 +731,7 @@ typedef _Float16 h2v __attribute__((ext_vector_type(2)));
 constexpr int kBlockTile = 64;                // tokens in LDS at a time
 constexpr int kBlockSlots = 512;              // workgroups that a split launch aims at
 constexpr int kBlockMaxSplits = 16;
+constexpr float kSlack = 8.f;
 
 __device__ __forceinline__ h8v widen8h(uint32_t w0, uint32_t w1) {
     const h2v a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w0, 1.f, false);
@@ -748,9 +751,9 @@ __device__ __forceinline__ float half_sum(float x) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-template <int DK, int DV, int WAVES>
-__global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, int blocks, int splits) {
-    constexpr int CB = 32 * WAVES, NT = 64 * WAVES;  // columns and threads of a workgroup
+template <int DK, int DV, int WAVES, int NC>
+__global__ __launch_bounds__(WAVES * 64, 2 / NC) void attn_block_kernel(AttnArgs a, int blocks, int splits) {
+    constexpr int CB = 32 * NC * WAVES, NT = 64 * WAVES;        // columns and threads of a workgroup
     constexpr int KS = DK / 16, DT = DV / 32;        // steps of the products, 32-row tiles of O^T
     constexpr int K_CHUNKS = kBlockTile * DK / 16, V_CHUNKS = kBlockTile * DV / 16;
     constexpr int KCH = (K_CHUNKS + NT - 1) / NT, VCH = (V_CHUNKS + NT - 1) / NT;
@@ -788,69 +791,106 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
     const int t_first = (int)((int64_t)tiles * z / splits), t_end = (int)((int64_t)tiles * (z + 1) / splits);
     const int n = t_end - t_first;
     const int kv_len = it.kv_len, last = max(kv_len - 1, 0) >> a.log_b, B = 1 << a.log_b;
-    const scalar_i32 table = (scalar_i32)(uintptr_t)(a.block_table + r * a.width);
-    const scalar_f32 k_scales = (scalar_f32)(uintptr_t)a.k_scales;
-    const scalar_i32 v_scales = (scalar_i32)(uintptr_t)a.v_scales;
     const float c = exp2_scale(a);
 
-    // this lane's column
-    const int col = c0 + wave * 32 + lr;
-    const bool used = col < it.cols;
-    const int limit = used ? it.limit(col) : 0;
-    bf8v q[KS];
-    {
+    // this lane's columns: 32 t + lr of the wave's
+    int limit[NC];
+    bf8v q[NC][KS];
+    v16f o[NC][DT];
+    float m[NC], l[NC];
+#pragma unroll
+    for (int t = 0; t < NC; ++t) {
+        const int col = c0 + (wave * NC + t) * 32 + lr;
+        const bool used = col < it.cols;
+        limit[t] = used ? it.limit(col) : 0;
         const uint16_t* const row = it.row(a, h, used ? col : c0);
         const bool vec = q_vec(a), negate = a.scale < 0.f;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) q[ks] = load_q8(row + 16 * ks + 8 * hh, vec, negate);
+        for (int ks = 0; ks < KS; ++ks) q[t][ks] = load_q8(row + 16 * ks + 8 * hh, vec, negate);
+        m[t] = neg_inf();
+        l[t] = 0.f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[t][d][i] = 0.f;
     }
-    v16f o[DT];
-    float m = neg_inf(), l = 0.f;
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
 
     if (n > 0) {
-        // staging: global codes of one tile in registers, widened into LDS later
+        // staging: global codes of one tile in registers, widened into LDS later.  Page numbers and
+        // scales of 64 groups of 32 tokens are held by the wave's lanes, the next 64 fetched while
+        // these are in use: scalar loads in the loop would have every LDS wait behind them wait
+        // for them too (they share a counter).
         uint4 kr[KCH], vr[VCH];
-        float ks_r[2];                                           // scales of kr's two 32-token groups
-        const auto page_of = [&](int token) {
-            return min(max((int64_t)table[min(token >> a.log_b, last)], (int64_t)0), a.pages - 1) * a.heads_kv + h;
+        struct Pages {                                           // of a tile's two 32-token groups
+            int64_t page0, page1;
+            float ks0, ks1, vs0, vs1;
         };
-        const auto load_k = [&](int tile) {
+        int entry, entry_n = 0;
+        float ks_l, vs_l, ks_n = 0.f, vs_n = 0.f;
+        const auto fetch_table = [&](int tile) {                 // the lanes' entries from `tile` on
+            const int j = min((tile * kBlockTile + 32 * lane) >> a.log_b, last);
+            return (int)min(max((int64_t)a.block_table[(int64_t)r * a.width + j], (int64_t)0), a.pages - 1);
+        };
+        const auto fetch_scale = [&](const float* x, int e) { return x[(int64_t)e * a.heads_kv + h]; };
+        entry = fetch_table(t_first);
+        ks_l = fetch_scale(a.k_scales, entry);
+        vs_l = fetch_scale(a.v_scales, entry);
+        // of tile t_first + i, for i = 0, 1, 2, ... in order
+        const auto pages_of = [&](int i) {
+            const int at = 2 * i & 63;
+            if (at == 0 && i > 0) {
+                entry = entry_n;
+                ks_l = ks_n;
+                vs_l = vs_n;
+            }
+            if (at == 16) entry_n = fetch_table(t_first + i + 24);
+            if (at == 40) {
+                ks_n = fetch_scale(a.k_scales, entry_n);
+                vs_n = fetch_scale(a.v_scales, entry_n);
+            }
+            const auto lane_of = [&](float x, int l) {
+                return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), l));
+            };
+            Pages x;
+            x.page0 = (int64_t)__builtin_amdgcn_readlane(entry, at) * a.heads_kv + h;
+            x.page1 = (int64_t)__builtin_amdgcn_readlane(entry, at + 1) * a.heads_kv + h;
+            x.ks0 = lane_of(ks_l, at);
+            x.ks1 = lane_of(ks_l, at + 1);
+            x.vs0 = lane_of(vs_l, at);
+            x.vs1 = lane_of(vs_l, at + 1);
+            return x;
+        };
+        const auto load_k = [&](int tile, const Pages& pg) {
             const int base = min(tile, t_end - 1) * kBlockTile;
-            const int64_t p0 = page_of(base), p1 = page_of(base + 32);
-            ks_r[0] = k_scales[p0];
-            ks_r[1] = k_scales[p1];
 #pragma unroll
             for (int e = 0; e < KCH; ++e) {
                 const int x = e * NT + tid, token = x / (DK / 16), at = x % (DK / 16);
-                const uint8_t* const page = a.k_cache + (token < 32 ? p0 : p1) * ((int64_t)B * DK);
+                // 64 chunks lie in one group: the page is the wave's
+                const bool second = e * NT + wave * 64 >= K_CHUNKS / 2;
+                const uint8_t* const page = a.k_cache + uniform(second ? pg.page1 : pg.page0) * ((int64_t)B * DK);
                 if (K_CHUNKS % NT == 0 || x < K_CHUNKS)
-                    kr[e] = *(const uint4*)(page + ((base + token) & (B - 1)) * DK + 16 * at);
+                    kr[e] = *(const uint4*)(page + (uint32_t)(((base + token) & (B - 1)) * DK + 16 * at));
             }
         };
-        const auto load_v = [&](int tile) {
+        const auto load_v = [&](int tile, const Pages& pg) {
             const int base = min(tile, t_end - 1) * kBlockTile;
-            const int64_t p0 = page_of(base), p1 = page_of(base + 32);
 #pragma unroll
             for (int e = 0; e < VCH; ++e) {
                 const int x = e * NT + tid, d = x >> 2, token = (x & 3) * 16;
-                const uint8_t* const page = a.v_cache + (token < 32 ? p0 : p1) * ((int64_t)B * DV);
+                const uint8_t* const page = a.v_cache + (token < 32 ? pg.page0 : pg.page1) * ((int64_t)B * DV);
                 if (V_CHUNKS % NT == 0 || x < V_CHUNKS)
-                    vr[e] = *(const uint4*)(page + d * B + ((base + token) & (B - 1)));
+                    vr[e] = *(const uint4*)(page + (uint32_t)(d * B + ((base + token) & (B - 1))));
             }
         };
         // a row's 16-byte chunks are permuted so that the rows that lanes read together lie in
         // different banks
         const auto k_swz = [](int row) { return DK == 128 ? (row & 15) : (row >> 1 & 7); };
-        const auto store_k = [&](int buf) {
+        const auto store_k = [&](int buf, const Pages& pg) {
 #pragma unroll
             for (int e = 0; e < KCH; ++e) {
                 const int x = e * NT + tid, token = x / (DK / 16), at = x % (DK / 16);
                 if (K_CHUNKS % NT != 0 && x >= K_CHUNKS) break;
-                const float s = token < 32 ? ks_r[0] : ks_r[1];
+                const float s = e * NT + wave * 64 >= K_CHUNKS / 2 ? pg.ks1 : pg.ks0;
                 uint8_t* const to = lds_k + buf * K_BUF + token * K_ROW;
                 *(bf8v*)(to + ((2 * at) ^ k_swz(token)) * 16) = widen8((int)kr[e].x, (int)kr[e].y, s);
                 *(bf8v*)(to + ((2 * at + 1) ^ k_swz(token)) * 16) = widen8((int)kr[e].z, (int)kr[e].w, s);
@@ -885,14 +925,18 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
 #pragma unroll
         for (int x = 0; x < 4; ++x) vat[x] = lr * V_ROW + (((2 * x) ^ ((lr >> 1 & 7) ^ hh)) * 16);
 
-        v16f s;
-        uint4 p[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-        float top;                                               // maximum of s
+        v16f s_even[NC], s_odd[NC];                              // logits of even and odd subtiles
+        uint4 p_even[NC][2], p_odd[NC][2];                       // and their p'
+        float top[NC];                                           // maximum of the current ones
+#pragma unroll
+        for (int t = 0; t < NC; ++t) p_odd[t][0] = p_odd[t][1] = make_uint4(0, 0, 0, 0);
         // one step: softmax of subtile j, logits of j + 1 (half KSUB of buffer KBUF) and their
         // maximum, values of j - 1 (half VSUB of buffer VBUF)
-        constexpr int NM = KS + 2 * DT;                          // matrix instructions
+        constexpr int NM = KS + 2 * DT;                          // fragments, matrix instructions a column tile
         constexpr int AHEAD = 3;
-        const auto step = [&](int j, auto kbuf_, auto ksub_, auto vbuf_, auto vsub_) __attribute__((always_inline)) {
+        const auto step = [&](int j, float vs, v16f (&s)[NC], v16f (&next)[NC], const uint4 (&p)[NC][2],
+                              uint4 (&p_new)[NC][2], auto kbuf_, auto ksub_, auto vbuf_,
+                              auto vsub_) __attribute__((always_inline)) {
             constexpr int KBUF = decltype(kbuf_)::value, KSUB = decltype(ksub_)::value;
             constexpr int VBUF = decltype(vbuf_)::value, VSUB = decltype(vsub_)::value;
             uint4 ring[AHEAD + 1];
@@ -910,63 +954,80 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
             const int base = t_first * kBlockTile + 32 * j;
             if (base + 32 > seen_by_all) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (base + 16 * (i >> 3) + 8 * hh + (i & 7) >= limit) s[i] = neg_inf();
-                top = s[0];
+                for (int t = 0; t < NC; ++t) {
 #pragma unroll
-                for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+                    for (int i = 0; i < 16; ++i)
+                        if (base + 16 * (i >> 3) + 8 * hh + (i & 7) >= limit[t]) s[t][i] = neg_inf();
+                    top[t] = s[t][0];
+#pragma unroll
+                    for (int i = 1; i < 16; ++i) top[t] = fmaxf(top[t], s[t][i]);
+                }
             }
-            const int e = (int)((uint32_t)v_scales[page_of(base)] >> 23) - 127;
-            const float m_new = fmaxf(m, __builtin_ceilf(half_max(top) * c) + (float)e);
-            const float alpha = m == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(m - m_new);
-            const float add = m_new == neg_inf() ? 0.f : (float)(e + 15) - m_new;
-            const bool grew = __any(m_new != m);
+            const int e = (int)(__float_as_uint(vs) >> 23) - 127;
+            float alpha[NC], add[NC], sum[NC][2], y_last[NC];
+            bool grew = false, far = false;
+#pragma unroll
+            for (int t = 0; t < NC; ++t) {
+                // the reference follows the maximum only where it would be passed by over 2^kSlack
+                const float x = __builtin_ceilf(half_max(top[t]) * c) + (float)e;
+                const float m_new = x > m[t] + kSlack ? x : m[t];
+                alpha[t] = m[t] == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(m[t] - m_new);
+                add[t] = m_new == neg_inf() ? 0.f : (float)(e + 15 - (int)kSlack) - m_new;
+                grew |= m_new != m[t];
+                far |= __builtin_fabsf(m_new) > 4194304.f && m_new != neg_inf();
+                m[t] = m_new;
+                sum[t][0] = sum[t][1] = 0.f;
+            }
             float cc = c;
-            if (__any(__builtin_fabsf(m_new) > 4194304.f && m_new != neg_inf())) {      // see AttnWave::softmax
+            if (__any(far)) {                                    // see AttnWave::softmax
                 asm volatile("" ::: "memory");                   // a branch: it is hardly ever taken
-                s *= c;
+#pragma unroll
+                for (int t = 0; t < NC; ++t) s[t] *= c;
                 cc = 1.f;
             }
-            m = m_new;
-            v16f next;
-            float sum[2] = {0.f, 0.f}, y_last = 0.f;
-            uint32_t w[8];
+            uint32_t w[NC][8];
             __builtin_amdgcn_sched_barrier(0);
             const auto slot = [&](auto y_) __attribute__((always_inline)) {
                 constexpr int Y = decltype(y_)::value;
                 read(StageId<Y + AHEAD>{});
                 const uint4 f = ring[Y % (AHEAD + 1)];
-                if constexpr (Y < KS) {
-                    if constexpr (Y == 0) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) next[i] = 0.f;
+                for (int t = 0; t < NC; ++t) {
+                    if constexpr (Y < KS) {
+                        if constexpr (Y == 0) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) next[t][i] = 0.f;
+                        }
+                        next[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8v, f), q[t][Y],
+                                                                          next[t], 0, 0, 0);
+                    } else {
+                        constexpr int U = (Y - KS) / DT, D = (Y - KS) % DT;
+                        o[t][D] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                            __builtin_bit_cast(h8v, f), __builtin_bit_cast(h8v, p[t][U]), o[t][D], 0, 0, 0);
                     }
-                    next = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8v, f), q[Y], next, 0, 0, 0);
-                } else {
-                    constexpr int U = (Y - KS) / DT, D = (Y - KS) % DT;
-                    o[D] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8v, f),
-                                                                  __builtin_bit_cast(h8v, p[U]), o[D], 0, 0, 0);
-                }
-                // this slot's softmax elements
+                    // this slot's softmax elements
 #pragma unroll
-                for (int i = 16 * Y / NM; i < 16 * (Y + 1) / NM; ++i) {
-                    const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], cc, add));
-                    sum[i & 1] += y;
-                    if (i & 1) {
-                        w[i >> 1] = __builtin_bit_cast(uint32_t, h2v{(_Float16)y_last, (_Float16)y});
-                        asm volatile("" : "+v"(w[i >> 1]), "+v"(sum[0]), "+v"(sum[1]));  // computed here
+                    for (int i = 16 * Y / NM; i < 16 * (Y + 1) / NM; ++i) {
+                        const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], cc, add[t]));
+                        sum[t][i & 1] += y;
+                        if (i & 1) {
+                            w[t][i >> 1] = __builtin_bit_cast(uint32_t, h2v{(_Float16)y_last[t], (_Float16)y});
+                            asm volatile("" : "+v"(w[t][i >> 1]), "+v"(sum[t][0]), "+v"(sum[t][1]));  // computed here
+                        }
+                        y_last[t] = y;
                     }
-                    y_last = y;
-                }
-                // and of the next step's maximum, once its logits are there
-                if constexpr (Y > KS) {
-                    constexpr int N = 2 * DT - 1, X = Y - KS - 1;
-                    if constexpr (X == 0) top = next[0];
+                    // and of the next step's maximum, once its logits are there
+                    if constexpr (Y > KS) {
+                        constexpr int N = 2 * DT - 1, X = Y - KS - 1;
+                        if constexpr (X == 0) top[t] = next[t][0];
 #pragma unroll
-                    for (int i = 16 * X / N; i < 16 * (X + 1) / N; ++i) top = fmaxf(top, next[i]);
+                        for (int i = 16 * X / N; i < 16 * (X + 1) / N; ++i) top[t] = fmaxf(top[t], next[t][i]);
+                        asm volatile("" : "+v"(top[t]));
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                __builtin_amdgcn_sched_barrier(0);
             };
+            __builtin_amdgcn_s_setprio(1);                       // before a wave that is between its steps
             slot(StageId<0>{}); slot(StageId<1>{}); slot(StageId<2>{}); slot(StageId<3>{});
             slot(StageId<4>{}); slot(StageId<5>{}); slot(StageId<6>{}); slot(StageId<7>{});
             if constexpr (NM > 8) {
@@ -976,47 +1037,73 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
             if constexpr (NM > 16) {
                 slot(StageId<16>{}); slot(StageId<17>{}); slot(StageId<18>{}); slot(StageId<19>{});
             }
-            l = __builtin_fmaf(sum[0] + sum[1], __uint_as_float((uint32_t)(127 - e) << 23), l * alpha);
-            p[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            p[1] = make_uint4(w[4], w[5], w[6], w[7]);
-            s = next;
-            if (grew) {                                          // O holds the values up to j - 1
 #pragma unroll
-                for (int d = 0; d < DT; ++d) o[d] *= alpha;
+            for (int t = 0; t < NC; ++t) {
+                if (t == 0) __builtin_amdgcn_s_setprio(0);
+                l[t] = __builtin_fmaf(sum[t][0] + sum[t][1], __uint_as_float((uint32_t)(127 - e) << 23), l[t] * alpha[t]);
+                p_new[t][0] = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+                p_new[t][1] = make_uint4(w[t][4], w[t][5], w[t][6], w[t][7]);
+            }
+            if (__any(grew)) {                                   // O holds the values up to j - 1
+#pragma unroll
+                for (int t = 0; t < NC; ++t)
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) o[t][d] *= alpha[t];
             }
         };
         static_assert(NM == 8 || NM == 16 || NM == 20, "slots written out");
 
-        load_k(t_first);
-        load_v(t_first);
-        store_k(0);
+        Pages p0 = pages_of(0);                                  // of tiles i .. i + 3
+        load_k(t_first, p0);
+        load_v(t_first, p0);
+        Pages p1 = pages_of(1);
+        store_k(0, p0);
         store_v(t_first, 0);
-        load_k(t_first + 1);
-        store_k(1);
+        load_k(t_first + 1, p1);
+        Pages p2 = pages_of(2), p3;
+        store_k(1, p1);
         // the values "before the first" meet p = 0: zeros, since LDS may hold anything
         for (int x = tid; x < V_BUF / 16; x += NT) ((uint4*)(lds_v + V_BUF))[x] = make_uint4(0, 0, 0, 0);
         __syncthreads();
-        load_k(t_first + 2);
-        load_v(t_first + 1);
+        load_k(t_first + 2, p2);
+        load_v(t_first + 1, p1);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = 0.f;
+        for (int t = 0; t < NC; ++t) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-            s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*(const bf8v*)(lds_k + kat[ks]), q[ks], s, 0, 0, 0);
-        top = s[0];
+            for (int i = 0; i < 16; ++i) s_even[t][i] = 0.f;
 #pragma unroll
-        for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+            for (int ks = 0; ks < KS; ++ks)
+                s_even[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*(const bf8v*)(lds_k + kat[ks]), q[t][ks],
+                                                                    s_even[t], 0, 0, 0);
+            top[t] = s_even[t][0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) top[t] = fmaxf(top[t], s_even[t][i]);
+        }
         // tile i: buffers i & 1.  Between its two steps every wave is done with the keys of tile i
-        // and the values of tile i - 1, and their buffers take those of i + 2 and i + 1
+        // and the values of tile i - 1, and their buffers take those of i + 2 and i + 1.  Half of
+        // the waves stage before their step, half behind it: the two that share a SIMD then do
+        // not both leave its matrix unit idle at a time.
+        const bool early = WAVES < 8 || wave < WAVES / 2;
+        const auto stage = [&](int i, auto par) __attribute__((always_inline)) {
+            constexpr int P = decltype(par)::value;
+            store_k(P, p2);
+            store_v(t_first + i + 1, 1 - P);
+            p3 = pages_of(i + 3);
+            load_k(t_first + i + 3, p3);
+            load_v(t_first + i + 2, p2);
+        };
         const auto tile_pair = [&](int i, auto par) __attribute__((always_inline)) {
             constexpr int P = decltype(par)::value;
-            step(2 * i, StageId<P>{}, StageId<1>{}, StageId<1 - P>{}, StageId<1>{});
+            step(2 * i, p0.vs0, s_even, s_odd, p_odd, p_even, StageId<P>{}, StageId<1>{}, StageId<1 - P>{},
+                 StageId<1>{});
             __syncthreads();
-            store_k(P);
-            store_v(t_first + i + 1, 1 - P);
-            load_k(t_first + i + 3);
-            load_v(t_first + i + 2);
-            step(2 * i + 1, StageId<1 - P>{}, StageId<0>{}, StageId<P>{}, StageId<0>{});
+            if (early) stage(i, par);
+            step(2 * i + 1, p0.vs1, s_odd, s_even, p_even, p_odd, StageId<1 - P>{}, StageId<0>{}, StageId<P>{},
+                 StageId<0>{});
+            if (!early) stage(i, par);
+            p0 = p1;
+            p1 = p2;
+            p2 = p3;
         };
         for (int i = 0; i < n; i += 2) {
             tile_pair(i, StageId<0>{});
@@ -1027,48 +1114,54 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
         for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int d = 0; d < DT; ++d)
-                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const h8v*)(at + vat[2 + u] + d * 32 * V_ROW),
-                                                              __builtin_bit_cast(h8v, p[u]), o[d], 0, 0, 0);
+#pragma unroll
+                for (int t = 0; t < NC; ++t)
+                    o[t][d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const h8v*)(at + vat[2 + u] + d * 32 * V_ROW),
+                                                                     __builtin_bit_cast(h8v, p_odd[t][u]), o[t][d], 0, 0, 0);
     }
 
-    // results: lane half hh holds dims 32 d + 8 (i / 4) + 4 hh + i % 4 of its column
-    const float ll = half_sum(l) * 0x1p-15f;
-    if (!used) return;
-    if (splits == 1) {
-        const float rl = ll == 0.f ? 0.f : 0x1p-15f / ll;
-        const int64_t row = it.q0 + col / G;
-        const int head = h * G + col % G;
-        uint16_t* const out = a.out + (row * a.heads_q + head) * DV + 4 * hh;
+    // results: lane half hh holds dims 32 d + 8 (i / 4) + 4 hh + i % 4 of its columns
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
+    for (int t = 0; t < NC; ++t) {
+        const float ll = half_sum(l[t]) * 0x1p-7f;
+        const int x = (wave * NC + t) * 32 + lr, col = c0 + x;
+        if (col >= it.cols) continue;
+        if (splits == 1) {
+            const float rl = ll == 0.f ? 0.f : 0x1p-7f / ll;
+            const int64_t row = it.q0 + col / G;
+            const int head = h * G + col % G;
+            uint16_t* const out = a.out + (row * a.heads_q + head) * DV + 4 * hh;
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-                *(uint2*)(out + 32 * d + 8 * y) =
-                    make_uint2(pack_bf16x2(o[d][4 * y] * rl, o[d][4 * y + 1] * rl),
-                               pack_bf16x2(o[d][4 * y + 2] * rl, o[d][4 * y + 3] * rl));
-        if (a.lse && hh == 0)
-            a.lse[row * a.heads_q + head] = ll == 0.f ? neg_inf() : (m + __builtin_log2f(ll)) * kLn2;
-    } else {
-        const int64_t slot = (int64_t)blockIdx.x * CB + wave * 32 + lr;
-        float* const ws = a.ws + slot * DV + 4 * hh;
+            for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
+                for (int y = 0; y < 4; ++y)
+                    *(uint2*)(out + 32 * d + 8 * y) =
+                        make_uint2(pack_bf16x2(o[t][d][4 * y] * rl, o[t][d][4 * y + 1] * rl),
+                                   pack_bf16x2(o[t][d][4 * y + 2] * rl, o[t][d][4 * y + 3] * rl));
+            if (a.lse && hh == 0)
+                a.lse[row * a.heads_q + head] = ll == 0.f ? neg_inf() : (m[t] + __builtin_log2f(ll)) * kLn2;
+        } else {
+            const int64_t slot = (int64_t)blockIdx.x * CB + x;
+            float* const ws = a.ws + slot * DV + 4 * hh;
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-                *(v4f*)(ws + 32 * d + 8 * y) =
-                    v4f{o[d][4 * y], o[d][4 * y + 1], o[d][4 * y + 2], o[d][4 * y + 3]} * 0x1p-15f;
-        if (hh == 0) {
-            float* const ml = a.ws + (int64_t)gridDim.x * CB * DV + slot * 2;
-            ml[0] = m;
-            ml[1] = ll;
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    *(v4f*)(ws + 32 * d + 8 * y) = v4f{o[t][d][4 * y], o[t][d][4 * y + 1], o[t][d][4 * y + 2],
+                                                       o[t][d][4 * y + 3]} * 0x1p-7f;
+            if (hh == 0) {
+                float* const ml = a.ws + (int64_t)gridDim.x * CB * DV + slot * 2;
+                ml[0] = m[t];
+                ml[1] = ll;
+            }
         }
     }
 }
 
 // Adds the parts of a split launch, in token order: one row per DV / 4 lanes.
-template <int DV, int WAVES>
+template <int DV, int CB>
 __global__ __launch_bounds__(kAttnThreads) void attn_block_join_kernel(AttnArgs a, int blocks, int splits) {
-    constexpr int CB = 32 * WAVES, L = DV / 4, ROWS = kAttnThreads / L;
+    constexpr int L = DV / 4, ROWS = kAttnThreads / L;
     const int tid = threadIdx.x, d4 = tid % L * 4;
     const int G = a.heads_q / a.heads_kv;
     const int64_t row = (int64_t)blockIdx.x * ROWS + tid / L;   // of T * heads_q
@@ -1168,16 +1261,16 @@ static hipError_t split_launch(const AttnArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int DK, int DV, int WAVES>
+template <int DK, int DV, int WAVES, int NC>
 static hipError_t block_launch(const AttnArgs& a, const BlockPlan& p, hipStream_t stream) {
     // as many parts as the workspace holds
-    const int64_t hold = a.ws ? (int64_t)(a.ws_bytes / (32 * WAVES * (DV + 2) * sizeof(float))) : 0;
+    const int64_t hold = a.ws ? (int64_t)(a.ws_bytes / (32 * NC * WAVES * (DV + 2) * sizeof(float))) : 0;
     const int64_t splits = std::max<int64_t>(1, std::min(p.splits, hold / (p.blocks * a.heads_kv)));
     const unsigned grid = (unsigned)(p.blocks * a.heads_kv * splits);
-    attn_block_kernel<DK, DV, WAVES><<<dim3(grid), dim3(64 * WAVES), 0, stream>>>(a, (int)p.blocks, (int)splits);
+    attn_block_kernel<DK, DV, WAVES, NC><<<dim3(grid), dim3(64 * WAVES), 0, stream>>>(a, (int)p.blocks, (int)splits);
     if (splits > 1) {
         const int64_t rows = a.T * a.heads_q, per = kAttnThreads / (DV / 4);
-        attn_block_join_kernel<DV, WAVES><<<dim3((unsigned)((rows + per - 1) / per)), dim3(kAttnThreads), 0, stream>>>(
+        attn_block_join_kernel<DV, 32 * NC * WAVES><<<dim3((unsigned)((rows + per - 1) / per)), dim3(kAttnThreads), 0, stream>>>(
             a, (int)p.blocks, (int)splits);
     }
     return hipGetLastError();
@@ -1190,7 +1283,7 @@ static hipError_t attn_launch(const AttnArgs& a, hipStream_t stream) {
                : a.log_b == 6 ? split_launch<DK, DV, 64>(a, stream)
                               : split_launch<DK, DV, 128>(a, stream);
     const BlockPlan p = block_plan(a.T, a.R, a.heads_q, a.heads_kv);
-    return p.waves == 4 ? block_launch<DK, DV, 4>(a, p, stream) : block_launch<DK, DV, 8>(a, p, stream);
+    return p.waves == 4 ? block_launch<DK, DV, 4, 1>(a, p, stream) : block_launch<DK, DV, 8, 1>(a, p, stream);
 }
 
 hipError_t launch_attn_paged(const AttnArgs& a, int32_t dk, int32_t dv, hipStream_t stream) {
