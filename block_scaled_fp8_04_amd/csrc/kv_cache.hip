@@ -196,6 +196,12 @@ hipError_t launch_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int6
 // power-of-two form): x / s is exact and below 448, and re-encoding an older
 // code by old / s is exact but for values that fall under the format's normal
 // range, so a page's growing scale does not wear its codes down.
+//
+// Bound by the loads' latency more than by their bytes: 13240 tokens x 8 heads of 128 + 128
+// elements (54 MB read, 27 MB written) take 25.6 us, 3.2 TB/s, 64 tokens x 8 heads 5.0 us.  What
+// bought the most: the row slices of a page held in registers sized for its page size, so that
+// four workgroups share a compute unit (33.5 us with registers for 128 tokens throughout), and
+// values turned by words instead of bytes (121 us).  512 threads: 28.9 and 5.6 us.
 constexpr int kAppendThreads = 256;
 
 __device__ __forceinline__ float append_scale(float amax) {
@@ -292,21 +298,20 @@ __device__ __forceinline__ uint4 reencode16(const uint4 v, float ratio, int keep
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-template <int DK, int DV, bool kVec>
+template <int DK, int DV, int B, bool kVec>
 __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(
     const uint16_t* __restrict__ k, int64_t k_ts, int64_t k_hs, const uint16_t* __restrict__ v,
     int64_t v_ts, int64_t v_hs, const int32_t* __restrict__ slot_map, int64_t T, int run,
     uint8_t* __restrict__ k_cache, float* __restrict__ k_scales, uint8_t* __restrict__ v_cache,
-    float* __restrict__ v_scales, int64_t slots, int log_b, int H) {
+    float* __restrict__ v_scales, int64_t slots, int H) {
     constexpr int KC = DK / 8, VC = DV / 8;                       // 8-element chunks per row
-    constexpr int KP = (128 * KC + kAppendThreads - 1) / kAppendThreads;
-    constexpr int VP = (32 * VC + kAppendThreads - 1) / kAppendThreads;   // items of 4 slots, 8 dims
-    const int B = 1 << log_b;
-    extern __shared__ uint32_t vt[];                               // [DV][B + 4] bytes
-    const int vrow = B + 4;
+    constexpr int KP = (B * KC + kAppendThreads - 1) / kAppendThreads;
+    constexpr int VP = (B / 4 * VC + kAppendThreads - 1) / kAppendThreads;   // items of 4 slots, 8 dims
+    constexpr int vrow = B + 4;
+    __shared__ uint32_t vt[DV * vrow / 4];                         // [DV][B + 4] bytes
     __shared__ uint32_t red[2][kAppendThreads / 64];
-    __shared__ uint32_t poison[128];
-    __shared__ int32_t token[128];                                 // of each new slot
+    __shared__ uint32_t poison[B];
+    __shared__ int32_t token[B];                                   // of each new slot
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int h = blockIdx.y;
     k += h * k_hs;
@@ -329,14 +334,14 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(
     for (uint64_t leaders = __ballot(leads); leaders; leaders &= leaders - 1) {
         const int which = __ffsll((unsigned long long)leaders) - 1;
         const int64_t t = t0 + which;
-        const int64_t s0 = __shfl(mine, which);
+        const uint32_t s0 = __shfl(mine, which);
         const int off = (int)(s0 & (B - 1));
-        const int64_t page = s0 >> log_b;
+        const int64_t page = s0 / B;
         uint8_t* const kc = k_cache + (page * H + h) * ((int64_t)B * DK);
         uint8_t* const vc = v_cache + (page * H + h) * ((int64_t)B * DV);
 
         __syncthreads();                                           // the last page's LDS reads
-        if (tid < 128) poison[tid] = 0;
+        if (tid < B) poison[tid] = 0;
         // the tokens that follow in ascending slots of this page
         int n = 0;
         for (int64_t from = t; off + n < B;) {
@@ -501,21 +506,20 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(
     }
 }
 
-template <int DK, int DV, bool kVec>
+template <int DK, int DV, int B, bool kVec>
 static hipError_t append_launch(const void* k, int64_t k_ts, int64_t k_hs, const void* v,
                                 int64_t v_ts, int64_t v_hs, const int32_t* slot_map, int64_t T,
                                 void* k_cache, float* k_scales, void* v_cache, float* v_scales,
-                                int64_t pages, int32_t page, int32_t heads, hipStream_t stream) {
+                                int64_t pages, int32_t heads, hipStream_t stream) {
     // tokens per workgroup: one, until the launch would pass 2048 workgroups.  13240 tokens x 8
-    // heads take 44.8 us so, 46.2 with up to 4096 workgroups, 74.8 with 8192 and 56.6 with 16384.
+    // heads: 41.3 us so, 40.5 with up to 4096, 69.5 with 8192 (all before the page size was a
+    // constant of the kernel).
     int run = 1;
     while (run < 64 && (T + run - 1) / run * heads > 2048) run *= 2;
     const dim3 grid((unsigned)((T + run - 1) / run), (unsigned)heads);
-    const size_t lds = (size_t)DV * (page + 4);
-    kv_append_kernel<DK, DV, kVec><<<grid, dim3(kAppendThreads), lds, stream>>>(
+    kv_append_kernel<DK, DV, B, kVec><<<grid, dim3(kAppendThreads), 0, stream>>>(
         (const uint16_t*)k, k_ts, k_hs, (const uint16_t*)v, v_ts, v_hs, slot_map, T, run,
-        (uint8_t*)k_cache, k_scales, (uint8_t*)v_cache, v_scales, pages * page,
-        __builtin_ctz(page), heads);
+        (uint8_t*)k_cache, k_scales, (uint8_t*)v_cache, v_scales, pages * B, heads);
     return hipGetLastError();
 }
 
@@ -525,17 +529,19 @@ hipError_t launch_kv_append(const void* k, int64_t k_ts, int64_t k_hs, const voi
                             int32_t page, int32_t heads, int32_t dk, int32_t dv,
                             hipStream_t stream) {
     const bool vec = ((uintptr_t)k | (uintptr_t)v) % 16 == 0 && ((k_ts | k_hs | v_ts | v_hs) % 8) == 0;
-#define BFP8_APPEND(DK, DV)                                                                        \
-    if (dk == DK && dv == DV)                                                                      \
-        return vec ? append_launch<DK, DV, true>(k, k_ts, k_hs, v, v_ts, v_hs, slot_map, T,        \
-                                                 k_cache, k_scales, v_cache, v_scales, pages,      \
-                                                 page, heads, stream)                              \
-                   : append_launch<DK, DV, false>(k, k_ts, k_hs, v, v_ts, v_hs, slot_map, T,       \
-                                                  k_cache, k_scales, v_cache, v_scales, pages,     \
-                                                  page, heads, stream);
-    BFP8_APPEND(64, 64)
-    BFP8_APPEND(128, 128)
-    BFP8_APPEND(192, 128)
+#define BFP8_APPEND(DK, DV, B)                                                                     \
+    if (dk == DK && dv == DV && page == B)                                                         \
+        return vec ? append_launch<DK, DV, B, true>(k, k_ts, k_hs, v, v_ts, v_hs, slot_map, T,     \
+                                                    k_cache, k_scales, v_cache, v_scales, pages,   \
+                                                    heads, stream)                                 \
+                   : append_launch<DK, DV, B, false>(k, k_ts, k_hs, v, v_ts, v_hs, slot_map, T,    \
+                                                     k_cache, k_scales, v_cache, v_scales, pages,  \
+                                                     heads, stream);
+#define BFP8_APPEND_PAGES(DK, DV) BFP8_APPEND(DK, DV, 32) BFP8_APPEND(DK, DV, 64) BFP8_APPEND(DK, DV, 128)
+    BFP8_APPEND_PAGES(64, 64)
+    BFP8_APPEND_PAGES(128, 128)
+    BFP8_APPEND_PAGES(192, 128)
+#undef BFP8_APPEND_PAGES
 #undef BFP8_APPEND
     return hipErrorInvalidValue;
 }
