@@ -68,8 +68,11 @@ __device__ __forceinline__ bf8v load_q8(const uint16_t* p, bool vec, bool negate
         for (int j = 0; j < 4; ++j) w[j] = (uint32_t)p[2 * j] | ((uint32_t)p[2 * j + 1] << 16);
         x = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    const uint32_t f = negate ? 0x80008000u : 0u;
-    return __builtin_bit_cast(bf8v, make_uint4(x.x ^ f, x.y ^ f, x.z ^ f, x.w ^ f));
+    if (negate) {
+        asm volatile("");                                       // a branch: otherwise the load is waited for here
+        x = make_uint4(x.x ^ 0x80008000u, x.y ^ 0x80008000u, x.z ^ 0x80008000u, x.w ^ 0x80008000u);
+    }
+    return __builtin_bit_cast(bf8v, x);
 }
 
 // Reads through the scalar cache (uniform addresses): page numbers and scales.
@@ -82,25 +85,37 @@ __device__ __forceinline__ int64_t uniform(int64_t x) {
            (int64_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32;
 }
 
-// What an item's columns are: shared by the three kernels.  kUniform: r is the same for the wave,
-// and so is then all of this, in scalar registers.
+// x / y for 0 <= x < 2^52, 0 < y, a quotient below 2^31: by the reciprocal in 64-bit floating point,
+// refined twice, which is off by one at most.  The compiler's 64-bit division takes a kilobyte of
+// code, and what a short call spends its time on is code that it runs for the first time.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+    const double d = (double)y;
+    double inv = __builtin_amdgcn_rcp(d);
+    inv = __builtin_fma(__builtin_fma(-d, inv, 1.0), inv, inv);
+    inv = __builtin_fma(__builtin_fma(-d, inv, 1.0), inv, inv);
+    int64_t q = (uint32_t)((double)x * inv);
+    const int64_t left = x - q * y;
+    if (left < 0) q -= 1;
+    if (left >= y) q += 1;
+    return q;
+}
+
+// What an item's columns are: shared by all kernels.
 struct Item {
     int64_t q0;
     int n, cols, kv_len, G;
-    template <bool kUniform>
-    static __device__ __forceinline__ int32_t at(const int32_t* p, int i) {
-        return kUniform ? ((scalar_i32)(uintptr_t)p)[i] : p[i];
-    }
-    template <bool kUniform>
-    static __device__ __forceinline__ Item of(const AttnArgs& a, int r) {
+    static __device__ __forceinline__ Item of(const AttnArgs& a, int from, int to, int kv_len) {
         Item it;
         it.G = a.heads_q / a.heads_kv;
-        it.q0 = min(max((int64_t)at<kUniform>(a.q_offsets, r), (int64_t)0), a.T);
-        const int64_t q1 = min(max((int64_t)at<kUniform>(a.q_offsets, r + 1), it.q0), a.T);
+        it.q0 = min(max((int64_t)from, (int64_t)0), a.T);
+        const int64_t q1 = min(max((int64_t)to, it.q0), a.T);
         it.n = (int)(q1 - it.q0);
         it.cols = (int)min((int64_t)it.n, a.max_new) * it.G;
-        it.kv_len = (int)min(max((int64_t)at<kUniform>(a.kv_lens, r), (int64_t)0), a.width << a.log_b);
+        it.kv_len = (int)min(max((int64_t)kv_len, (int64_t)0), a.width << a.log_b);
         return it;
+    }
+    static __device__ __forceinline__ Item of(const AttnArgs& a, int r) {
+        return of(a, a.q_offsets[r], a.q_offsets[r + 1], a.kv_lens[r]);
     }
     // tokens that column c sees
     __device__ __forceinline__ int limit(int c) const {
@@ -110,6 +125,34 @@ struct Item {
         return a.q + (q0 + c / G) * a.q_ts + (int64_t)(h * G + c % G) * a.q_hs;
     }
 };
+
+// 64 consecutive requests, one per lane: what a workgroup has to know of the requests it meets,
+// read at once.  Reads that follow one another, each for the next one's address, are what a short
+// call spends its time on.
+struct Requests {
+    int base;                                        // the first one
+    int tiles0, tiles1, q0, q1, kv_len;              // of request base + lane
+    __device__ __forceinline__ void load(const AttnArgs& a, int from) {
+        base = from;
+        const int r = min(base + (int)(threadIdx.x & 63), a.R - 1);
+        tiles0 = a.tile_offsets[r];
+        tiles1 = a.tile_offsets[r + 1];
+        q0 = a.q_offsets[r];
+        q1 = a.q_offsets[r + 1];
+        kv_len = a.kv_lens[r];
+    }
+    // of request r, in scalar registers
+    __device__ __forceinline__ int tiles_from(int r) const { return __builtin_amdgcn_readlane(tiles0, r - base); }
+    __device__ __forceinline__ int tiles_to(int r) const { return __builtin_amdgcn_readlane(tiles1, r - base); }
+    __device__ __forceinline__ Item item(const AttnArgs& a, int r) const {
+        return Item::of(a, __builtin_amdgcn_readlane(q0, r - base), __builtin_amdgcn_readlane(q1, r - base),
+                        __builtin_amdgcn_readlane(kv_len, r - base));
+    }
+};
+static_assert(kKvMaxRequests <= 64 * 64, "a request is found in two steps of 64");
+
+// How many of the lanes' conditions hold, from the first lane on, less one; at least 0.
+__device__ __forceinline__ int last_of(bool holds) { return max(__popcll(__ballot(holds)) - 1, 0); }
 
 __device__ __forceinline__ bool q_vec(const AttnArgs& a) {
     return ((uintptr_t)a.q % 16) == 0 && ((a.q_ts | a.q_hs) % 8) == 0;
@@ -469,16 +512,21 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, int64_t row, int he
 // item by item; an item that lies within one workgroup is finished there, the others leave
 // partial sums (at most two of them per workgroup: its first and its last item) that
 // attn_join_kernel adds in token order.
-constexpr int kSplitMinUnits = kAttnWaves;    // tiles per workgroup, at least one for each wave
+
+// Workgroups: as many as the CUs hold at once (16 KB of LDS a wave at 128/128, 20 at 192/128: two
+// workgroups a CU; four at 64/64).  768 or 1024 at 128/128 are slower: 86 and 82 us against 77 (64
+// requests, 180k tokens).
+constexpr int split_groups(int dv) { return dv == 64 ? 1024 : 512; }
 
 struct SplitPlan {
     int64_t units;      // tiles of all items
     int64_t per;        // tiles per workgroup
 };
 
-__device__ __forceinline__ SplitPlan split_plan(const AttnArgs& a, int col_tiles, int groups) {
-    const int64_t units = (int64_t)max(a.tile_offsets[a.R], 0) * a.heads_kv * col_tiles;
-    return {units, max((units + groups - 1) / groups, (int64_t)kSplitMinUnits)};
+template <int DV>
+__device__ __forceinline__ SplitPlan split_plan(const AttnArgs& a, int tiles, int col_tiles) {
+    const int64_t units = (int64_t)max(tiles, 0) * a.heads_kv * col_tiles;
+    return {units, max((units + split_groups(DV) - 1) / split_groups(DV), (int64_t)1)};
 }
 
 // One workgroup per (request, KV head, 16 query columns): its waves take every fourth tile.
@@ -489,18 +537,19 @@ __global__ __launch_bounds__(kAttnThreads) void attn_item_kernel(AttnArgs a, int
     __shared__ __attribute__((aligned(1024))) uint8_t lds_v[kAttnWaves * W::V_BYTES];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int64_t item = blockIdx.x;
+    uint32_t item = blockIdx.x;
     const int ct = (int)(item % col_tiles);
     item /= col_tiles;
     const int h = (int)(item % a.heads_kv);
-    const Item it = Item::of<true>(a, (int)(item / a.heads_kv));
+    const int r = __builtin_amdgcn_readfirstlane((int)(item / a.heads_kv));
+    const Item it = Item::of(a, r);
     if (ct * kCols >= it.cols) return;
     const int col = ct * kCols + (lane & 15);
     const bool used = col < it.cols;
     W w;
     w.load_q(used ? it.row(a, h, col) : nullptr, q_vec(a), a.scale < 0.f, lane >> 4);
     Segment seg;
-    seg.r = (int)(item / a.heads_kv);
+    seg.r = r;
     seg.h = h;
     seg.ct = ct;
     seg.t0 = 0;
@@ -524,29 +573,28 @@ __global__ __launch_bounds__(kAttnThreads) void attn_split_kernel(AttnArgs a, in
     __shared__ __attribute__((aligned(1024))) uint8_t lds_v[kAttnWaves * W::V_BYTES];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const SplitPlan sp = split_plan(a, col_tiles, gridDim.x);
-    int64_t u = (int64_t)blockIdx.x * uniform(sp.per);
-    const int64_t end = min(u + uniform(sp.per), uniform(sp.units));
+    Requests reqs;
+    reqs.load(a, 0);
+    const int each64 = a.tile_offsets[min(lane * 64, a.R)];
+    const SplitPlan sp = split_plan<DV>(a, __builtin_amdgcn_readfirstlane(a.tile_offsets[a.R]), col_tiles);
+    int64_t u = (int64_t)blockIdx.x * sp.per;
+    const int64_t end = min(u + sp.per, sp.units);
     if (u >= end) return;
     const int64_t items = (int64_t)a.heads_kv * col_tiles;   // of one request
-    // the request of the first unit: how many offsets lie at or below it, counted by 64 lanes on
-    // every 64th offset and then on the 64 behind the last of those
-    static_assert(kKvMaxRequests <= 64 * 64, "two steps");
-    const int64_t ut = uniform(u / items);
-    const int lo64 = __popcll(__ballot(lane * 64 < a.R && a.tile_offsets[min(lane * 64, a.R)] <= ut)) - 1;
-    const int at = max(lo64, 0) * 64 + lane;
-    const int lo = max(lo64, 0) * 64 +
-                   max(__popcll(__ballot(at < a.R && a.tile_offsets[min(at, a.R)] <= ut)) - 1, 0);
-    const scalar_i32 offs = (scalar_i32)(uintptr_t)a.tile_offsets;
-    int r = __builtin_amdgcn_readfirstlane(lo);
+    // the request of the first unit
+    const int64_t ut = quotient(u, items);
+    const int from = last_of(lane * 64 < a.R && each64 <= ut) * 64;
+    if (from > 0) reqs.load(a, from);
+    int r = __builtin_amdgcn_readfirstlane(from + last_of(from + lane < a.R && reqs.tiles0 <= ut));
     // the workgroup's next run of tiles, from unit u on
-    const auto advance = [&](Segment& s) {
+    const auto advance = [&](Segment& s, Item& it) {
         for (; r < a.R && u < end; ++r) {
-            const int64_t f = offs[r];
-            const int nt = (int)min(max((int64_t)offs[r + 1] - f, (int64_t)0), (int64_t)1 << 24);
+            if (r - reqs.base >= 64) reqs.load(a, r);
+            const int64_t f = reqs.tiles_from(r);
+            const int nt = (int)min(max((int64_t)reqs.tiles_to(r) - f, (int64_t)0), (int64_t)1 << 24);
             const int64_t local = max(u - f * items, (int64_t)0);
             if (nt <= 0 || local >= (int64_t)nt * items) continue;
-            const int item = __builtin_amdgcn_readfirstlane((int)(local / nt));
+            const int item = __builtin_amdgcn_readfirstlane((int)quotient(local, nt));
             const int tile0 = (int)(local - (int64_t)item * nt);
             const int count = (int)min((int64_t)(nt - tile0), end - u);
             u += count;
@@ -556,6 +604,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_split_kernel(AttnArgs a, in
             s.t0 = tile0 * (kKvTile / TT);
             s.t1 = (tile0 + count) * (kKvTile / TT);
             s.whole = count == nt;
+            it = reqs.item(a, r);
             return true;
         }
         return false;
@@ -564,12 +613,12 @@ __global__ __launch_bounds__(kAttnThreads) void attn_split_kernel(AttnArgs a, in
     int64_t page[W::NP] = {};                                  // of the keys that are on their way
     float ks[W::NP] = {}, vs[W::NP] = {};
     Segment cur, next;
-    bool valid = advance(cur);
-    Item it = Item::of<true>(a, valid ? cur.r : 0);
+    Item it = {}, nit;
+    bool valid = advance(cur, it);
     while (valid) {
         next = cur;                                             // defined, and inside the pool, if there is none
-        const bool has = advance(next);
-        const Item nit = Item::of<true>(a, has ? next.r : 0);
+        nit = it;
+        const bool has = advance(next, nit);
         W w;
         const int col = cur.ct * kCols + (lane & 15);
         const bool used = col < it.cols;
@@ -610,7 +659,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_split_kernel(AttnArgs a, in
                         *(v4f*)(ws + 64 * j) = v4f{part[4 * j], part[4 * j + 1], part[4 * j + 2],
                                                    part[4 * j + 3]};
                     if (od == 0) {
-                        float* const ml = a.ws + (int64_t)gridDim.x * 2 * kCols * DV + slot * 2;
+                        float* const ml = a.ws + (int64_t)split_groups(DV) * 2 * kCols * DV + slot * 2;
                         ml[0] = m;
                         ml[1] = l;
                     }
@@ -625,82 +674,73 @@ __global__ __launch_bounds__(kAttnThreads) void attn_split_kernel(AttnArgs a, in
     wait_vmcnt<0>();                                            // no load outlives its LDS
 }
 
+// Partial sums of one row, or of a strand of it: O, l and the maximum they refer to.
+struct Part {
+    v4f acc = {0.f, 0.f, 0.f, 0.f};
+    float m = neg_inf(), l = 0.f;
+    __device__ __forceinline__ void add(const v4f& v, float mw, float lw) {
+        const float top = fmaxf(m, mw);
+        const float f0 = m == top ? 1.f : __builtin_amdgcn_exp2f(m - top);
+        const float f1 = mw == top ? 1.f : __builtin_amdgcn_exp2f(mw - top);
+        m = top;
+        l = __builtin_fmaf(lw, f1, l * f0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(v[i], f1, acc[i] * f0);
+    }
+    __device__ __forceinline__ void store(const AttnArgs& a, int64_t row, int dv, int d4) const {
+        const float rl = l == 0.f ? 0.f : 1.0f / l;
+        *(uint2*)(a.out + row * dv + d4) =
+            make_uint2(pack_bf16x2(acc[0] * rl, acc[1] * rl), pack_bf16x2(acc[2] * rl, acc[3] * rl));
+        if (a.lse && d4 == 0) a.lse[row] = l == 0.f ? neg_inf() : (m + __builtin_log2f(l)) * kLn2;
+    }
+};
+
 // Adds the partial sums of the workgroups that shared an item, one row (item column) by STRANDS
 // strands of DV / 4 lanes each: every strand takes its workgroups in token order, then the strands
 // are added in order.  Rows of a request without tokens get their zeros here.
-//
-// Where items are many, an item has few parts and two strands (128 wide: one wave) take a row;
-// where they are few, a workgroup of eight strands does.
 template <int DV, int STRANDS>
-__global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int col_tiles,
-                                                                 int groups, int max_cols) {
-    constexpr int L = DV / 4, ROWS = kAttnThreads / (L * STRANDS);
+__global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int col_tiles, int max_cols) {
+    constexpr int L = DV / 4, ROWS = kAttnThreads / (L * STRANDS), GROUPS = split_groups(DV);
     __shared__ float red[kAttnThreads / L][DV + 4];
-    __shared__ float red_l[kAttnThreads / L];
+    __shared__ float red_m[kAttnThreads / L], red_l[kAttnThreads / L];
     const int tid = threadIdx.x, strand = tid / L % STRANDS, d4 = tid % L * 4;
-    int64_t x = (int64_t)blockIdx.x * ROWS + tid / (L * STRANDS);
-    const int col = (int)(x % max_cols);
-    x /= max_cols;
-    const int h = (int)(x % a.heads_kv);
-    const int r = (int)min(x / a.heads_kv, (int64_t)a.R - 1);
-    const Item it = Item::of<false>(a, r);
-    const bool live = x / a.heads_kv < a.R && col < it.cols;
-    const int ct = col / kCols;
-    const int64_t items = (int64_t)a.heads_kv * col_tiles;
-    const int64_t t0 = max(a.tile_offsets[r], 0), nt = (int64_t)a.tile_offsets[r + 1] - t0;
-    const int64_t row = it.q0 + col / it.G;
-    const int head = h * it.G + col % it.G;
-    const SplitPlan sp = split_plan(a, col_tiles, groups);
-    const int64_t begin = t0 * items + ((int64_t)h * col_tiles + ct) * nt;
-    const int wa = (int)min(begin / sp.per, (int64_t)groups);
-    const int wb = (int)min((begin + nt - 1) / sp.per, (int64_t)groups - 1);
+    const int64_t x = (int64_t)blockIdx.x * ROWS + tid / (L * STRANDS);
+    const int64_t rh = quotient(x, max_cols);                   // request and KV head
+    const int col = (int)(x - rh * max_cols);
+    const int64_t rq = quotient(rh, a.heads_kv);
+    const int h = (int)(rh - rq * a.heads_kv);
+    const int r = (int)min(rq, (int64_t)a.R - 1);
+    const int tiles = a.tile_offsets[a.R], from = a.tile_offsets[r], to = a.tile_offsets[r + 1];
+    const Item it = Item::of(a, r);
+    const bool live = rq < a.R && col < it.cols;
+    const int64_t t0 = max(from, 0), nt = (int64_t)to - t0;
+    const int64_t row = (it.q0 + col / it.G) * a.heads_q + h * it.G + col % it.G;
+    const SplitPlan sp = split_plan<DV>(a, tiles, col_tiles);
+    const int64_t begin = t0 * a.heads_kv * col_tiles + ((int64_t)h * col_tiles + col / kCols) * nt;
+    const int wa = (int)min(quotient(begin, sp.per), (int64_t)GROUPS);
+    const int wb = (int)min(quotient(begin + max(nt, (int64_t)1) - 1, sp.per), (int64_t)GROUPS - 1);
     const bool joins = live && nt > 0 && wa < wb;               // else finished by one workgroup
-    const auto slot_of = [&](int w) {
-        return ((int64_t)w * 2 + (w * sp.per >= begin ? 0 : 1)) * kCols + col % kCols;
-    };
-    const float* const ml = a.ws + (int64_t)groups * 2 * kCols * DV;
-    float m = neg_inf(), l = 0.f;
-    v4f acc = {0.f, 0.f, 0.f, 0.f};
+    Part part;
     if (joins) {
-        // the row's lanes (64, or all 256 of the workgroup's waves alike) look at every part's m
-        for (int w = wa + (tid & 63); w <= wb; w += 64) m = fmaxf(m, ml[slot_of(w) * 2]);
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-    if (joins) {
+        const float* const ml = a.ws + (int64_t)GROUPS * 2 * kCols * DV;
 #pragma unroll 4
         for (int w = wa + strand; w <= wb; w += STRANDS) {
-            const int64_t slot = slot_of(w);
-            const float mw = ml[slot * 2], lw = ml[slot * 2 + 1];
-            const v4f v = *(const v4f*)(a.ws + slot * DV + d4);
-            const bool saw = mw != neg_inf() || lw != 0.f;      // otherwise its sums are zeros
-            const float f = saw ? __builtin_amdgcn_exp2f(mw - m) : 0.f;
-            l = __builtin_fmaf(lw, f, l);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(v[i], f, acc[i]);
+            const int64_t slot = ((int64_t)w * 2 + (w * sp.per >= begin ? 0 : 1)) * kCols + col % kCols;
+            const float2 mw = *(const float2*)(ml + slot * 2);
+            part.add(*(const v4f*)(a.ws + slot * DV + d4), mw.x, mw.y);
         }
     }
     const int mine = tid / L;
-    *(v4f*)&red[mine][d4] = acc;
-    if (tid % L == 0) red_l[mine] = l;
-    __syncthreads();
-    if (strand != 0 || !live) return;
-    uint16_t* const out = a.out + (row * a.heads_q + head) * DV + d4;
-    if (nt <= 0) {
-        *(uint2*)out = make_uint2(0, 0);
-        if (a.lse && d4 == 0) a.lse[row * a.heads_q + head] = neg_inf();
-    } else if (joins) {
-#pragma unroll
-        for (int i = 1; i < STRANDS; ++i) {
-            l += red_l[mine + i];
-            acc += *(const v4f*)&red[mine + i][d4];
-        }
-        const float rl = l == 0.f ? 0.f : 1.0f / l;
-        *(uint2*)out =
-            make_uint2(pack_bf16x2(acc[0] * rl, acc[1] * rl), pack_bf16x2(acc[2] * rl, acc[3] * rl));
-        if (a.lse && d4 == 0)
-            a.lse[row * a.heads_q + head] = l == 0.f ? neg_inf() : (m + __builtin_log2f(l)) * kLn2;
+    *(v4f*)&red[mine][d4] = part.acc;
+    if (tid % L == 0) {
+        red_m[mine] = part.m;
+        red_l[mine] = part.l;
     }
+    __syncthreads();
+    if (strand != 0 || !live || (nt > 0 && !joins)) return;
+#pragma unroll
+    for (int i = 1; i < STRANDS; ++i) part.add(*(const v4f*)&red[mine + i][d4], red_m[mine + i], red_l[mine + i]);
+    part.store(a, row, DV, d4);
 }
 
 // ---------------------------------------------------------------- many query columns
@@ -731,6 +771,7 @@ typedef _Float16 h2v __attribute__((ext_vector_type(2)));
 constexpr int kBlockTile = 64;                // tokens in LDS at a time
 constexpr int kBlockSlots = 512;              // workgroups that a split launch aims at
 constexpr int kBlockMaxSplits = 16;
+constexpr int kPartTokens = 512;              // tokens that are not split further
 constexpr float kSlack = 8.f;
 
 __device__ __forceinline__ h8v widen8h(uint32_t w0, uint32_t w1) {
@@ -751,9 +792,79 @@ __device__ __forceinline__ float half_sum(float x) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-template <int DK, int DV, int WAVES, int NC>
-__global__ __launch_bounds__(WAVES * 64, 2 / NC) void attn_block_kernel(AttnArgs a, int blocks, int splits) {
-    constexpr int CB = 32 * NC * WAVES, NT = 64 * WAVES;        // columns and threads of a workgroup
+// Sum and maximum of the wave's values, in scalar registers.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ int dpp(int x) { return __builtin_amdgcn_update_dpp(0, x, kCtrl, kRows, 0xF, false); }
+template <class F>
+__device__ __forceinline__ int wave_reduce(int x, F f) {
+    x = f(x, dpp<0x111, 0xF>(x));                               // shifts within rows of 16 lanes
+    x = f(x, dpp<0x112, 0xF>(x));
+    x = f(x, dpp<0x114, 0xF>(x));
+    x = f(x, dpp<0x118, 0xF>(x));
+    x = f(x, dpp<0x142, 0xA>(x));                               // a row's last lane to the next row
+    x = f(x, dpp<0x143, 0xC>(x));                               // and to the upper two rows
+    return __builtin_amdgcn_readlane(x, 63);
+}
+// (of values that are not negative: lanes without a partner take 0)
+__device__ __forceinline__ int wave_sum(int x) { return wave_reduce(x, [](int a, int b) { return a + b; }); }
+__device__ __forceinline__ int wave_max(int x) { return wave_reduce(x, [](int a, int b) { return max(a, b); }); }
+
+// A block of cb columns of a launch.  Request r's blocks are numbered from q_offsets[r] * G / cb + r
+// on, where there is room for all of them.
+struct Block {
+    Item it;
+    int r, c0, seen;                                 // first column; tokens that the last column sees
+    __device__ __forceinline__ bool find(const AttnArgs& a, int b, int cb) {
+        const int lane = threadIdx.x & 63, G = a.heads_q / a.heads_kv;
+        const auto start = [&](int q, int r) {
+            return (int64_t)((uint64_t)min(max((int64_t)q, (int64_t)0), a.T) * G / cb) + r;
+        };
+        Requests reqs;
+        reqs.load(a, 0);
+        const int each64 = a.q_offsets[min(lane * 64, a.R)];
+        const int from = last_of(lane * 64 < a.R && start(each64, lane * 64) <= b) * 64;
+        if (from > 0) reqs.load(a, from);
+        r = __builtin_amdgcn_readfirstlane(
+            from + last_of(from + lane < a.R && start(reqs.q0, from + lane) <= b));
+        it = reqs.item(a, r);
+        c0 = (int)min(b - start((int)it.q0, r), (int64_t)1 << 22) * cb;
+        if (c0 < 0 || c0 >= it.cols) return false;
+        seen = it.limit(min(c0 + cb, it.cols) - 1);
+        return true;
+    }
+    // The block of this rank by the tokens that it sees, most first (in steps of a block's own
+    // tokens); one request per lane, so for R <= 64.
+    __device__ __forceinline__ bool ranked(const AttnArgs& a, int rank, int cb) {
+        const int lane = threadIdx.x & 63;
+        Requests reqs;
+        reqs.load(a, 0);
+        const Item mine = Item::of(a, reqs.q0, reqs.q1, reqs.kv_len);
+        // level of a block: the level of its request's first one, and one more for each further
+        const int count = lane < a.R ? (mine.cols + cb - 1) / cb : 0;
+        const int low = (int)((uint64_t)max(mine.kv_len - mine.n, 0) * mine.G / cb), high = low + count;
+        const auto above = [&](int level) { return wave_sum(min(max(high - level, 0), count)); };
+        if (above(0) <= rank) return false;
+        int level = 0;                               // the highest with more than `rank` blocks from it on
+        for (int step = 1 << (31 - __builtin_clz(wave_max(high) | 1)); step > 0; step >>= 1)
+            if (above(level + step) > rank) level += step;
+        const uint64_t here = __ballot(low <= level && level < high);
+        const int nth = rank - above(level + 1);
+        r = __ffsll((unsigned long long)__ballot((here >> lane & 1) &&
+                                                 __popcll(here & ((1ull << lane) - 1)) == nth)) - 1;
+        it = reqs.item(a, r);
+        c0 = (level - __builtin_amdgcn_readlane(low, r)) * cb;
+        seen = it.limit(min(c0 + cb, it.cols) - 1);
+        return true;
+    }
+    // workgroups that share its tokens
+    __device__ __forceinline__ int parts(int splits) const {
+        return min(splits, max((seen + kPartTokens - 1) / kPartTokens, 1));
+    }
+};
+
+template <int DK, int DV, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, int blocks, int splits) {
+    constexpr int CB = 32 * WAVES, NT = 64 * WAVES;        // columns and threads of a workgroup
     constexpr int KS = DK / 16, DT = DV / 32;        // steps of the products, 32-row tiles of O^T
     constexpr int K_CHUNKS = kBlockTile * DK / 16, V_CHUNKS = kBlockTile * DV / 16;
     constexpr int KCH = (K_CHUNKS + NT - 1) / NT, VCH = (V_CHUNKS + NT - 1) / NT;
@@ -765,55 +876,42 @@ __global__ __launch_bounds__(WAVES * 64, 2 / NC) void attn_block_kernel(AttnArgs
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int G = a.heads_q / a.heads_kv;
 
-    // block b of the launch: request r's blocks start at q_offsets[r] * G / CB + r, where there
-    // is room for all of them; the last ones, which see the most tokens, go first
+    // blocks that see the most tokens go first, for the last ones to end together: by rank, or by
+    // number from the last one down (many requests, or a split launch, whose parts all run at once)
     int idx = blockIdx.x;
     const int z = idx % splits;
     idx /= splits;
-    const int h = idx % a.heads_kv, b = blocks - 1 - idx / a.heads_kv;
-    const auto start_of = [&](int r) {
-        return (int64_t)min(max((int64_t)a.q_offsets[r], (int64_t)0), a.T) * G / CB + r;
-    };
-    int r = 0;
-    {
-        const int hi = __popcll(__ballot(lane * 64 < a.R && start_of(min(lane * 64, a.R)) <= b)) - 1;
-        const int at = max(hi, 0) * 64 + lane;
-        r = max(hi, 0) * 64 +
-            max(__popcll(__ballot(at < a.R && start_of(min(at, a.R)) <= b)) - 1, 0);
-        r = __builtin_amdgcn_readfirstlane(r);
-    }
-    const Item it = Item::of<true>(a, r);
-    const int c0 = __builtin_amdgcn_readfirstlane((int)min(b - start_of(r), (int64_t)1 << 22)) * CB;
-    if (c0 < 0 || c0 >= it.cols) return;
-    const int c1 = min(c0 + CB, it.cols) - 1;                   // last column
-    const int seen_by_all = it.limit(c0), seen = it.limit(c1);
-    const int tiles = (seen + kBlockTile - 1) / kBlockTile;
-    const int t_first = (int)((int64_t)tiles * z / splits), t_end = (int)((int64_t)tiles * (z + 1) / splits);
+    const int h = idx % a.heads_kv, nth = idx / a.heads_kv;
+    Block k;
+    if (!(a.R <= 64 && splits == 1 ? k.ranked(a, nth, CB) : k.find(a, blocks - 1 - nth, CB))) return;
+    const Item& it = k.it;
+    const int r = k.r, c0 = k.c0, parts = k.parts(splits);
+    if (z >= parts) return;
+    const int seen_by_all = it.limit(c0);
+    const int tiles = (k.seen + kBlockTile - 1) / kBlockTile;
+    static_assert(kBlockMaxSplits <= 32, "2^25 tiles at most, so 32 bits will do");
+    const int t_first = __builtin_amdgcn_readfirstlane(tiles * z / parts);
+    const int t_end = __builtin_amdgcn_readfirstlane(tiles * (z + 1) / parts);
     const int n = t_end - t_first;
     const int kv_len = it.kv_len, last = max(kv_len - 1, 0) >> a.log_b, B = 1 << a.log_b;
     const float c = exp2_scale(a);
 
-    // this lane's columns: 32 t + lr of the wave's
-    int limit[NC];
-    bf8v q[NC][KS];
-    v16f o[NC][DT];
-    float m[NC], l[NC];
+    bf8v q[KS];
+    v16f o[DT];
+    float m, l;
+    const int col = c0 + wave * 32 + lr;
+    const bool used = col < it.cols;
+    const int limit = used ? it.limit(col) : 0;
+    const uint16_t* const row = it.row(a, h, used ? col : c0);
+    const bool vec = q_vec(a), negate = a.scale < 0.f;
 #pragma unroll
-    for (int t = 0; t < NC; ++t) {
-        const int col = c0 + (wave * NC + t) * 32 + lr;
-        const bool used = col < it.cols;
-        limit[t] = used ? it.limit(col) : 0;
-        const uint16_t* const row = it.row(a, h, used ? col : c0);
-        const bool vec = q_vec(a), negate = a.scale < 0.f;
+    for (int ks = 0; ks < KS; ++ks) q[ks] = load_q8(row + 16 * ks + 8 * hh, vec, negate);
+    m = neg_inf();
+    l = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) q[t][ks] = load_q8(row + 16 * ks + 8 * hh, vec, negate);
-        m[t] = neg_inf();
-        l[t] = 0.f;
+    for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[t][d][i] = 0.f;
-    }
+        for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
 
     if (n > 0) {
         // staging: global codes of one tile in registers, widened into LDS later.  Page numbers and
@@ -835,7 +933,20 @@ __global__ __launch_bounds__(WAVES * 64, 2 / NC) void attn_block_kernel(AttnArgs
         entry = fetch_table(t_first);
         ks_l = fetch_scale(a.k_scales, entry);
         vs_l = fetch_scale(a.v_scales, entry);
-        // of tile t_first + i, for i = 0, 1, 2, ... in order
+        const auto pages_at = [&](Pages& x, int at) {
+            x.page0 = (int64_t)__builtin_amdgcn_readlane(entry, at) * a.heads_kv + h;
+            x.page1 = (int64_t)__builtin_amdgcn_readlane(entry, at + 1) * a.heads_kv + h;
+        };
+        const auto scales_at = [&](Pages& x, int at) {
+            const auto lane_of = [&](float x, int l) {
+                return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), l));
+            };
+            x.ks0 = lane_of(ks_l, at);
+            x.ks1 = lane_of(ks_l, at + 1);
+            x.vs0 = lane_of(vs_l, at);
+            x.vs1 = lane_of(vs_l, at + 1);
+        };
+        // of tile t_first + i, for i = 3, 4, 5, ... in order
         const auto pages_of = [&](int i) {
             const int at = 2 * i & 63;
             if (at == 0 && i > 0) {
@@ -848,19 +959,12 @@ __global__ __launch_bounds__(WAVES * 64, 2 / NC) void attn_block_kernel(AttnArgs
                 ks_n = fetch_scale(a.k_scales, entry_n);
                 vs_n = fetch_scale(a.v_scales, entry_n);
             }
-            const auto lane_of = [&](float x, int l) {
-                return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), l));
-            };
             Pages x;
-            x.page0 = (int64_t)__builtin_amdgcn_readlane(entry, at) * a.heads_kv + h;
-            x.page1 = (int64_t)__builtin_amdgcn_readlane(entry, at + 1) * a.heads_kv + h;
-            x.ks0 = lane_of(ks_l, at);
-            x.ks1 = lane_of(ks_l, at + 1);
-            x.vs0 = lane_of(vs_l, at);
-            x.vs1 = lane_of(vs_l, at + 1);
+            pages_at(x, at);
+            scales_at(x, at);
             return x;
         };
-        const auto load_k = [&](int tile, const Pages& pg) {
+        const auto load_k = [&](uint4 (&kr)[KCH], int tile, const Pages& pg) {
             const int base = min(tile, t_end - 1) * kBlockTile;
 #pragma unroll
             for (int e = 0; e < KCH; ++e) {
@@ -885,7 +989,7 @@ __global__ __launch_bounds__(WAVES * 64, 2 / NC) void attn_block_kernel(AttnArgs
         // a row's 16-byte chunks are permuted so that the rows that lanes read together lie in
         // different banks
         const auto k_swz = [](int row) { return DK == 128 ? (row & 15) : (row >> 1 & 7); };
-        const auto store_k = [&](int buf, const Pages& pg) {
+        const auto store_k = [&](const uint4 (&kr)[KCH], int buf, const Pages& pg) {
 #pragma unroll
             for (int e = 0; e < KCH; ++e) {
                 const int x = e * NT + tid, token = x / (DK / 16), at = x % (DK / 16);
@@ -919,23 +1023,23 @@ __global__ __launch_bounds__(WAVES * 64, 2 / NC) void attn_block_kernel(AttnArgs
         };
         // fragment places: K rows are tokens with bits 2 and 3 exchanged, V rows are lr + 32 d
         const int krow = (lr & 0x13) | (lr & 4) << 1 | (lr & 8) >> 1;
-        int kat[KS], vat[4];
+        constexpr int KA = DK == 128 ? 8 : 4;                    // k_swz takes 2 KA chunks: then it repeats
+        int kat[KA], vat[4];
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) kat[ks] = krow * K_ROW + (((2 * ks) ^ (k_swz(krow) ^ hh)) * 16);
+        for (int ks = 0; ks < KA; ++ks) kat[ks] = krow * K_ROW + (((2 * ks) ^ (k_swz(krow) ^ hh)) * 16);
 #pragma unroll
         for (int x = 0; x < 4; ++x) vat[x] = lr * V_ROW + (((2 * x) ^ ((lr >> 1 & 7) ^ hh)) * 16);
 
-        v16f s_even[NC], s_odd[NC];                              // logits of even and odd subtiles
-        uint4 p_even[NC][2], p_odd[NC][2];                       // and their p'
-        float top[NC];                                           // maximum of the current ones
-#pragma unroll
-        for (int t = 0; t < NC; ++t) p_odd[t][0] = p_odd[t][1] = make_uint4(0, 0, 0, 0);
+        v16f s_even, s_odd;                              // logits of even and odd subtiles
+        uint4 p_even[2], p_odd[2];                       // and their p'
+        float top;                                           // maximum of the current ones
+        p_odd[0] = p_odd[1] = make_uint4(0, 0, 0, 0);
         // one step: softmax of subtile j, logits of j + 1 (half KSUB of buffer KBUF) and their
         // maximum, values of j - 1 (half VSUB of buffer VBUF)
         constexpr int NM = KS + 2 * DT;                          // fragments, matrix instructions a column tile
         constexpr int AHEAD = 3;
-        const auto step = [&](int j, float vs, v16f (&s)[NC], v16f (&next)[NC], const uint4 (&p)[NC][2],
-                              uint4 (&p_new)[NC][2], auto kbuf_, auto ksub_, auto vbuf_,
+        const auto step = [&](int j, float vs, v16f& s, v16f& next, const uint4 (&p)[2],
+                              uint4 (&p_new)[2], auto kbuf_, auto ksub_, auto vbuf_,
                               auto vsub_) __attribute__((always_inline)) {
             constexpr int KBUF = decltype(kbuf_)::value, KSUB = decltype(ksub_)::value;
             constexpr int VBUF = decltype(vbuf_)::value, VSUB = decltype(vsub_)::value;
@@ -943,7 +1047,8 @@ __global__ __launch_bounds__(WAVES * 64, 2 / NC) void attn_block_kernel(AttnArgs
             const auto read = [&](auto y_) __attribute__((always_inline)) {
                 constexpr int Y = decltype(y_)::value;
                 if constexpr (Y < KS)
-                    ring[Y % (AHEAD + 1)] = *(const uint4*)(lds_k + kat[Y] + KBUF * K_BUF + KSUB * 32 * K_ROW);
+                    ring[Y % (AHEAD + 1)] = *(const uint4*)(lds_k + kat[Y % KA] + Y / KA * KA * 32 + KBUF * K_BUF +
+                                                           KSUB * 32 * K_ROW);
                 else if constexpr (Y < NM)
                     ring[Y % (AHEAD + 1)] = *(const uint4*)(lds_v + vat[2 * VSUB + (Y - KS) / DT] + VBUF * V_BUF +
                                                            (Y - KS) % DT * 32 * V_ROW);
@@ -954,78 +1059,68 @@ __global__ __launch_bounds__(WAVES * 64, 2 / NC) void attn_block_kernel(AttnArgs
             const int base = t_first * kBlockTile + 32 * j;
             if (base + 32 > seen_by_all) {
 #pragma unroll
-                for (int t = 0; t < NC; ++t) {
+                for (int i = 0; i < 16; ++i)
+                    if (base + 16 * (i >> 3) + 8 * hh + (i & 7) >= limit) s[i] = neg_inf();
+                top = s[0];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (base + 16 * (i >> 3) + 8 * hh + (i & 7) >= limit[t]) s[t][i] = neg_inf();
-                    top[t] = s[t][0];
-#pragma unroll
-                    for (int i = 1; i < 16; ++i) top[t] = fmaxf(top[t], s[t][i]);
-                }
+                for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
             }
             const int e = (int)(__float_as_uint(vs) >> 23) - 127;
-            float alpha[NC], add[NC], sum[NC][2], y_last[NC];
+            float alpha, add, sum[2], y_last;
             bool grew = false, far = false;
-#pragma unroll
-            for (int t = 0; t < NC; ++t) {
-                // the reference follows the maximum only where it would be passed by over 2^kSlack
-                const float x = __builtin_ceilf(half_max(top[t]) * c) + (float)e;
-                const float m_new = x > m[t] + kSlack ? x : m[t];
-                alpha[t] = m[t] == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(m[t] - m_new);
-                add[t] = m_new == neg_inf() ? 0.f : (float)(e + 15 - (int)kSlack) - m_new;
-                grew |= m_new != m[t];
-                far |= __builtin_fabsf(m_new) > 4194304.f && m_new != neg_inf();
-                m[t] = m_new;
-                sum[t][0] = sum[t][1] = 0.f;
-            }
+            // the reference follows the maximum only where it would be passed by over 2^kSlack
+            const float x = __builtin_ceilf(half_max(top) * c) + (float)e;
+            const float m_new = x > m + kSlack ? x : m;
+            alpha = m == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(m - m_new);
+            add = m_new == neg_inf() ? 0.f : (float)(e + 15 - (int)kSlack) - m_new;
+            grew |= m_new != m;
+            far |= __builtin_fabsf(m_new) > 4194304.f && m_new != neg_inf();
+            m = m_new;
+            sum[0] = sum[1] = 0.f;
             float cc = c;
             if (__any(far)) {                                    // see AttnWave::softmax
                 asm volatile("" ::: "memory");                   // a branch: it is hardly ever taken
-#pragma unroll
-                for (int t = 0; t < NC; ++t) s[t] *= c;
+                s *= c;
                 cc = 1.f;
             }
-            uint32_t w[NC][8];
+            uint32_t w[8];
             __builtin_amdgcn_sched_barrier(0);
             const auto slot = [&](auto y_) __attribute__((always_inline)) {
                 constexpr int Y = decltype(y_)::value;
                 read(StageId<Y + AHEAD>{});
                 const uint4 f = ring[Y % (AHEAD + 1)];
+                if constexpr (Y < KS) {
+                    if constexpr (Y == 0) {
 #pragma unroll
-                for (int t = 0; t < NC; ++t) {
-                    if constexpr (Y < KS) {
-                        if constexpr (Y == 0) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) next[t][i] = 0.f;
-                        }
-                        next[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8v, f), q[t][Y],
-                                                                          next[t], 0, 0, 0);
-                    } else {
-                        constexpr int U = (Y - KS) / DT, D = (Y - KS) % DT;
-                        o[t][D] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                            __builtin_bit_cast(h8v, f), __builtin_bit_cast(h8v, p[t][U]), o[t][D], 0, 0, 0);
+                        for (int i = 0; i < 16; ++i) next[i] = 0.f;
                     }
-                    // this slot's softmax elements
-#pragma unroll
-                    for (int i = 16 * Y / NM; i < 16 * (Y + 1) / NM; ++i) {
-                        const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], cc, add[t]));
-                        sum[t][i & 1] += y;
-                        if (i & 1) {
-                            w[t][i >> 1] = __builtin_bit_cast(uint32_t, h2v{(_Float16)y_last[t], (_Float16)y});
-                            asm volatile("" : "+v"(w[t][i >> 1]), "+v"(sum[t][0]), "+v"(sum[t][1]));  // computed here
-                        }
-                        y_last[t] = y;
-                    }
-                    // and of the next step's maximum, once its logits are there
-                    if constexpr (Y > KS) {
-                        constexpr int N = 2 * DT - 1, X = Y - KS - 1;
-                        if constexpr (X == 0) top[t] = next[t][0];
-#pragma unroll
-                        for (int i = 16 * X / N; i < 16 * (X + 1) / N; ++i) top[t] = fmaxf(top[t], next[t][i]);
-                        asm volatile("" : "+v"(top[t]));
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
+                    next = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8v, f), q[Y],
+                                                                      next, 0, 0, 0);
+                } else {
+                    constexpr int U = (Y - KS) / DT, D = (Y - KS) % DT;
+                    o[D] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                        __builtin_bit_cast(h8v, f), __builtin_bit_cast(h8v, p[U]), o[D], 0, 0, 0);
                 }
+                // this slot's softmax elements
+#pragma unroll
+                for (int i = 16 * Y / NM; i < 16 * (Y + 1) / NM; ++i) {
+                    const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], cc, add));
+                    sum[i & 1] += y;
+                    if (i & 1) {
+                        w[i >> 1] = __builtin_bit_cast(uint32_t, h2v{(_Float16)y_last, (_Float16)y});
+                        asm volatile("" : "+v"(w[i >> 1]), "+v"(sum[0]), "+v"(sum[1]));  // computed here
+                    }
+                    y_last = y;
+                }
+                // and of the next step's maximum, once its logits are there
+                if constexpr (Y > KS) {
+                    constexpr int N = 2 * DT - 1, X = Y - KS - 1;
+                    if constexpr (X == 0) top = next[0];
+#pragma unroll
+                    for (int i = 16 * X / N; i < 16 * (X + 1) / N; ++i) top = fmaxf(top, next[i]);
+                    asm volatile("" : "+v"(top));
+                }
+                __builtin_amdgcn_sched_barrier(0);
             };
             __builtin_amdgcn_s_setprio(1);                       // before a wave that is between its steps
             slot(StageId<0>{}); slot(StageId<1>{}); slot(StageId<2>{}); slot(StageId<3>{});
@@ -1037,48 +1132,45 @@ __global__ __launch_bounds__(WAVES * 64, 2 / NC) void attn_block_kernel(AttnArgs
             if constexpr (NM > 16) {
                 slot(StageId<16>{}); slot(StageId<17>{}); slot(StageId<18>{}); slot(StageId<19>{});
             }
-#pragma unroll
-            for (int t = 0; t < NC; ++t) {
-                if (t == 0) __builtin_amdgcn_s_setprio(0);
-                l[t] = __builtin_fmaf(sum[t][0] + sum[t][1], __uint_as_float((uint32_t)(127 - e) << 23), l[t] * alpha[t]);
-                p_new[t][0] = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
-                p_new[t][1] = make_uint4(w[t][4], w[t][5], w[t][6], w[t][7]);
-            }
+            __builtin_amdgcn_s_setprio(0);
+            l = __builtin_fmaf(sum[0] + sum[1], __uint_as_float((uint32_t)(127 - e) << 23), l * alpha);
+            p_new[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            p_new[1] = make_uint4(w[4], w[5], w[6], w[7]);
             if (__any(grew)) {                                   // O holds the values up to j - 1
 #pragma unroll
-                for (int t = 0; t < NC; ++t)
-#pragma unroll
-                    for (int d = 0; d < DT; ++d) o[t][d] *= alpha[t];
+                for (int d = 0; d < DT; ++d) o[d] *= alpha;
             }
         };
         static_assert(NM == 8 || NM == 16 || NM == 20, "slots written out");
 
-        Pages p0 = pages_of(0);                                  // of tiles i .. i + 3
-        load_k(t_first, p0);
+        Pages p0, p1, p2, p3;                                    // of tiles i .. i + 3
+        uint4 kr1[KCH];
+        pages_at(p0, 0);
+        pages_at(p1, 2);
+        pages_at(p2, 4);
+        load_k(kr, t_first, p0);
         load_v(t_first, p0);
-        Pages p1 = pages_of(1);
-        store_k(0, p0);
+        load_k(kr1, t_first + 1, p1);
+        scales_at(p0, 0);
+        scales_at(p1, 2);
+        scales_at(p2, 4);
+        store_k(kr, 0, p0);
         store_v(t_first, 0);
-        load_k(t_first + 1, p1);
-        Pages p2 = pages_of(2), p3;
-        store_k(1, p1);
+        store_k(kr1, 1, p1);
         // the values "before the first" meet p = 0: zeros, since LDS may hold anything
         for (int x = tid; x < V_BUF / 16; x += NT) ((uint4*)(lds_v + V_BUF))[x] = make_uint4(0, 0, 0, 0);
-        __syncthreads();
-        load_k(t_first + 2, p2);
+        load_k(kr, t_first + 2, p2);
         load_v(t_first + 1, p1);
+        __syncthreads();
 #pragma unroll
-        for (int t = 0; t < NC; ++t) {
+        for (int i = 0; i < 16; ++i) s_even[i] = 0.f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s_even[t][i] = 0.f;
+        for (int ks = 0; ks < KS; ++ks)
+            s_even = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*(const bf8v*)(lds_k + kat[ks % KA] + ks / KA * KA * 32), q[ks],
+                                                                s_even, 0, 0, 0);
+        top = s_even[0];
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-                s_even[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*(const bf8v*)(lds_k + kat[ks]), q[t][ks],
-                                                                    s_even[t], 0, 0, 0);
-            top[t] = s_even[t][0];
-#pragma unroll
-            for (int i = 1; i < 16; ++i) top[t] = fmaxf(top[t], s_even[t][i]);
-        }
+        for (int i = 1; i < 16; ++i) top = fmaxf(top, s_even[i]);
         // tile i: buffers i & 1.  Between its two steps every wave is done with the keys of tile i
         // and the values of tile i - 1, and their buffers take those of i + 2 and i + 1.  Half of
         // the waves stage before their step, half behind it: the two that share a SIMD then do
@@ -1086,10 +1178,10 @@ __global__ __launch_bounds__(WAVES * 64, 2 / NC) void attn_block_kernel(AttnArgs
         const bool early = WAVES < 8 || wave < WAVES / 2;
         const auto stage = [&](int i, auto par) __attribute__((always_inline)) {
             constexpr int P = decltype(par)::value;
-            store_k(P, p2);
+            store_k(kr, P, p2);
             store_v(t_first + i + 1, 1 - P);
             p3 = pages_of(i + 3);
-            load_k(t_first + i + 3, p3);
+            load_k(kr, t_first + i + 3, p3);
             load_v(t_first + i + 2, p2);
         };
         const auto tile_pair = [&](int i, auto par) __attribute__((always_inline)) {
@@ -1114,95 +1206,73 @@ __global__ __launch_bounds__(WAVES * 64, 2 / NC) void attn_block_kernel(AttnArgs
         for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int d = 0; d < DT; ++d)
-#pragma unroll
-                for (int t = 0; t < NC; ++t)
-                    o[t][d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const h8v*)(at + vat[2 + u] + d * 32 * V_ROW),
-                                                                     __builtin_bit_cast(h8v, p_odd[t][u]), o[t][d], 0, 0, 0);
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const h8v*)(at + vat[2 + u] + d * 32 * V_ROW),
+                                                                 __builtin_bit_cast(h8v, p_odd[u]), o[d], 0, 0, 0);
     }
 
     // results: lane half hh holds dims 32 d + 8 (i / 4) + 4 hh + i % 4 of its columns
+    const float ll = half_sum(l) * 0x1p-7f;
+    if (!used) return;
+    if (parts == 1) {
+        const float rl = ll == 0.f ? 0.f : 0x1p-7f / ll;
+        const int64_t at = (it.q0 + col / G) * a.heads_q + h * G + col % G;
+        uint16_t* const out = a.out + at * DV + 4 * hh;
 #pragma unroll
-    for (int t = 0; t < NC; ++t) {
-        const float ll = half_sum(l[t]) * 0x1p-7f;
-        const int x = (wave * NC + t) * 32 + lr, col = c0 + x;
-        if (col >= it.cols) continue;
-        if (splits == 1) {
-            const float rl = ll == 0.f ? 0.f : 0x1p-7f / ll;
-            const int64_t row = it.q0 + col / G;
-            const int head = h * G + col % G;
-            uint16_t* const out = a.out + (row * a.heads_q + head) * DV + 4 * hh;
+        for (int d = 0; d < DT; ++d)
 #pragma unroll
-            for (int d = 0; d < DT; ++d)
+            for (int y = 0; y < 4; ++y)
+                *(uint2*)(out + 32 * d + 8 * y) =
+                    make_uint2(pack_bf16x2(o[d][4 * y] * rl, o[d][4 * y + 1] * rl),
+                               pack_bf16x2(o[d][4 * y + 2] * rl, o[d][4 * y + 3] * rl));
+        if (a.lse && hh == 0)
+            a.lse[at] = ll == 0.f ? neg_inf() : (m + __builtin_log2f(ll)) * kLn2;
+    } else {
+        const int64_t slot = (int64_t)blockIdx.x * CB + wave * 32 + lr;
+        float* const ws = a.ws + slot * DV + 4 * hh;
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    *(uint2*)(out + 32 * d + 8 * y) =
-                        make_uint2(pack_bf16x2(o[t][d][4 * y] * rl, o[t][d][4 * y + 1] * rl),
-                                   pack_bf16x2(o[t][d][4 * y + 2] * rl, o[t][d][4 * y + 3] * rl));
-            if (a.lse && hh == 0)
-                a.lse[row * a.heads_q + head] = ll == 0.f ? neg_inf() : (m[t] + __builtin_log2f(ll)) * kLn2;
-        } else {
-            const int64_t slot = (int64_t)blockIdx.x * CB + x;
-            float* const ws = a.ws + slot * DV + 4 * hh;
+        for (int d = 0; d < DT; ++d)
 #pragma unroll
-            for (int d = 0; d < DT; ++d)
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    *(v4f*)(ws + 32 * d + 8 * y) = v4f{o[t][d][4 * y], o[t][d][4 * y + 1], o[t][d][4 * y + 2],
-                                                       o[t][d][4 * y + 3]} * 0x1p-7f;
-            if (hh == 0) {
-                float* const ml = a.ws + (int64_t)gridDim.x * CB * DV + slot * 2;
-                ml[0] = m[t];
-                ml[1] = ll;
-            }
+            for (int y = 0; y < 4; ++y)
+                *(v4f*)(ws + 32 * d + 8 * y) = v4f{o[d][4 * y], o[d][4 * y + 1], o[d][4 * y + 2],
+                                                   o[d][4 * y + 3]} * 0x1p-7f;
+        if (hh == 0) {
+            float* const ml = a.ws + (int64_t)gridDim.x * CB * DV + slot * 2;
+            ml[0] = m;
+            ml[1] = ll;
         }
     }
 }
 
-// Adds the parts of a split launch, in token order: one row per DV / 4 lanes.
+// Adds the parts of a split block, in token order: DV / 4 lanes a row, a workgroup 32 rows.
+constexpr int kJoinRows = 32;
 template <int DV, int CB>
 __global__ __launch_bounds__(kAttnThreads) void attn_block_join_kernel(AttnArgs a, int blocks, int splits) {
     constexpr int L = DV / 4, ROWS = kAttnThreads / L;
     const int tid = threadIdx.x, d4 = tid % L * 4;
-    const int G = a.heads_q / a.heads_kv;
-    const int64_t row = (int64_t)blockIdx.x * ROWS + tid / L;   // of T * heads_q
-    const int64_t t = row / a.heads_q;
-    const int head = (int)(row % a.heads_q), h = head / G;
-    if (t >= a.T) return;
-    int lo = 0, hi = a.R;                                      // the request of token t
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.q_offsets[mid] <= t) lo = mid;
-        else hi = mid;
-    }
-    const Item it = Item::of<false>(a, lo);
-    const int64_t col = (t - it.q0) * G + head % G;
-    if (t < it.q0 || col >= it.cols) return;
-    const int b = (int)(it.q0 * G / CB + lo + col / CB);
-    const int64_t first = ((int64_t)(blocks - 1 - b) * a.heads_kv + h) * splits;
+    const int piece = blockIdx.x % (CB / kJoinRows), block = blockIdx.x / (CB / kJoinRows);
+    const int h = block % a.heads_kv;
+    Block k;
+    if (!k.find(a, blocks - 1 - block / a.heads_kv, CB)) return;
+    const int parts = k.parts(splits);
+    if (parts == 1) return;                                     // finished by its workgroup
+    const int64_t first = (int64_t)block * splits * CB;
     const float* const ml = a.ws + (int64_t)blocks * a.heads_kv * splits * CB * DV;
-    float m = neg_inf();
-    for (int z = 0; z < splits; ++z) m = fmaxf(m, ml[((first + z) * CB + col % CB) * 2]);
-    v4f acc = {0.f, 0.f, 0.f, 0.f};
-    float l = 0.f;
-    for (int z = 0; z < splits; ++z) {
-        const int64_t slot = (first + z) * CB + col % CB;
-        const float mw = ml[slot * 2], lw = ml[slot * 2 + 1];
-        const float f = mw != neg_inf() || lw != 0.f ? __builtin_amdgcn_exp2f(mw - m) : 0.f;
-        const v4f v = *(const v4f*)(a.ws + slot * DV + d4);
-        l = __builtin_fmaf(lw, f, l);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(v[i], f, acc[i]);
+    for (int y = 0; y < kJoinRows / ROWS; ++y) {
+        const int x = piece * kJoinRows + y * ROWS + tid / L, col = k.c0 + x;
+        if (col >= k.it.cols) continue;
+        Part part;
+#pragma unroll 4
+        for (int z = 0; z < parts; ++z) {
+            const int64_t slot = first + z * CB + x;
+            const float2 mw = *(const float2*)(ml + slot * 2);
+            part.add(*(const v4f*)(a.ws + slot * DV + d4), mw.x, mw.y);
+        }
+        part.store(a, (k.it.q0 + col / k.it.G) * a.heads_q + h * k.it.G + col % k.it.G, DV, d4);
     }
-    const float rl = l == 0.f ? 0.f : 1.0f / l;
-    *(uint2*)(a.out + (t * a.heads_q + head) * DV + d4) =
-        make_uint2(pack_bf16x2(acc[0] * rl, acc[1] * rl), pack_bf16x2(acc[2] * rl, acc[3] * rl));
-    if (a.lse && d4 == 0) a.lse[t * a.heads_q + head] = l == 0.f ? neg_inf() : (m + __builtin_log2f(l)) * kLn2;
 }
 
-// Tile of a wave, and workgroups of a split launch: as many as the CUs hold at once (16 KB of
-// LDS a wave at 128/128, 20 at 192/128: two workgroups; four at 64/64).
-constexpr int kSplitTile = 64;
-static int split_groups(int dk) { return dk == 64 ? 1024 : 512; }
+constexpr int kSplitTile = 64;                // tokens of a wave's tile
 static bool splits(int64_t max_new, int32_t heads_q, int32_t heads_kv) {
     return max_new * (heads_q / heads_kv) <= kSplitMaxCols;
 }
@@ -1229,7 +1299,7 @@ static BlockPlan block_plan(int64_t T, int64_t R, int heads_q, int heads_kv) {
 size_t attn_paged_workspace_bytes(int64_t R, int64_t max_new, int32_t heads_q, int32_t heads_kv,
                                   int32_t dk, int32_t dv) {
     if (splits(max_new, heads_q, heads_kv))
-        return (size_t)split_groups(dk) * 2 * kCols * (dv + 2) * sizeof(float);
+        return (size_t)split_groups(dv) * 2 * kCols * (dv + 2) * sizeof(float);
     // any number of tokens up to R * max_new: at most kBlockSlots parts of 128 columns
     const BlockPlan p = block_plan(R * max_new, R, heads_q, heads_kv);
     const int64_t most = p.waves == 4 ? p.blocks * heads_kv * kBlockMaxSplits : kBlockSlots;
@@ -1246,32 +1316,37 @@ static hipError_t split_launch(const AttnArgs& a, hipStream_t stream) {
             <<<dim3((unsigned)items), dim3(kAttnThreads), 0, stream>>>(a, (int)col_tiles);
         return hipGetLastError();
     }
-    const int groups = split_groups(DK);
-    attn_split_kernel<DK, DV, B, kSplitTile><<<dim3(groups), dim3(kAttnThreads), 0, stream>>>(a, (int)col_tiles);
+    constexpr int groups = split_groups(DV);
+    // no more workgroups than the tables have room for: idle ones cost a short call 1 us
+    const int64_t most = items * ((a.width << a.log_b) / kKvTile + 1);
+    const int64_t grid = std::min<int64_t>(groups, most);
+    attn_split_kernel<DK, DV, B, kSplitTile><<<dim3((unsigned)grid), dim3(kAttnThreads), 0, stream>>>(a, (int)col_tiles);
     const int64_t rows = (int64_t)a.R * a.heads_kv * max_cols;
-    // parts per item, about groups / items + 1
+    // where items are many, an item has few parts (about groups / items + 1) and two strands (128
+    // wide: one wave) take a row; where they are few, a workgroup of eight strands does
     constexpr int FEW = 256 / DV;                               // a wave's strands
     if (items * 4 >= groups) {
         attn_join_kernel<DV, FEW><<<dim3((unsigned)((rows + 3) / 4)), dim3(kAttnThreads), 0, stream>>>(
-            a, (int)col_tiles, groups, max_cols);
+            a, (int)col_tiles, max_cols);
     } else {
         attn_join_kernel<DV, 4 * FEW><<<dim3((unsigned)rows), dim3(kAttnThreads), 0, stream>>>(
-            a, (int)col_tiles, groups, max_cols);
+            a, (int)col_tiles, max_cols);
     }
     return hipGetLastError();
 }
 
-template <int DK, int DV, int WAVES, int NC>
+template <int DK, int DV, int WAVES>
 static hipError_t block_launch(const AttnArgs& a, const BlockPlan& p, hipStream_t stream) {
     // as many parts as the workspace holds
-    const int64_t hold = a.ws ? (int64_t)(a.ws_bytes / (32 * NC * WAVES * (DV + 2) * sizeof(float))) : 0;
+    const int64_t hold = a.ws ? (int64_t)(a.ws_bytes / (32 * WAVES * (DV + 2) * sizeof(float))) : 0;
     const int64_t splits = std::max<int64_t>(1, std::min(p.splits, hold / (p.blocks * a.heads_kv)));
     const unsigned grid = (unsigned)(p.blocks * a.heads_kv * splits);
-    attn_block_kernel<DK, DV, WAVES, NC><<<dim3(grid), dim3(64 * WAVES), 0, stream>>>(a, (int)p.blocks, (int)splits);
+    attn_block_kernel<DK, DV, WAVES><<<dim3(grid), dim3(64 * WAVES), 0, stream>>>(a, (int)p.blocks, (int)splits);
     if (splits > 1) {
-        const int64_t rows = a.T * a.heads_q, per = kAttnThreads / (DV / 4);
-        attn_block_join_kernel<DV, 32 * NC * WAVES><<<dim3((unsigned)((rows + per - 1) / per)), dim3(kAttnThreads), 0, stream>>>(
-            a, (int)p.blocks, (int)splits);
+        constexpr int CB = 32 * WAVES;
+        attn_block_join_kernel<DV, CB>
+            <<<dim3((unsigned)(p.blocks * a.heads_kv * (CB / kJoinRows))), dim3(kAttnThreads), 0, stream>>>(
+                a, (int)p.blocks, (int)splits);
     }
     return hipGetLastError();
 }
@@ -1283,7 +1358,7 @@ static hipError_t attn_launch(const AttnArgs& a, hipStream_t stream) {
                : a.log_b == 6 ? split_launch<DK, DV, 64>(a, stream)
                               : split_launch<DK, DV, 128>(a, stream);
     const BlockPlan p = block_plan(a.T, a.R, a.heads_q, a.heads_kv);
-    return p.waves == 4 ? block_launch<DK, DV, 4, 1>(a, p, stream) : block_launch<DK, DV, 8, 1>(a, p, stream);
+    return p.waves == 4 ? block_launch<DK, DV, 4>(a, p, stream) : block_launch<DK, DV, 8>(a, p, stream);
 }
 
 hipError_t launch_attn_paged(const AttnArgs& a, int32_t dk, int32_t dv, hipStream_t stream) {
