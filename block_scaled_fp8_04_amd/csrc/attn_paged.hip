@@ -747,16 +747,12 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int
 //
 // Prompts and chunks: a workgroup takes 32 columns a wave of one request and KV head and walks
 // the tokens they see.  The products and the softmax beside them bound this, so the codes are
-// widened once per workgroup on their way into LDS, keys to bf16 with their scale, values to f16
-// without it, and every wave reads its fragments from there.
+// widened with their scales once per workgroup on their way into LDS, and every wave reads its
+// fragments from there.
 //
-// p enters its product as one f16 term (eleven bits).  Its range is kept by the value page's
-// scale 2^e: with m' within kSlack of the running maximum of x + e over the tokens (x the logit
-// in units of log 2), p' = 2^(x + e - m' + 15 - kSlack) lies in (0, 2^15], is exact to 2^-11
-// down to 2^-21 of the largest weighted token and to 2^-32 of it below that.  O sums p' times
-// the codes, l sums p' 2^-e: their quotient is the result.  The slack is there because a
-// maximum over 32 columns that is followed at once moves in every second step (2048 tokens
-// over 32k), and O has to be rescaled each time.
+// p enters its product as two bf16 terms here too, for the same fragment of values; p may pass 1,
+// up to 2^kSlack: a maximum over 32 columns that is followed at once moves in every second step
+// (2048 tokens over 32k), and O has to be rescaled each time.
 //
 // A step forms the logits of 32 tokens, does the softmax of the 32 before and adds the values of
 // the 32 before those: three independent streams, written out so that each matrix instruction
@@ -765,22 +761,12 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int
 // with bits 2 and 3 exchanged, which makes its registers the second product's operand as they
 // stand.
 typedef float v16f __attribute__((ext_vector_type(16)));
-typedef _Float16 h8v __attribute__((ext_vector_type(8)));
-typedef _Float16 h2v __attribute__((ext_vector_type(2)));
 
 constexpr int kBlockTile = 64;                // tokens in LDS at a time
 constexpr int kBlockSlots = 512;              // workgroups that a split launch aims at
 constexpr int kBlockMaxSplits = 16;
 constexpr int kPartTokens = 512;              // tokens that are not split further
 constexpr float kSlack = 8.f;
-
-__device__ __forceinline__ h8v widen8h(uint32_t w0, uint32_t w1) {
-    const h2v a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w0, 1.f, false);
-    const h2v b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w0, 1.f, true);
-    const h2v c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w1, 1.f, false);
-    const h2v d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)w1, 1.f, true);
-    return h8v{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
 
 // x of the two halves of the wave: their maximum, their sum
 __device__ __forceinline__ float half_max(float x) {
@@ -1000,7 +986,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
                 *(bf8v*)(to + ((2 * at + 1) ^ k_swz(token)) * 16) = widen8((int)kr[e].z, (int)kr[e].w, s);
             }
         };
-        const auto store_v = [&](int tile, int buf) {
+        const auto store_v = [&](int tile, int buf, const Pages& pg) {
             const int live = kv_len - min(tile, t_end - 1) * kBlockTile;
 #pragma unroll
             for (int e = 0; e < VCH; ++e) {
@@ -1016,9 +1002,10 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
                     }
                 }
                 const int f = d >> 1 & 7;
+                const float s = token < 32 ? pg.vs0 : pg.vs1;
                 uint8_t* const to = lds_v + buf * V_BUF + d * V_ROW;
-                *(h8v*)(to + (((x & 3) * 2) ^ f) * 16) = widen8h(w[0], w[1]);
-                *(h8v*)(to + (((x & 3) * 2 + 1) ^ f) * 16) = widen8h(w[2], w[3]);
+                *(bf8v*)(to + (((x & 3) * 2) ^ f) * 16) = widen8((int)w[0], (int)w[1], s);
+                *(bf8v*)(to + (((x & 3) * 2 + 1) ^ f) * 16) = widen8((int)w[2], (int)w[3], s);
             }
         };
         // fragment places: K rows are tokens with bits 2 and 3 exchanged, V rows are lr + 32 d
@@ -1031,27 +1018,26 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
         for (int x = 0; x < 4; ++x) vat[x] = lr * V_ROW + (((2 * x) ^ ((lr >> 1 & 7) ^ hh)) * 16);
 
         v16f s_even, s_odd;                              // logits of even and odd subtiles
-        uint4 p_even[2], p_odd[2];                       // and their p'
-        float top;                                           // maximum of the current ones
-        p_odd[0] = p_odd[1] = make_uint4(0, 0, 0, 0);
-        // one step: softmax of subtile j, logits of j + 1 (half KSUB of buffer KBUF) and their
-        // maximum, values of j - 1 (half VSUB of buffer VBUF)
-        constexpr int NM = KS + 2 * DT;                          // fragments, matrix instructions a column tile
+        uint4 p_even[4], p_odd[4];                       // and their p: rounded, remainders
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p_odd[i] = make_uint4(0, 0, 0, 0);
+        // one step: values of subtile j - 1 (half VSUB of buffer VBUF), softmax of j, logits of j + 1
+        // (half KSUB of buffer KBUF).  The values go first: their p make room for the new ones.
+        constexpr int NV = 2 * DT, NM = NV + KS;                 // fragments, of values and in all
         constexpr int AHEAD = 3;
-        const auto step = [&](int j, float vs, v16f& s, v16f& next, const uint4 (&p)[2],
-                              uint4 (&p_new)[2], auto kbuf_, auto ksub_, auto vbuf_,
-                              auto vsub_) __attribute__((always_inline)) {
+        const auto step = [&](int j, v16f& s, v16f& next, const uint4 (&p)[4], uint4 (&p_new)[4], auto kbuf_,
+                              auto ksub_, auto vbuf_, auto vsub_) __attribute__((always_inline)) {
             constexpr int KBUF = decltype(kbuf_)::value, KSUB = decltype(ksub_)::value;
             constexpr int VBUF = decltype(vbuf_)::value, VSUB = decltype(vsub_)::value;
             uint4 ring[AHEAD + 1];
             const auto read = [&](auto y_) __attribute__((always_inline)) {
-                constexpr int Y = decltype(y_)::value;
-                if constexpr (Y < KS)
-                    ring[Y % (AHEAD + 1)] = *(const uint4*)(lds_k + kat[Y % KA] + Y / KA * KA * 32 + KBUF * K_BUF +
-                                                           KSUB * 32 * K_ROW);
+                constexpr int Y = decltype(y_)::value, K = Y - NV;
+                if constexpr (Y < NV)
+                    ring[Y % (AHEAD + 1)] = *(const uint4*)(lds_v + vat[2 * VSUB + Y / DT] + VBUF * V_BUF +
+                                                           Y % DT * 32 * V_ROW);
                 else if constexpr (Y < NM)
-                    ring[Y % (AHEAD + 1)] = *(const uint4*)(lds_v + vat[2 * VSUB + (Y - KS) / DT] + VBUF * V_BUF +
-                                                           (Y - KS) % DT * 32 * V_ROW);
+                    ring[Y % (AHEAD + 1)] = *(const uint4*)(lds_k + kat[K % KA] + K / KA * KA * 32 + KBUF * K_BUF +
+                                                           KSUB * 32 * K_ROW);
             };
             read(StageId<0>{});
             read(StageId<1>{});
@@ -1061,64 +1047,69 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     if (base + 16 * (i >> 3) + 8 * hh + (i & 7) >= limit) s[i] = neg_inf();
-                top = s[0];
-#pragma unroll
-                for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
             }
-            const int e = (int)(__float_as_uint(vs) >> 23) - 127;
-            float alpha, add, sum[2], y_last;
-            bool grew = false, far = false;
-            // the reference follows the maximum only where it would be passed by over 2^kSlack
-            const float x = __builtin_ceilf(half_max(top) * c) + (float)e;
-            const float m_new = x > m + kSlack ? x : m;
-            alpha = m == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(m - m_new);
-            add = m_new == neg_inf() ? 0.f : (float)(e + 15 - (int)kSlack) - m_new;
-            grew |= m_new != m;
-            far |= __builtin_fabsf(m_new) > 4194304.f && m_new != neg_inf();
-            m = m_new;
-            sum[0] = sum[1] = 0.f;
-            float cc = c;
-            if (__any(far)) {                                    // see AttnWave::softmax
-                asm volatile("" ::: "memory");                   // a branch: it is hardly ever taken
-                s *= c;
-                cc = 1.f;
-            }
-            uint32_t w[8];
+            float top, alpha, add, sum[2] = {0.f, 0.f}, y_last, cc = c;
+            bool grew;
+            uint32_t w[8], rest[8];
             __builtin_amdgcn_sched_barrier(0);
             const auto slot = [&](auto y_) __attribute__((always_inline)) {
                 constexpr int Y = decltype(y_)::value;
+                // elements of the softmax that are done before slot y: they start in slot FIRST and
+                // spread over the matrix instructions from there on, two a slot of values
+                constexpr int FIRST = DT == 2 ? 2 : 3;
+                constexpr auto at = [](int y) { return y < NV ? 2 * y : NV + y; };
+                constexpr auto done = [at](int y) {
+                    return y <= FIRST ? 0 : 16 * (at(y) - at(FIRST)) / (at(NM) - at(FIRST));
+                };
                 read(StageId<Y + AHEAD>{});
                 const uint4 f = ring[Y % (AHEAD + 1)];
-                if constexpr (Y < KS) {
-                    if constexpr (Y == 0) {
+                if constexpr (Y < NV) {
+                    constexpr int U = Y / DT, D = Y % DT;
+                    o[D] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        __builtin_bit_cast(bf8v, f), __builtin_bit_cast(bf8v, p[U]), o[D], 0, 0, 0);
+                    o[D] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        __builtin_bit_cast(bf8v, f), __builtin_bit_cast(bf8v, p[2 + U]), o[D], 0, 0, 0);
+                } else {
+                    if constexpr (Y == NV) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) next[i] = 0.f;
                     }
-                    next = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8v, f), q[Y],
-                                                                      next, 0, 0, 0);
-                } else {
-                    constexpr int U = (Y - KS) / DT, D = (Y - KS) % DT;
-                    o[D] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                        __builtin_bit_cast(h8v, f), __builtin_bit_cast(h8v, p[U]), o[D], 0, 0, 0);
+                    next = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8v, f), q[Y - NV], next, 0,
+                                                                   0, 0);
                 }
-                // this slot's softmax elements
+                if constexpr (Y > 0 && Y < FIRST) {              // the maximum
+                    constexpr int N = FIRST - 1, X = Y - 1;
+                    if constexpr (X == 0) top = s[0];
 #pragma unroll
-                for (int i = 16 * Y / NM; i < 16 * (Y + 1) / NM; ++i) {
+                    for (int i = 16 * X / N; i < 16 * (X + 1) / N; ++i) top = fmaxf(top, s[i]);
+                }
+                if constexpr (Y == FIRST - 1) {
+                    // the reference follows the maximum only where it would be passed by over 2^kSlack
+                    const float x = __builtin_ceilf(half_max(top) * c);
+                    const float m_new = x > m + kSlack ? x : m;
+                    alpha = m == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(m - m_new);
+                    add = m_new == neg_inf() ? 0.f : -m_new;
+                    grew = m_new != m;
+                    if (__any(__builtin_fabsf(m_new) > 4194304.f && m_new != neg_inf())) {
+                        asm volatile("" ::: "memory");           // a branch: see AttnWave::softmax
+                        s *= c;
+                        cc = 1.f;
+                    }
+                    m = m_new;
+                }
+#pragma unroll
+                for (int i = done(Y); i < done(Y + 1); ++i) {
                     const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], cc, add));
                     sum[i & 1] += y;
                     if (i & 1) {
-                        w[i >> 1] = __builtin_bit_cast(uint32_t, h2v{(_Float16)y_last, (_Float16)y});
-                        asm volatile("" : "+v"(w[i >> 1]), "+v"(sum[0]), "+v"(sum[1]));  // computed here
+                        const uint32_t hi = __builtin_bit_cast(uint32_t, bf2v{(__bf16)y_last, (__bf16)y});
+                        w[i >> 1] = hi;
+                        rest[i >> 1] = __builtin_bit_cast(uint32_t, bf2v{(__bf16)(y_last - bf16_lo(hi)),
+                                                                         (__bf16)(y - bf16_hi(hi))});
+                        // computed here
+                        asm volatile("" : "+v"(w[i >> 1]), "+v"(rest[i >> 1]), "+v"(sum[0]), "+v"(sum[1]));
                     }
                     y_last = y;
-                }
-                // and of the next step's maximum, once its logits are there
-                if constexpr (Y > KS) {
-                    constexpr int N = 2 * DT - 1, X = Y - KS - 1;
-                    if constexpr (X == 0) top = next[0];
-#pragma unroll
-                    for (int i = 16 * X / N; i < 16 * (X + 1) / N; ++i) top = fmaxf(top, next[i]);
-                    asm volatile("" : "+v"(top));
                 }
                 __builtin_amdgcn_sched_barrier(0);
             };
@@ -1133,9 +1124,11 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
                 slot(StageId<16>{}); slot(StageId<17>{}); slot(StageId<18>{}); slot(StageId<19>{});
             }
             __builtin_amdgcn_s_setprio(0);
-            l = __builtin_fmaf(sum[0] + sum[1], __uint_as_float((uint32_t)(127 - e) << 23), l * alpha);
+            l = __builtin_fmaf(l, alpha, sum[0] + sum[1]);
             p_new[0] = make_uint4(w[0], w[1], w[2], w[3]);
             p_new[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            p_new[2] = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+            p_new[3] = make_uint4(rest[4], rest[5], rest[6], rest[7]);
             if (__any(grew)) {                                   // O holds the values up to j - 1
 #pragma unroll
                 for (int d = 0; d < DT; ++d) o[d] *= alpha;
@@ -1143,7 +1136,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
         };
         static_assert(NM == 8 || NM == 16 || NM == 20, "slots written out");
 
-        Pages p0, p1, p2, p3;                                    // of tiles i .. i + 3
+        Pages p0, p1, p2, p3;                                    // of tile 0 and tiles i + 1 .. i + 3
         uint4 kr1[KCH];
         pages_at(p0, 0);
         pages_at(p1, 2);
@@ -1155,7 +1148,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
         scales_at(p1, 2);
         scales_at(p2, 4);
         store_k(kr, 0, p0);
-        store_v(t_first, 0);
+        store_v(t_first, 0, p0);
         store_k(kr1, 1, p1);
         // the values "before the first" meet p = 0: zeros, since LDS may hold anything
         for (int x = tid; x < V_BUF / 16; x += NT) ((uint4*)(lds_v + V_BUF))[x] = make_uint4(0, 0, 0, 0);
@@ -1168,9 +1161,6 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
         for (int ks = 0; ks < KS; ++ks)
             s_even = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*(const bf8v*)(lds_k + kat[ks % KA] + ks / KA * KA * 32), q[ks],
                                                                 s_even, 0, 0, 0);
-        top = s_even[0];
-#pragma unroll
-        for (int i = 1; i < 16; ++i) top = fmaxf(top, s_even[i]);
         // tile i: buffers i & 1.  Between its two steps every wave is done with the keys of tile i
         // and the values of tile i - 1, and their buffers take those of i + 2 and i + 1.  Half of
         // the waves stage before their step, half behind it: the two that share a SIMD then do
@@ -1179,21 +1169,20 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
         const auto stage = [&](int i, auto par) __attribute__((always_inline)) {
             constexpr int P = decltype(par)::value;
             store_k(kr, P, p2);
-            store_v(t_first + i + 1, 1 - P);
+            store_v(t_first + i + 1, 1 - P, p1);
             p3 = pages_of(i + 3);
             load_k(kr, t_first + i + 3, p3);
             load_v(t_first + i + 2, p2);
         };
         const auto tile_pair = [&](int i, auto par) __attribute__((always_inline)) {
             constexpr int P = decltype(par)::value;
-            step(2 * i, p0.vs0, s_even, s_odd, p_odd, p_even, StageId<P>{}, StageId<1>{}, StageId<1 - P>{},
+            step(2 * i, s_even, s_odd, p_odd, p_even, StageId<P>{}, StageId<1>{}, StageId<1 - P>{},
                  StageId<1>{});
             __syncthreads();
             if (early) stage(i, par);
-            step(2 * i + 1, p0.vs1, s_odd, s_even, p_even, p_odd, StageId<1 - P>{}, StageId<0>{}, StageId<P>{},
+            step(2 * i + 1, s_odd, s_even, p_even, p_odd, StageId<1 - P>{}, StageId<0>{}, StageId<P>{},
                  StageId<0>{});
             if (!early) stage(i, par);
-            p0 = p1;
             p1 = p2;
             p2 = p3;
         };
@@ -1205,16 +1194,20 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int d = 0; d < DT; ++d)
-                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const h8v*)(at + vat[2 + u] + d * 32 * V_ROW),
-                                                                 __builtin_bit_cast(h8v, p_odd[u]), o[d], 0, 0, 0);
+            for (int d = 0; d < DT; ++d) {
+                const bf8v f = *(const bf8v*)(at + vat[2 + u] + d * 32 * V_ROW);
+#pragma unroll
+                for (int x = u; x < 4; x += 2)
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, __builtin_bit_cast(bf8v, p_odd[x]), o[d], 0,
+                                                                   0, 0);
+            }
     }
 
     // results: lane half hh holds dims 32 d + 8 (i / 4) + 4 hh + i % 4 of its columns
-    const float ll = half_sum(l) * 0x1p-7f;
+    const float ll = half_sum(l);
     if (!used) return;
     if (parts == 1) {
-        const float rl = ll == 0.f ? 0.f : 0x1p-7f / ll;
+        const float rl = ll == 0.f ? 0.f : 1.0f / ll;
         const int64_t at = (it.q0 + col / G) * a.heads_q + h * G + col % G;
         uint16_t* const out = a.out + at * DV + 4 * hh;
 #pragma unroll
@@ -1234,7 +1227,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
 #pragma unroll
             for (int y = 0; y < 4; ++y)
                 *(v4f*)(ws + 32 * d + 8 * y) = v4f{o[d][4 * y], o[d][4 * y + 1], o[d][4 * y + 2],
-                                                   o[d][4 * y + 3]} * 0x1p-7f;
+                                                   o[d][4 * y + 3]};
         if (hh == 0) {
             float* const ml = a.ws + (int64_t)gridDim.x * CB * DV + slot * 2;
             ml[0] = m;
@@ -1337,7 +1330,7 @@ static hipError_t split_launch(const AttnArgs& a, hipStream_t stream) {
 
 template <int DK, int DV, int WAVES>
 static hipError_t block_launch(const AttnArgs& a, const BlockPlan& p, hipStream_t stream) {
-    // as many parts as the workspace holds
+    // as many parts as the workspace holds: it is sized for R * max_new tokens, T may be padded
     const int64_t hold = a.ws ? (int64_t)(a.ws_bytes / (32 * WAVES * (DV + 2) * sizeof(float))) : 0;
     const int64_t splits = std::max<int64_t>(1, std::min(p.splits, hold / (p.blocks * a.heads_kv)));
     const unsigned grid = (unsigned)(p.blocks * a.heads_kv * splits);

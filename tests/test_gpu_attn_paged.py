@@ -253,3 +253,83 @@ def test_seeded_random_sizes(seed):
     new = [int(x) for x in rng.integers(0, top + 1, R)]
     kv = [n + int(rng.integers(0, 600)) if n else 0 for n in new]
     _case(1000 + seed, kv, new, H, G, B, dk, dv, workspace=bool(seed % 4))
+
+
+# ------------------------------------------------------------- many query columns
+
+@pytest.mark.parametrize("dk,dv", DIMS)
+@pytest.mark.parametrize("B", [32, 64, 128])
+def test_chunks_split_over_tokens(dk, dv, B):
+    # few blocks: their tokens are shared by several workgroups where they are many
+    _case(dk + B, [1500, 40, 513, 2100], [40, 40, 17, 1], 2, 4, B, dk, dv)
+
+
+@pytest.mark.parametrize("dk,dv", DIMS)
+def test_chunks_of_many_heads(dk, dv):
+    # enough blocks for the larger workgroups
+    _case(dk + 1, [300, 700, 64, 90], [300, 150, 64, 33], 64, 1, 64, dk, dv)
+
+
+@pytest.mark.parametrize("H", [1, 4])
+def test_more_requests_than_lanes_with_a_chunk(H):
+    rng = np.random.default_rng(H)
+    new = [int(x) for x in rng.integers(0, 4, 150)]
+    kv = [n + int(rng.integers(0, 90)) if n else 0 for n in new]
+    new[3], kv[3], new[140], kv[140] = 130, 1300, 70, 70
+    _case(30 + H, kv, new, H, 2, 32, 128, 128)
+
+
+@pytest.mark.parametrize("G", [1, 3])
+def test_more_requests_than_lanes(G):
+    # every workgroup's range of tiles passes over idle requests and request boundaries
+    rng = np.random.default_rng(40 + G)
+    new = [int(x) for x in rng.integers(0, 3, 333)]
+    kv = [n + int(rng.choice([0, 1, 60, 127, 128, 300])) if n else 0 for n in new]
+    _case(40 + G, kv, new, 9, G, 64, 64, 64)
+
+
+def test_most_requests():
+    R = bfp8.KV_MAX_REQUESTS
+    rng = np.random.default_rng(50)
+    new = [int(x) for x in rng.integers(0, 2, R)]
+    kv = [n + int(rng.integers(0, 5)) if n else 0 for n in new]
+    _case(50, kv, new, 1, 2, 32, 64, 64)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.1, 3.0])
+def test_scales_of_chunks(scale):
+    _case(22, [300, 600], [90, 30], 2, 4, 64, 128, 128, scale=scale)
+
+
+@pytest.mark.parametrize("workspace", [True, False])
+def test_chunks_with_and_without_a_workspace(workspace):
+    _case(60, [1700, 1100], [60, 50], 2, 4, 64, 128, 128, workspace=workspace)
+
+
+def test_padded_tokens_and_a_small_workspace():
+    """T far above R * max_new: the workspace is sized for the latter."""
+    rng = np.random.default_rng(62)
+    cache = Cache(rng, [1300], 1, 64, 128, 128)
+    q = bf16(rng.standard_normal((900, 4, 128)))
+    out, lse = attend(q, cache.gpu(), cache.table, [0, 30], [1300], 30, 0.1)
+    check_attention(out[:30], lse[:30], f64(q)[:30], cache.arrays, cache.table, [0, 30], [1300], 0.1, "padded")
+    assert (out[30:].view(torch.int16) == -23131).all()
+
+
+def test_far_logits_of_chunks():
+    """Queries of 2^60, 2^-60 and a wide spread in one block, and value scales 2^20 apart."""
+    rng = np.random.default_rng(61)
+    n = 200
+    cache = Cache(rng, [n], 1, 64, 128, 128, spread=20)
+    q = rng.standard_normal((n, 1, 128))
+    q[64:70] *= 2.0 ** 60
+    q[70:80] *= 2.0 ** -60
+    q[80:, :, ::3] *= 2.0 ** -9
+    q = bf16(q)
+    out, lse = attend(q, cache.gpu(), cache.table, [0, n], [n], n, 4.0)
+    want, want_lse, weight, slack = ref.attention(f64(q), *cache.arrays, cache.table, [0, n], [n], 4.0)
+    plain = np.r_[0:64, 70:n]
+    err = np.abs(f64(out) - want)[plain]
+    bound = 2.0 ** -9 * np.abs(want) + (2.0 ** -8 + 2 * slack[..., None]) * weight + 1e-30
+    assert (err <= bound[plain]).all(), f"worst {np.max(err / bound[plain]):.3f}"
+    assert np.allclose(f64(out)[64:70], want[64:70], rtol=2.0 ** -8)         # one-hot weights
