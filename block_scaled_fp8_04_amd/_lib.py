@@ -474,8 +474,9 @@ def kv_plan_buffers(R, T, device) -> KVPlan:
 
 
 def _need_i32(device, *named):
+    gpu = device.index
     for name, t, shape in named:
-        if t.dtype is not torch.int32 or t.device != device or not t.is_contiguous():
+        if t.dtype is not torch.int32 or t.get_device() != gpu or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous int32 tensor on the call's GPU")
         if shape is not None and t.shape != shape:
             raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -528,9 +529,10 @@ def _cache_shape(device, k_cache, k_scales, v_cache, v_scales):
     _need(v_cache.shape == (P, H, dv, B), "v_cache must be [P, H, Dv, B] next to k_cache [P, H, B, Dk]")
     _need(k_scales.dtype is torch.float32 and v_scales.dtype is torch.float32 and
           k_scales.shape == (P, H) and v_scales.shape == (P, H), "scales must be fp32 [P, H]")
+    gpu = device.index
     for t in (k_cache, k_scales, v_cache, v_scales):
-        _need(t.device == device and t.is_contiguous(),
-              "the cache must be contiguous, on the call's GPU")
+        if t.get_device() != gpu or not t.is_contiguous():
+            raise ValueError("the cache must be contiguous, on the call's GPU")
     return P, H, B, dk, dv
 
 
@@ -543,11 +545,12 @@ def bfp8_kv_append(k, v, slot_map, k_cache, k_scales, v_cache, v_scales, stream=
     _need(k.dtype is torch.bfloat16 and v.dtype is torch.bfloat16, "k and v must be bf16")
     T = slot_map.shape[0]
     _need(k.shape == (T, H, dk) and v.shape == (T, H, dv), "k must be [T, H, Dk], v [T, H, Dv]")
-    _need(v.device == dev and (T == 0 or (k.stride(2) == 1 and v.stride(2) == 1)),
+    k_strides, v_strides = k.stride(), v.stride()
+    _need(v.get_device() == dev.index and (T == 0 or (k_strides[2] == 1 and v_strides[2] == 1)),
           "k and v must be on one GPU, their rows contiguous")
     _need_i32(dev, ("slot_map", slot_map, (T,)))
     _check("bfp8_kv_append", library().bfp8_kv_append(
-        k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1),
+        k.data_ptr(), k_strides[0], k_strides[1], v.data_ptr(), v_strides[0], v_strides[1],
         slot_map.data_ptr(), T, k_cache.data_ptr(), k_scales.data_ptr(), v_cache.data_ptr(),
         v_scales.data_ptr(), P, B, H, dk, dv, _stream(stream, dev)))
 

@@ -30,7 +30,10 @@ namespace bfp8 {
 constexpr int kAttnThreads = 256;
 constexpr int kAttnWaves = kAttnThreads / 64;
 constexpr int kCols = 16;                     // query columns of a wave
-constexpr int kSplitMaxCols = 64;             // most query columns of a split item
+// Most query columns (new tokens times heads per KV head) of the kernels for few of them; the
+// others widen the codes once for 128 or 256 columns.  32 requests x 4096 tokens x 8 heads of 128:
+// 64 columns take 173 us by the former and 179 by the latter, 96 columns 257 and 181.
+constexpr int kSplitMaxCols = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -173,7 +176,7 @@ struct Segment {
 // Each wave brings its own tiles to LDS, by loads that bypass the registers, and reads them
 // back as fragments; nothing is shared between waves, so there is no barrier in the loop.  A
 // fragment's lanes take sixteen different rows, and read straight from memory that way every
-// 16 bytes are an access of their own: 3.8 instead of 5.2 TB/s (64 requests, 180k tokens, 8
+// 16 bytes are an access of their own: 3.8 instead of 5.1 TB/s (64 requests, 180k tokens, 8
 // heads of 128).  The next tile's keys are requested when this tile's have been multiplied,
 // its values when this tile's have: one of the two is always on its way while the wave
 // computes, and the keys also while the waves of a finished item are joined.  The loads are
@@ -512,6 +515,12 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, int64_t row, int he
 // item by item; an item that lies within one workgroup is finished there, the others leave
 // partial sums (at most two of them per workgroup: its first and its last item) that
 // attn_join_kernel adds in token order.
+//
+// Bound by reading the cache: 64 requests, 180k tokens, 8 heads of 128 (370 MB) take 72 + 5 us, 5.1
+// TB/s, of 63 at the rate of a large copy's reads; without the computation 75 (before the next
+// item's keys were requested early, then 77 with it).  One token over 1030: 7.5 + 4 us, which is
+// latency: four dependent reads, one tile, the join.  There a workgroup takes a single 128-token
+// tile; with four tiles, one for each wave twice, it is 13.2 us.
 
 // Workgroups: as many as the CUs hold at once (16 KB of LDS a wave at 128/128, 20 at 192/128: two
 // workgroups a CU; four at 64/64).  768 or 1024 at 128/128 are slower: 86 and 82 us against 77 (64
@@ -760,12 +769,24 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int
 // cycles) and by the LDS read of a fragment three instructions on.  S^T's rows are the tokens
 // with bits 2 and 3 exchanged, which makes its registers the second product's operand as they
 // stand.
+//
+// 2048 tokens behind 30000, 32 heads of 192/128: 1.51 ms, 0.86 PFLOP/s of the operator's own
+// products (the matrix cores also multiply the remainders of p: 1.21 PFLOP/s).  The two waves of
+// a SIMD keep the matrix cores 60 % busy: what a step leaves uncovered is the vector work of the
+// softmax and of splitting p (28 cycles an element), the staging of the next tile, and the clock,
+// which falls to 2.0 GHz under this load.  One f16 term of p takes 1.21 ms and loses weights under
+// 2^-32 of the largest, which show where the largest one's value is zero.  64 columns a wave (one
+// wave a SIMD) 1.47 ms against 1.24 at that time, four waves a workgroup 1.32 against 1.21.
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr int kBlockTile = 64;                // tokens in LDS at a time
-constexpr int kBlockSlots = 512;              // workgroups that a split launch aims at
+// Workgroups that a split launch aims at: two a CU.  1024: 245 us against 230 (256 tokens behind 30k,
+// 32 heads on 8), 35 against 28 (behind 2k, 8 heads on 2).
+constexpr int kBlockSlots = 512;
 constexpr int kBlockMaxSplits = 16;
-constexpr int kPartTokens = 512;              // tokens that are not split further
+// Tokens that are not split further.  24 requests, decodes and chunks of up to 600 tokens: 37.7 us
+// so, 38.2 with 512, 43.3 with 1024.
+constexpr int kPartTokens = 256;
 constexpr float kSlack = 8.f;
 
 // x of the two halves of the wave: their maximum, their sum
@@ -862,8 +883,9 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int G = a.heads_q / a.heads_kv;
 
-    // blocks that see the most tokens go first, for the last ones to end together: by rank, or by
-    // number from the last one down (many requests, or a split launch, whose parts all run at once)
+    // blocks that see the most tokens go first, for the last ones to end together: by rank (eight
+    // prompts of 296 to 1662 tokens: 120 us, 125 by number), or by number from the last one down
+    // where there are more requests than lanes, or the launch is split and runs all at once
     int idx = blockIdx.x;
     const int z = idx % splits;
     idx /= splits;
@@ -1271,7 +1293,9 @@ static bool splits(int64_t max_new, int32_t heads_q, int32_t heads_kv) {
 }
 
 // How a launch of many columns divides: eight waves a workgroup, or four where that leaves CUs
-// idle, and the tokens of a block over several workgroups where even those are few.
+// idle, and the tokens of a block over several workgroups where even those are few.  Behind 8k
+// tokens, 32 heads of 128: a chunk of 1024 tokens takes 240 us by four waves and 281 by eight, one
+// of 2048 354 and 341.
 struct BlockPlan {
     int waves;
     int64_t blocks, splits;                          // per KV head; parts of each
@@ -1316,7 +1340,8 @@ static hipError_t split_launch(const AttnArgs& a, hipStream_t stream) {
     attn_split_kernel<DK, DV, B, kSplitTile><<<dim3((unsigned)grid), dim3(kAttnThreads), 0, stream>>>(a, (int)col_tiles);
     const int64_t rows = (int64_t)a.R * a.heads_kv * max_cols;
     // where items are many, an item has few parts (about groups / items + 1) and two strands (128
-    // wide: one wave) take a row; where they are few, a workgroup of eight strands does
+    // wide: one wave) take a row; where they are few, a workgroup of eight strands does.  64 requests
+    // x 8 heads: 69 us by the former, 73 by the latter; 3 requests x 80k tokens x 2 heads: 37 and 32.
     constexpr int FEW = 256 / DV;                               // a wave's strands
     if (items * 4 >= groups) {
         attn_join_kernel<DV, FEW><<<dim3((unsigned)((rows + 3) / 4)), dim3(kAttnThreads), 0, stream>>>(
