@@ -1124,7 +1124,8 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
                     const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], cc, add));
                     sum[i & 1] += y;
                     if (i & 1) {
-                        const uint32_t hi = __builtin_bit_cast(uint32_t, bf2v{(__bf16)y_last, (__bf16)y});
+                        uint32_t hi = __builtin_bit_cast(uint32_t, bf2v{(__bf16)y_last, (__bf16)y});
+                        asm("" : "+v"(hi));                      // not rounded again for the remainder
                         w[i >> 1] = hi;
                         rest[i >> 1] = __builtin_bit_cast(uint32_t, bf2v{(__bf16)(y_last - bf16_lo(hi)),
                                                                          (__bf16)(y - bf16_hi(hi))});
