@@ -1335,10 +1335,7 @@ static hipError_t split_launch(const AttnArgs& a, hipStream_t stream) {
         return hipGetLastError();
     }
     constexpr int groups = split_groups(DV);
-    // no more workgroups than the tables have room for: idle ones cost a short call 1 us
-    const int64_t most = items * ((a.width << a.log_b) / kKvTile + 1);
-    const int64_t grid = std::min<int64_t>(groups, most);
-    attn_split_kernel<DK, DV, B, kSplitTile><<<dim3((unsigned)grid), dim3(kAttnThreads), 0, stream>>>(a, (int)col_tiles);
+    attn_split_kernel<DK, DV, B, kSplitTile><<<dim3(groups), dim3(kAttnThreads), 0, stream>>>(a, (int)col_tiles);
     const int64_t rows = (int64_t)a.R * a.heads_kv * max_cols;
     // where items are many, an item has few parts (about groups / items + 1) and two strands (128
     // wide: one wave) take a row; where they are few, a workgroup of eight strands does.  64 requests
