@@ -770,8 +770,8 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int
 // with bits 2 and 3 exchanged, which makes its registers the second product's operand as they
 // stand.
 //
-// 2048 tokens behind 30000, 32 heads of 192/128: 1.51 ms, 0.86 PFLOP/s of the operator's own
-// products (the matrix cores also multiply the remainders of p: 1.21 PFLOP/s).  The two waves of
+// 2048 tokens behind 30000, 32 heads of 192/128: 1.52 ms, 0.86 PFLOP/s of the operator's own
+// products (the matrix cores also multiply the remainders of p: 1.20 PFLOP/s).  The two waves of
 // a SIMD keep the matrix cores 60 % busy: what a step leaves uncovered is the vector work of the
 // softmax and of splitting p (28 cycles an element), the staging of the next tile, and the clock,
 // which falls to 2.0 GHz under this load.  One f16 term of p takes 1.21 ms and loses weights under
