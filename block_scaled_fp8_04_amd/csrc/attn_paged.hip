@@ -4,11 +4,10 @@
 //
 // Both products are taken transposed, keys and values as the first operand:
 //     S^T [token, query] = K Q^T,     O^T [d, query] += V^T P^T
-// Lane group g = lane / 16 takes tokens 32 g .. 32 g + 31 of a 128-token tile in both: the
-// rows of K enter the first product in the order that leaves those tokens' results in that
-// group's lanes, where they are the second product's P^T operand as they stand.  P never
-// moves between lanes, and with values stored token-contiguous neither product's operands
-// need a transposition.
+// A group of lanes takes the same run of a tile's tokens in both: the rows of K enter the first
+// product in the order that leaves those tokens' results in that group's lanes, where they are
+// the second product's P^T operand as they stand.  P never moves between lanes, and with values
+// stored token-contiguous neither product's operands need a transposition.
 //
 // Precision.  Codes are widened to bf16 with their page's scale on the way to the matrix
 // cores (exact: four significant bits and a power of two) and q is bf16 as it comes.  p
@@ -435,16 +434,16 @@ struct AttnWave {
     }
 };
 
-// Joins the four waves' results of one 16-column item in their bytes of lds_v (the keys' bytes
-// may be receiving the next item's): first m and l, then each wave's O times 2^(m_w - m), its
-// four-dim groups permuted by the column against bank conflicts.  Thread x gets column x / 16,
-// dims 4 (x % 16) + 64 j of the sum, in wave order, and that column's m and l.
 // Barrier behind finished LDS accesses, leaving the loads that are on their way alone.
 __device__ __forceinline__ void barrier_ds() {
     __builtin_amdgcn_s_waitcnt(0xC07F);                         // lgkmcnt(0)
     barrier_lds();
 }
 
+// Joins the four waves' results of one 16-column item in their bytes of lds_v (the keys' bytes
+// may be receiving the next item's): first m and l, then each wave's O times 2^(m_w - m), its
+// four-dim groups permuted by the column against bank conflicts.  Thread x gets column x / 16,
+// dims 4 (x % 16) + 64 j of the sum, in wave order, and that column's m and l.
 template <class W, int DV>
 __device__ __forceinline__ void join_waves(const W& w, uint8_t* lds_v, float (&part)[DV / 16], float& m,
                                            float& l) {
@@ -1182,8 +1181,8 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
         for (int i = 0; i < 16; ++i) s_even[i] = 0.f;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
-            s_even = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*(const bf8v*)(lds_k + kat[ks % KA] + ks / KA * KA * 32), q[ks],
-                                                                s_even, 0, 0, 0);
+            s_even = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                *(const bf8v*)(lds_k + kat[ks % KA] + ks / KA * KA * 32), q[ks], s_even, 0, 0, 0);
         // tile i: buffers i & 1.  Between its two steps every wave is done with the keys of tile i
         // and the values of tile i - 1, and their buffers take those of i + 2 and i + 1.  Half of
         // the waves stage before their step, half behind it: the two that share a SIMD then do
