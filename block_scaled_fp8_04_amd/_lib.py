@@ -6,6 +6,7 @@ signature, and passes their device pointers, the sizes and the current HIP
 stream to the library.  No arithmetic of the path happens here, and there is
 no fallback: if the library is missing the call raises.
 """
+import contextlib
 import ctypes
 import os
 from typing import NamedTuple
@@ -141,6 +142,19 @@ def _stream(stream, device):
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
+
+
+def _allocating_on(stream, device):
+    """Context in which an allocating call makes its arrays: on the stream that its kernels take.
+    Fills then stay in order with them, and what the call drops or the caller frees is handed out
+    again behind them."""
+    if stream is None or device.type != "cuda":        # (the call itself refuses host tensors)
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)               # 0 names no stream to ExternalStream
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else \
+            torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 def _ptr(t):
@@ -600,38 +614,45 @@ def bfp8_attn_paged(q, k_cache, k_scales, v_cache, v_scales, block_table, q_offs
 
 
 # ------------------------------------------------------- allocating conveniences
+#
+# New arrays belong to the stream that is given, as if made under torch.cuda.stream(stream).
 
 def act_quant(x, stream=None):
     """(q e4m3 as uint8 [M,K], scales fp32 [M,K/128]) = act_quant(x bf16 [M,K])."""
     M, K = x.shape
-    q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
-    s = torch.empty((M, K // BLOCK), dtype=torch.float32, device=x.device)
-    bfp8_act_quant(x, q, s, stream)
-    return q, s
+    with _allocating_on(stream, x.device):
+        q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        s = torch.empty((M, K // BLOCK), dtype=torch.float32, device=x.device)
+        bfp8_act_quant(x, q, s, stream)
+        return q, s
 
 
 def weight_dequant(w, s, stream=None):
-    out = torch.empty(w.shape, dtype=torch.bfloat16, device=w.device)
-    bfp8_weight_dequant(w, s, out, stream)
-    return out
+    with _allocating_on(stream, w.device):
+        out = torch.empty(w.shape, dtype=torch.bfloat16, device=w.device)
+        bfp8_weight_dequant(w, s, out, stream)
+        return out
 
 
 def gemm(a, a_s, b, b_s, workspace=None, stream=None):
-    c = torch.empty((a.shape[0], b.shape[0]), dtype=torch.bfloat16, device=a.device)
-    bfp8_gemm(a, a_s, b, b_s, c, workspace, stream)
-    return c
+    with _allocating_on(stream, a.device):
+        c = torch.empty((a.shape[0], b.shape[0]), dtype=torch.bfloat16, device=a.device)
+        bfp8_gemm(a, a_s, b, b_s, c, workspace, stream)
+        return c
 
 
 def gemm_grouped(a, a_s, b, b_s, group_offsets, stream=None):
-    c = torch.empty((a.shape[0], b.shape[1]), dtype=torch.bfloat16, device=a.device)
-    bfp8_gemm_grouped(a, a_s, b, b_s, c, group_offsets, stream)
-    return c
+    with _allocating_on(stream, a.device):
+        c = torch.empty((a.shape[0], b.shape[1]), dtype=torch.bfloat16, device=a.device)
+        bfp8_gemm_grouped(a, a_s, b, b_s, c, group_offsets, stream)
+        return c
 
 
 def gemm_bf16(a, b, workspace=None, stream=None):
-    c = torch.empty((a.shape[0], b.shape[0]), dtype=torch.bfloat16, device=a.device)
-    bfp8_gemm_bf16(a, b, c, workspace, stream)
-    return c
+    with _allocating_on(stream, a.device):
+        c = torch.empty((a.shape[0], b.shape[0]), dtype=torch.bfloat16, device=a.device)
+        bfp8_gemm_bf16(a, b, c, workspace, stream)
+        return c
 
 
 def linear_bf16(x, w, w_s, workspace=None, stream=None):
@@ -641,32 +662,36 @@ def linear_bf16(x, w, w_s, workspace=None, stream=None):
 
 def gemm_act_quant(a, a_s, b, b_s, stream=None):
     M, N = a.shape[0], b.shape[0]
-    q = torch.empty((M, N), dtype=torch.uint8, device=a.device)
-    qs = torch.empty((M, N // BLOCK), dtype=torch.float32, device=a.device)
-    bfp8_gemm_act_quant(a, a_s, b, b_s, q, qs, stream)
-    return q, qs
+    with _allocating_on(stream, a.device):
+        q = torch.empty((M, N), dtype=torch.uint8, device=a.device)
+        qs = torch.empty((M, N // BLOCK), dtype=torch.float32, device=a.device)
+        bfp8_gemm_act_quant(a, a_s, b, b_s, q, qs, stream)
+        return q, qs
 
 
 def gemm_swiglu_act_quant(a, a_s, w13, s13, stream=None):
     M, N = a.shape[0], w13.shape[0] // 2
-    q = torch.empty((M, N), dtype=torch.uint8, device=a.device)
-    qs = torch.empty((M, N // BLOCK), dtype=torch.float32, device=a.device)
-    bfp8_gemm_swiglu_act_quant(a, a_s, w13, s13, q, qs, stream)
-    return q, qs
+    with _allocating_on(stream, a.device):
+        q = torch.empty((M, N), dtype=torch.uint8, device=a.device)
+        qs = torch.empty((M, N // BLOCK), dtype=torch.float32, device=a.device)
+        bfp8_gemm_swiglu_act_quant(a, a_s, w13, s13, q, qs, stream)
+        return q, qs
 
 
 def act_quant_ue8m0(x, stream=None):
     M, K = x.shape
-    q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
-    s = torch.empty((M, K // BLOCK), dtype=torch.float32, device=x.device)
-    bfp8_act_quant_ue8m0(x, q, s, stream)
-    return q, s
+    with _allocating_on(stream, x.device):
+        q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        s = torch.empty((M, K // BLOCK), dtype=torch.float32, device=x.device)
+        bfp8_act_quant_ue8m0(x, q, s, stream)
+        return q, s
 
 
 def gemm_ue8m0(a, a_s, b, b_s, workspace=None, stream=None):
-    c = torch.empty((a.shape[0], b.shape[0]), dtype=torch.bfloat16, device=a.device)
-    bfp8_gemm_ue8m0(a, a_s, b, b_s, c, workspace, stream)
-    return c
+    with _allocating_on(stream, a.device):
+        c = torch.empty((a.shape[0], b.shape[0]), dtype=torch.bfloat16, device=a.device)
+        bfp8_gemm_ue8m0(a, a_s, b, b_s, c, workspace, stream)
+        return c
 
 
 def linear_fp8(x, w, w_s, workspace=None, stream=None):
@@ -679,20 +704,22 @@ def moe_dispatch(topk_idx, expert_lo, G, stream=None):
     """(group_offsets [G+1], row_token [T*k], slot_row [T, k]) for local experts expert_lo..+G-1."""
     T, k = topk_idx.shape
     dev = topk_idx.device
-    off = torch.empty(G + 1, dtype=torch.int32, device=dev)
-    row_token = torch.empty(max(1, T * k), dtype=torch.int32, device=dev)
-    slot_row = torch.empty((T, k), dtype=torch.int32, device=dev)
-    ws = torch.empty(max(1, bfp8_moe_dispatch_workspace_size(T, k, G) // 4), dtype=torch.int32,
-                     device=dev)
-    bfp8_moe_dispatch(topk_idx, expert_lo, off, row_token, slot_row, ws, stream)
-    return off, row_token, slot_row
+    with _allocating_on(stream, dev):
+        off = torch.empty(G + 1, dtype=torch.int32, device=dev)
+        row_token = torch.empty(max(1, T * k), dtype=torch.int32, device=dev)
+        slot_row = torch.empty((T, k), dtype=torch.int32, device=dev)
+        ws = torch.empty(max(1, bfp8_moe_dispatch_workspace_size(T, k, G) // 4), dtype=torch.int32,
+                         device=dev)
+        bfp8_moe_dispatch(topk_idx, expert_lo, off, row_token, slot_row, ws, stream)
+        return off, row_token, slot_row
 
 
 def moe_combine(expert_out, slot_row, weights, stream=None):
-    y = torch.empty((slot_row.shape[0], expert_out.shape[1]), dtype=torch.bfloat16,
-                    device=expert_out.device)
-    bfp8_moe_combine(expert_out, slot_row, weights, y, stream)
-    return y
+    with _allocating_on(stream, expert_out.device):
+        y = torch.empty((slot_row.shape[0], expert_out.shape[1]), dtype=torch.bfloat16,
+                        device=expert_out.device)
+        bfp8_moe_combine(expert_out, slot_row, weights, y, stream)
+        return y
 
 
 def moe_experts_fp8(x, topk_idx, weights, w, w_s, expert_lo, stream=None):
@@ -706,22 +733,24 @@ def moe_experts_fp8(x, topk_idx, weights, w, w_s, expert_lo, stream=None):
     T, K = x.shape
     k = topk_idx.shape[1]
     G, N, _ = w.shape
-    off, row_token, slot_row = moe_dispatch(topk_idx, expert_lo, G, stream)
-    cap = T * k
-    q = torch.empty((cap, K), dtype=torch.uint8, device=x.device)
-    qs = torch.empty((cap, K // BLOCK), dtype=torch.float32, device=x.device)
-    bfp8_act_quant_rows(x, row_token[:cap], off[G:], q, qs, stream)
-    out = torch.empty((cap, N), dtype=torch.bfloat16, device=x.device)
-    bfp8_gemm_grouped(q, qs, w, w_s, out, off, stream)
-    return moe_combine(out, slot_row, weights, stream)
+    with _allocating_on(stream, x.device):
+        off, row_token, slot_row = moe_dispatch(topk_idx, expert_lo, G, stream)
+        cap = T * k
+        q = torch.empty((cap, K), dtype=torch.uint8, device=x.device)
+        qs = torch.empty((cap, K // BLOCK), dtype=torch.float32, device=x.device)
+        bfp8_act_quant_rows(x, row_token[:cap], off[G:], q, qs, stream)
+        out = torch.empty((cap, N), dtype=torch.bfloat16, device=x.device)
+        bfp8_gemm_grouped(q, qs, w, w_s, out, off, stream)
+        return moe_combine(out, slot_row, weights, stream)
 
 
 def kv_plan(ctx_lens, new_lens, free_pages, block_table, page_size, num_tokens, free_head=None,
             stream=None):
     """bfp8_kv_plan into new arrays; num_tokens is the step's token capacity."""
-    plan = kv_plan_buffers(block_table.shape[0], num_tokens, block_table.device)
-    bfp8_kv_plan(ctx_lens, new_lens, free_pages, block_table, page_size, plan, free_head, stream)
-    return plan
+    with _allocating_on(stream, block_table.device):
+        plan = kv_plan_buffers(block_table.shape[0], num_tokens, block_table.device)
+        bfp8_kv_plan(ctx_lens, new_lens, free_pages, block_table, page_size, plan, free_head, stream)
+        return plan
 
 
 def attn_paged(q, cache, block_table, plan, max_new, scale=None, workspace=None, stream=None):
@@ -729,9 +758,10 @@ def attn_paged(q, cache, block_table, plan, max_new, scale=None, workspace=None,
     Dk**-0.5.  Returns out bf16 [T, Hq, Dv]; rows of no request are zero."""
     T, Hq, dk = q.shape
     H, dv = cache[0].shape[1], cache[2].shape[2]
-    out = torch.zeros((T, Hq, dv), dtype=torch.bfloat16, device=q.device)
-    if workspace is None:
-        workspace = attn_paged_workspace(block_table.shape[0], max_new, Hq, H, dk, dv, q.device)
-    bfp8_attn_paged(q, *cache, block_table, plan.q_offsets, plan.kv_lens, plan.tile_offsets, max_new,
-                    dk ** -0.5 if scale is None else scale, out, None, workspace, stream)
-    return out
+    with _allocating_on(stream, q.device):
+        out = torch.zeros((T, Hq, dv), dtype=torch.bfloat16, device=q.device)
+        if workspace is None:
+            workspace = attn_paged_workspace(block_table.shape[0], max_new, Hq, H, dk, dv, q.device)
+        bfp8_attn_paged(q, *cache, block_table, plan.q_offsets, plan.kv_lens, plan.tile_offsets, max_new,
+                        dk ** -0.5 if scale is None else scale, out, None, workspace, stream)
+        return out
