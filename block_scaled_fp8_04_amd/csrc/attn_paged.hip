@@ -1317,6 +1317,8 @@ size_t attn_paged_workspace_bytes(int64_t R, int64_t max_new, int32_t heads_q, i
                                   int32_t dk, int32_t dv) {
     if (splits(max_new, heads_q, heads_kv))
         return (size_t)split_groups(dv) * 2 * kCols * (dv + 2) * sizeof(float);
+    // more tokens make more blocks: what one token in all does not split, nothing does
+    if (block_plan(1, R, heads_q, heads_kv).splits == 1) return 0;
     // any number of tokens up to R * max_new: at most kBlockSlots parts of 128 columns
     const BlockPlan p = block_plan(R * max_new, R, heads_q, heads_kv);
     const int64_t most = p.waves == 4 ? p.blocks * heads_kv * kBlockMaxSplits : kBlockSlots;
