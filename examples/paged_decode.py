@@ -60,7 +60,8 @@ class Layer:
         bfp8.bfp8_attn_paged(q, *self.cache, self.table, plan.q_offsets, plan.kv_lens, plan.tile_offsets,
                              b["max_new"], WIDTH ** -0.5, b["out"], None, b["ws"])
         bfp8.bfp8_linear_fp8(b["out"].flatten(1), *self.w_out, b["y"], b["ws_out"])
-        self.ctx.copy_(plan.kv_lens)
+        # an idle or refused request has a kv_len of 0 and keeps what it has
+        self.ctx.copy_(torch.where(plan.kv_lens > 0, plan.kv_lens, self.ctx))
         self.free_head.copy_(plan.counts[1:2])
         return b["y"]
 
