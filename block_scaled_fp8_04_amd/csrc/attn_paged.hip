@@ -16,7 +16,10 @@
 // would take the codes as they are, but it drops what lies 2^-14 below the largest product of
 // a 16-element group (measured), which moves a logit by 1e-5 of that product, and p as two
 // e4m3 terms loses what lies 2^-22 below a tile's largest.  Logits, maxima,
-// norms and sums are fp32.  Running maxima are rounded up to integers (in units of log 2),
+// norms and sums are fp32.  Codes are widened with half their scale, because the largest value,
+// 256 * 2^120 for an element of 248 * 2^120 or more, would be infinite, and its token's zero weight in
+// the rows that do not see it NaN; logits and outputs get the factor of two back, so no result changes.
+// Running maxima are rounded up to integers (in units of log 2),
 // so that rescaling by 2^(old - new) is exact.
 #include <algorithm>
 
@@ -159,9 +162,12 @@ __device__ __forceinline__ int last_of(bool holds) { return max(__popcll(__ballo
 __device__ __forceinline__ bool q_vec(const AttnArgs& a) {
     return ((uintptr_t)a.q % 16) == 0 && ((a.q_ts | a.q_hs) % 8) == 0;
 }
+// The factor of half the logits that makes them exponents of two.
 __device__ __forceinline__ float exp2_scale(const AttnArgs& a) {
-    return fmaxf(__builtin_fabsf(a.scale) * kLog2e, 0x1p-126f);     // -inf times 0 is NaN
+    return 2.f * fmaxf(__builtin_fabsf(a.scale) * kLog2e, 0x1p-126f);     // -inf times 0 is NaN
 }
+// Twice 1 / l for sums over half the values; 0 for a row that sees nothing.
+__device__ __forceinline__ float out_factor(float l) { return l == 0.f ? 0.f : 2.0f / l; }
 
 // A run of tiles of one item that a workgroup walks; its waves take every fourth one.
 struct Segment {
@@ -328,7 +334,7 @@ struct AttnWave {
             const int base = tile * TT;
             wait_vmcnt<NV>();                                   // this tile's keys have landed
             __builtin_amdgcn_sched_barrier(0);
-            const float ke = pick(ks, LT * (lr >> 2)), ve = pick(vs, LT * g);
+            const float ke = 0.5f * pick(ks, LT * (lr >> 2)), ve = 0.5f * pick(vs, LT * g);
             v4f x[KT];
 #pragma unroll
             for (int t = 0; t < KT; ++t) x[t] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -496,7 +502,7 @@ __device__ __forceinline__ void join_waves(const W& w, uint8_t* lds_v, float (&p
 template <int DV>
 __device__ __forceinline__ void store_row(const AttnArgs& a, int64_t row, int head, int od,
                                           const float (&part)[DV / 16], float m, float l) {
-    const float r = l == 0.f ? 0.f : 1.0f / l;
+    const float r = out_factor(l);
     uint16_t* const out = a.out + (row * a.heads_q + head) * DV + od;
 #pragma unroll
     for (int j = 0; j < DV / 64; ++j) {
@@ -696,7 +702,7 @@ struct Part {
         for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(v[i], f1, acc[i] * f0);
     }
     __device__ __forceinline__ void store(const AttnArgs& a, int64_t row, int dv, int d4) const {
-        const float rl = l == 0.f ? 0.f : 1.0f / l;
+        const float rl = out_factor(l);
         *(uint2*)(a.out + row * dv + d4) =
             make_uint2(pack_bf16x2(acc[0] * rl, acc[1] * rl), pack_bf16x2(acc[2] * rl, acc[3] * rl));
         if (a.lse && d4 == 0) a.lse[row] = l == 0.f ? neg_inf() : (m + __builtin_log2f(l)) * kLn2;
@@ -938,8 +944,8 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
         };
         const auto fetch_scale = [&](const float* x, int e) { return x[(int64_t)e * a.heads_kv + h]; };
         entry = fetch_table(t_first);
-        ks_l = fetch_scale(a.k_scales, entry);
-        vs_l = fetch_scale(a.v_scales, entry);
+        ks_l = 0.5f * fetch_scale(a.k_scales, entry);
+        vs_l = 0.5f * fetch_scale(a.v_scales, entry);
         const auto pages_at = [&](Pages& x, int at) {
             x.page0 = (int64_t)__builtin_amdgcn_readlane(entry, at) * a.heads_kv + h;
             x.page1 = (int64_t)__builtin_amdgcn_readlane(entry, at + 1) * a.heads_kv + h;
@@ -958,8 +964,8 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
             const int at = 2 * i & 63;
             if (at == 0 && i > 0) {
                 entry = entry_n;
-                ks_l = ks_n;
-                vs_l = vs_n;
+                ks_l = 0.5f * ks_n;                              // (halved here: at the load, it would wait)
+                vs_l = 0.5f * vs_n;
             }
             if (at == 16) entry_n = fetch_table(t_first + i + 24);
             if (at == 40) {
@@ -1229,7 +1235,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
     const float ll = half_sum(l);
     if (!used) return;
     if (parts == 1) {
-        const float rl = ll == 0.f ? 0.f : 1.0f / ll;
+        const float rl = out_factor(ll);
         const int64_t at = (it.q0 + col / G) * a.heads_q + h * G + col % G;
         uint16_t* const out = a.out + at * DV + 4 * hh;
 #pragma unroll
