@@ -821,6 +821,16 @@ __device__ __forceinline__ int wave_reduce(int x, F f) {
 __device__ __forceinline__ int wave_sum(int x) { return wave_reduce(x, [](int a, int b) { return a + b; }); }
 __device__ __forceinline__ int wave_max(int x) { return wave_reduce(x, [](int a, int b) { return max(a, b); }); }
 
+// Level of a request's first block of cb columns by the tokens that it sees beside its own, in units
+// of a block's own; beyond kTopLevel (2^36 tokens times heads) blocks keep no order.
+constexpr int kTopLevel = 1 << 29;
+constexpr int first_level(int before, int G, int cb) {
+    const uint64_t level = (uint64_t)before * G / cb;
+    return level < kTopLevel ? (int)level : kTopLevel;
+}
+static_assert(first_level(INT32_MAX, 65535, 128) >= 0 && kTopLevel + ((INT32_MAX >> 7) + 1) < 1 << 30,
+              "a level and the search's step above it fit 32 bits");
+
 // A block of cb columns of a launch.  Request r's blocks are numbered from q_offsets[r] * G / cb + r
 // on, where there is room for all of them.
 struct Block {
@@ -853,7 +863,7 @@ struct Block {
         const Item mine = Item::of(a, reqs.q0, reqs.q1, reqs.kv_len);
         // level of a block: the level of its request's first one, and one more for each further
         const int count = lane < a.R ? (mine.cols + cb - 1) / cb : 0;
-        const int low = (int)((uint64_t)max(mine.kv_len - mine.n, 0) * mine.G / cb), high = low + count;
+        const int low = first_level(max(mine.kv_len - mine.n, 0), mine.G, cb), high = low + count;
         const auto above = [&](int level) { return wave_sum(min(max(high - level, 0), count)); };
         if (above(0) <= rank) return false;
         int level = 0;                               // the highest with more than `rank` blocks from it on
