@@ -105,6 +105,17 @@ __device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
     return q;
 }
 
+// Lengths reach 2^31 - 32 (pages of 32 tokens).  Pieces of `per` tokens that hold `tokens`, and the
+// table entry of a token `ahead` of a tile's first one, which may lie beyond the length: both pass
+// 31 bits on the way.
+constexpr int pieces(int tokens, int per) { return (int)(((uint32_t)tokens + per - 1) / per); }
+constexpr uint32_t entry_ahead(int tile, int per, int ahead, int log_b) {
+    return ((uint32_t)tile * per + ahead) >> log_b;
+}
+static_assert(pieces(INT32_MAX - 31, 64) == 1 << 25 && pieces(INT32_MAX - 31, 256) == 1 << 23 && pieces(0, 64) == 0,
+              "the largest length's pieces");
+static_assert(entry_ahead((1 << 25) + 24, 64, 63 * 32, 5) == (1u << 26) + 48 + 63, "an entry past the largest length");
+
 // What an item's columns are: shared by all kernels.
 struct Item {
     int64_t q0;
@@ -359,7 +370,7 @@ struct AttnWave {
             uint32_t mask[LT / 4];
 #pragma unroll
             for (int w = 0; w < LT / 4; ++w) mask[w] = 0xFFFFFFFFu;
-            if (base + TT > free_limit) {
+            if (base > free_limit - TT) {
                 const int seen = limit - base - LT * g;         // this lane's tokens: the first `seen`
 #pragma unroll
                 for (int t = 0; t < KT; ++t)
@@ -567,7 +578,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_item_kernel(AttnArgs a, int
     seg.h = h;
     seg.ct = ct;
     seg.t0 = 0;
-    seg.t1 = (it.limit(min(ct * kCols + kCols, it.cols) - 1) + TT - 1) / TT;
+    seg.t1 = pieces(it.limit(min(ct * kCols + kCols, it.cols) - 1), TT);
     seg.whole = 1;
     if (wave < seg.t1)
         w.walk(a, lds_k + wave * W::K_BYTES, lds_v + wave * W::V_BYTES, seg, wave, it.kv_len,
@@ -637,8 +648,8 @@ __global__ __launch_bounds__(kAttnThreads) void attn_split_kernel(AttnArgs a, in
         const int col = cur.ct * kCols + (lane & 15);
         const bool used = col < it.cols;
         if (cur.ct * kCols < it.cols) {
-            cur.t1 = min(cur.t1, (it.kv_len + TT - 1) / TT);
-            const int n1 = next.ct * kCols < nit.cols ? min(next.t1, (nit.kv_len + TT - 1) / TT) : 0;
+            cur.t1 = min(cur.t1, pieces(it.kv_len, TT));
+            const int n1 = next.ct * kCols < nit.cols ? min(next.t1, pieces(nit.kv_len, TT)) : 0;
             const bool chain = has && next.t0 + wave < n1;
             w.load_q(used ? it.row(a, cur.h, col) : nullptr, q_vec(a), a.scale < 0.f, lane >> 4);
             if (cur.t0 + wave < cur.t1) {
@@ -880,7 +891,7 @@ struct Block {
     }
     // workgroups that share its tokens
     __device__ __forceinline__ int parts(int splits) const {
-        return min(splits, max((seen + kPartTokens - 1) / kPartTokens, 1));
+        return min(splits, max(pieces(seen, kPartTokens), 1));
     }
 };
 
@@ -911,7 +922,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
     const int r = k.r, c0 = k.c0, parts = k.parts(splits);
     if (z >= parts) return;
     const int seen_by_all = it.limit(c0);
-    const int tiles = (k.seen + kBlockTile - 1) / kBlockTile;
+    const int tiles = pieces(k.seen, kBlockTile);
     static_assert(kBlockMaxSplits <= 32, "2^25 tiles at most, so 32 bits will do");
     const int t_first = __builtin_amdgcn_readfirstlane(tiles * z / parts);
     const int t_end = __builtin_amdgcn_readfirstlane(tiles * (z + 1) / parts);
@@ -949,7 +960,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
         int entry, entry_n = 0;
         float ks_l, vs_l, ks_n = 0.f, vs_n = 0.f;
         const auto fetch_table = [&](int tile) {                 // the lanes' entries from `tile` on
-            const int j = min((tile * kBlockTile + 32 * lane) >> a.log_b, last);
+            const int j = (int)min(entry_ahead(tile, kBlockTile, 32 * lane, a.log_b), (uint32_t)last);
             return (int)min(max((int64_t)a.block_table[(int64_t)r * a.width + j], (int64_t)0), a.pages - 1);
         };
         const auto fetch_scale = [&](const float* x, int e) { return x[(int64_t)e * a.heads_kv + h]; };
@@ -1080,7 +1091,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
             read(StageId<1>{});
             read(StageId<2>{});
             const int base = t_first * kBlockTile + 32 * j;
-            if (base + 32 > seen_by_all) {
+            if (base > seen_by_all - 32) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     if (base + 16 * (i >> 3) + 8 * hh + (i & 7) >= limit) s[i] = neg_inf();
