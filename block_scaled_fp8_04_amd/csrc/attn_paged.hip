@@ -19,8 +19,8 @@
 // norms and sums are fp32.  Codes are widened with half their scale, because the largest value,
 // 256 * 2^120 for an element of 248 * 2^120 or more, would be infinite, and its token's zero weight in
 // the rows that do not see it NaN; logits and outputs get the factor of two back, so no result changes.
-// Running maxima are rounded up to integers (in units of log 2),
-// so that rescaling by 2^(old - new) is exact.
+// Running maxima are rounded up to integers (in units of log 2), so that rescaling by 2^(old - new)
+// is exact.
 #include <algorithm>
 
 #include "device_codec.hpp"
@@ -34,7 +34,7 @@ constexpr int kAttnWaves = kAttnThreads / 64;
 constexpr int kCols = 16;                     // query columns of a wave
 // Most query columns (new tokens times heads per KV head) of the kernels for few of them; the
 // others widen the codes once for 128 or 256 columns.  32 requests x 4096 tokens x 8 heads of 128:
-// 64 columns take 173 us by the former and 179 by the latter, 96 columns 257 and 181.
+// 64 columns take 174 us by the former and 178 by the latter, 96 columns 260 and 182.
 constexpr int kSplitMaxCols = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -114,7 +114,8 @@ constexpr uint32_t entry_ahead(int tile, int per, int ahead, int log_b) {
 }
 static_assert(pieces(INT32_MAX - 31, 64) == 1 << 25 && pieces(INT32_MAX - 31, 256) == 1 << 23 && pieces(0, 64) == 0,
               "the largest length's pieces");
-static_assert(entry_ahead((1 << 25) + 24, 64, 63 * 32, 5) == (1u << 26) + 48 + 63, "an entry past the largest length");
+static_assert(entry_ahead((1 << 25) + 24, 64, 63 * 32, 5) == (1u << 26) + 48 + 63,
+              "an entry past the largest length");
 
 // What an item's columns are: shared by all kernels.
 struct Item {
@@ -532,15 +533,17 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, int64_t row, int he
 // partial sums (at most two of them per workgroup: its first and its last item) that
 // attn_join_kernel adds in token order.
 //
-// Bound by reading the cache: 64 requests, 180k tokens, 8 heads of 128 (370 MB) take 72 + 5 us, 5.1
-// TB/s, of 63 at the rate of a large copy's reads; without the computation 75 (before the next
-// item's keys were requested early, then 77 with it).  One token over 1030: 7.5 + 4 us, which is
-// latency: four dependent reads, one tile, the join.  There a workgroup takes a single 128-token
-// tile; with four tiles, one for each wave twice, it is 13.2 us.
+// Bound by reading the cache: 64 requests, 180k tokens, 8 heads of 128 (370 MB) take 70 + 5 us, 5.3
+// TB/s, where a large copy's reads take 63 us.  One token over 1030: 7.3 + 4 us, which is latency:
+// four dependent reads, one tile, the join.  There a workgroup takes a single 128-token tile; with
+// four tiles, one for each wave twice, it is 13.2 us.  The kernel has more uniform values than scalar
+// registers: the compiler keeps 28 to 79 of them in lanes of vector registers.
 
-// Workgroups: as many as the CUs hold at once (16 KB of LDS a wave at 128/128, 20 at 192/128: two
-// workgroups a CU; four at 64/64).  768 or 1024 at 128/128 are slower: 86 and 82 us against 77 (64
-// requests, 180k tokens).
+// Workgroups: at 128/128 and 192/128 as many as the CUs hold at once, two each (16 and 20 KB of LDS a
+// wave): 64 requests, 180k tokens, 64 heads on 8 of 128 take 74.5 us, with 768 workgroups 79.5, with
+// 1024 75.3.  At 64/64 the registers (137) let three a CU run, and 1024 workgroups are more than that:
+// the same requests take 47.1 us at 64/64, with 768 44.7, with 512 46.5; 24 requests of four drafts 17.2,
+// 16.6 and 16.4.
 constexpr int split_groups(int dv) { return dv == 64 ? 1024 : 512; }
 
 struct SplitPlan {
@@ -781,27 +784,28 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, int
 //
 // A step forms the logits of 32 tokens, does the softmax of the 32 before and adds the values of
 // the 32 before those: three independent streams, written out so that each matrix instruction
-// is followed by the vector work that fits beside it (a softmax element takes 26 of its 32
-// cycles) and by the LDS read of a fragment three instructions on.  S^T's rows are the tokens
+// (32 cycles) is followed by the vector work that fits beside it and by the LDS read of a fragment
+// three instructions on.  S^T's rows are the tokens
 // with bits 2 and 3 exchanged, which makes its registers the second product's operand as they
 // stand.
 //
-// 2048 tokens behind 30000, 32 heads of 192/128: 1.52 ms, 0.86 PFLOP/s of the operator's own
-// products (the matrix cores also multiply the remainders of p: 1.20 PFLOP/s).  The two waves of
-// a SIMD keep the matrix cores 60 % busy: what a step leaves uncovered is the vector work of the
-// softmax and of splitting p (28 cycles an element), the staging of the next tile, and the clock,
-// which falls to 2.0 GHz under this load.  One f16 term of p takes 1.21 ms and loses weights under
+// 2048 tokens behind 30000, 32 heads of 192/128: 1.52 to 1.55 ms, 0.85 PFLOP/s of the operator's own
+// products (the matrix cores also multiply the remainders of p: 1.2 PFLOP/s).  The two waves of
+// a SIMD keep the matrix cores 61 % busy (counters): an element has 56 cycles of matrix instructions
+// and 10.6 vector instructions, at least 42 cycles, of the softmax, of splitting p and of staging the
+// next tile; and the clock falls to 1.85 GHz under this load.  One f16 term of p takes 1.21 ms and
+// loses weights under
 // 2^-32 of the largest, which show where the largest one's value is zero.  64 columns a wave (one
 // wave a SIMD) 1.47 ms against 1.24 at that time, four waves a workgroup 1.32 against 1.21.
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr int kBlockTile = 64;                // tokens in LDS at a time
-// Workgroups that a split launch aims at: two a CU.  1024: 245 us against 230 (256 tokens behind 30k,
-// 32 heads on 8), 35 against 28 (behind 2k, 8 heads on 2).
+// Workgroups that a split launch aims at: two a CU.  1024: 215 us against 203 (256 tokens behind 30k,
+// 32 heads on 8); behind 2k, 8 heads on 2, both 24.
 constexpr int kBlockSlots = 512;
 constexpr int kBlockMaxSplits = 16;
-// Tokens that are not split further.  24 requests, decodes and chunks of up to 600 tokens: 37.7 us
-// so, 38.2 with 512, 43.3 with 1024.
+// Tokens that are not split further.  24 requests, decodes and chunks of up to 700 tokens: 44.3 us
+// so, 43.6 with 512, 45.4 with 1024.
 constexpr int kPartTokens = 256;
 constexpr float kSlack = 8.f;
 
@@ -910,7 +914,7 @@ __global__ __launch_bounds__(WAVES * 64, 2) void attn_block_kernel(AttnArgs a, i
     const int G = a.heads_q / a.heads_kv;
 
     // blocks that see the most tokens go first, for the last ones to end together: by rank (eight
-    // prompts of 296 to 1662 tokens: 120 us, 125 by number), or by number from the last one down
+    // prompts of 296 to 1662 tokens: 119 us, 122 by number), or by number from the last one down
     // where there are more requests than lanes, or the launch is split and runs all at once
     int idx = blockIdx.x;
     const int z = idx % splits;
@@ -1321,8 +1325,8 @@ static bool splits(int64_t max_new, int32_t heads_q, int32_t heads_kv) {
 
 // How a launch of many columns divides: eight waves a workgroup, or four where that leaves CUs
 // idle, and the tokens of a block over several workgroups where even those are few.  Behind 8k
-// tokens, 32 heads of 128: a chunk of 1024 tokens takes 240 us by four waves and 281 by eight, one
-// of 2048 354 and 341.
+// tokens, 32 heads of 128: a chunk of 1024 tokens takes 244 us by four waves and 309 by eight, one
+// of 2048 442 and 429.
 struct BlockPlan {
     int waves;
     int64_t blocks, splits;                          // per KV head; parts of each
@@ -1367,7 +1371,7 @@ static hipError_t split_launch(const AttnArgs& a, hipStream_t stream) {
     const int64_t rows = (int64_t)a.R * a.heads_kv * max_cols;
     // where items are many, an item has few parts (about groups / items + 1) and two strands (128
     // wide: one wave) take a row; where they are few, a workgroup of eight strands does.  64 requests
-    // x 8 heads: 69 us by the former, 73 by the latter; 3 requests x 80k tokens x 2 heads: 37 and 32.
+    // x 8 heads: 74.5 us by the former, 79 by the latter; 3 requests, 195k tokens, 2 heads: 36 and 29.
     constexpr int FEW = 256 / DV;                               // a wave's strands
     if (items * 4 >= groups) {
         attn_join_kernel<DV, FEW><<<dim3((unsigned)((rows + 3) / 4)), dim3(kAttnThreads), 0, stream>>>(

@@ -212,11 +212,17 @@ hipError_t launch_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int6
 // code by old / s is exact but for values that fall under the format's normal
 // range, so a page's growing scale does not wear its codes down.
 //
-// Bound by the loads' latency more than by their bytes: 13240 tokens x 8 heads of 128 + 128
-// elements (54 MB read, 27 MB written) take 25.6 us, 3.2 TB/s, 64 tokens x 8 heads 5.0 us.  What
-// bought the most: the row slices of a page held in registers sized for its page size, so that
-// four workgroups share a compute unit (33.5 us with registers for 128 tokens throughout), and
-// values turned by words instead of bytes (121 us).  512 threads: 28.9 and 5.6 us.
+// Bound by latency more than by bytes: 13240 tokens x 8 heads of 128 + 128 elements (54 MB read,
+// 27 MB written) take 25.4 us in pages of 64, 3.2 TB/s, 64 tokens x 8 heads 4.9 us.  A workgroup's
+// slots, loads, maximum and stores follow one another, and its registers, which hold the row
+// slices of a page, let four share a compute unit at 128/128 in pages of 64 (120 registers; 33.5 us
+// with registers for 128 tokens throughout): 1656 workgroups are one round and a second that is 60 %
+// full.  The same tokens in other forms, with the workgroups that share a unit:
+//                 pages of 32    of 64          of 128
+//     64/64       23.3 us (4)    16.5 us (5)    16.3 us (4)
+//     128/128     26.0 us (5)    25.1 us (4)    30.3 us (2)
+//     192/128     33.6 us (4)    35.0 us (3)    36.4 us (2)
+// Values turned by words instead of bytes bought the most (121 us); 512 threads take 28.9 and 5.6 us.
 constexpr int kAppendThreads = 256;
 
 __device__ __forceinline__ float append_scale(float amax) {
@@ -376,7 +382,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(
         // keys: a thread takes 8 elements of a token at a time; values: 8 of each of the four
         // tokens that share words of the turned rows.  One token alone (a decode step) is a few
         // lanes' work and branches over the rest, whose straight code costs more to fetch than
-        // to run: 64 tokens x 8 heads take 6.3 us through here, 8.8 us through the quads.
+        // to run: 64 tokens x 8 heads take 4.3 us through here, 5.3 us through the quads.
         uint4 kx[KP], vx[VP][4];
         uint32_t km = 0, vm = 0;
         bool k_odd = false, v_odd = false;
@@ -527,8 +533,8 @@ static hipError_t append_launch(const void* k, int64_t k_ts, int64_t k_hs, const
                                 void* k_cache, float* k_scales, void* v_cache, float* v_scales,
                                 int64_t pages, int32_t heads, hipStream_t stream) {
     // tokens per workgroup: one, until the launch would pass 2048 workgroups.  13240 tokens x 8
-    // heads: 41.3 us so, 40.5 with up to 4096, 69.5 with 8192 (all before the page size was a
-    // constant of the kernel).
+    // heads of 128 + 128: 25.1 us so, the same with up to 1024 or 4096, 35.4 with 8192; in pages of 128
+    // 30.3 us, and 32.5 with 4096.
     int run = 1;
     while (run < 64 && (T + run - 1) / run * heads > 2048) run *= 2;
     const dim3 grid((unsigned)((T + run - 1) / run), (unsigned)heads);

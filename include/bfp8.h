@@ -398,6 +398,9 @@ int bfp8_moe_combine(const void* expert_out_bf16, int64_t rows, const int32_t* s
  * to and including it exceed those left; one that wants no page is never
  * refused for lack of pages.  A refused request takes no page, its kv_len is
  * 0, its tokens keep their place in the token order (up to T).
+ * A caller that takes tokens back (rejected drafts) by a smaller ctx_lens also
+ * takes back the pages past ceil(ctx / page_size): their table entries are
+ * written again, and the pages are free for the caller to hand out.
  * Every output array is distinct from the inputs.  Deterministic.
  * Errors: BFP8_ERR_SHAPE if R < 0, T < 0, n_free < 0, table_width < 0,
  * T >= 2^31, n_free >= 2^31 or table_width * page_size >= 2^31;
@@ -469,7 +472,8 @@ int bfp8_kv_append(const void* k_bf16, int64_t k_token_stride, int64_t k_head_st
  *              16-byte aligned, any contents: partial results of token ranges;
  *              NULL lets every row's tokens be walked in one piece
  * Values stored in a visible page are finite codes, as bfp8_kv_append writes
- * them.  Deterministic.
+ * them.  Sums are fp32 and p may reach 2^8 in them: values beyond 2^100 may
+ * overflow in the rows that see them.  Deterministic.
  * Errors: BFP8_ERR_SHAPE if a size is negative, T >= 2^31, max_new < 1 (with R, T > 0),
  * heads_kv < 1, heads_q is no positive multiple of heads_kv, heads_q > 65535,
  * max_new * heads_q >= 2^31, num_pages or table_width times page_size >= 2^31,

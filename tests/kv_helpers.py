@@ -86,9 +86,10 @@ def attend(q, cache, table, q_off, kv_lens, max_new, scale, workspace=True, lse=
 
 
 def check_attention(out, lse, q, arrays, table, q_off, kv_lens, scale, what=""):
-    """Elementwise and in the mean.  The output is one bf16 rounding (2^-9 of the result) of a mean
-    whose weights are off by 2^-8 at most (the kernels' two terms of a weight stay far below) and by
-    the logits' fp32 error; rounded down weights do not add up in the mean."""
+    """Elementwise and in the mean.  The bounds leave room for weights that are off by 2^-8 (the
+    kernels' two terms of a weight stay far below: kv_terms.bound) and for the logits' fp32 error.
+    The output's one bf16 rounding is 2^-8 of the result at most: 2^-9 stands here, and the room of
+    the weights takes the rest."""
     want, want_lse, weight, slack = ref.attention(q, *arrays, table, q_off, kv_lens, scale)
     got, got_lse = f64(out), f64(lse)
     rows = ~np.isnan(want_lse)
