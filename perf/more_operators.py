@@ -23,7 +23,6 @@ import torch
 own = False
 
 LATENT, ROPE = 512, 64
-TILE = 128           # tokens per tile of the plan's tile_offsets
 E4M3_MAX = 448.0
 AMAX_FLOOR = 1e-4
 EPS = 1e-6
@@ -233,7 +232,6 @@ def prepare(case, seed):
         return st
     live = np.where(new > 0, total, 0)
     st["q_offsets"], st["kv_lens"] = sums(new), torch.from_numpy(live).to(dev, torch.int32)
-    st["tile_offsets"] = sums(-(-live // TILE))
     if case["op"] == "append":
         t = torch.arange(T, device=dev)
         r = torch.searchsorted(st["q_offsets"].long(), t, right=True) - 1
@@ -377,8 +375,8 @@ def _run_own(st):
         st["lse"] = torch.empty(T, H, dtype=torch.float32, device=dev) if c["lse"] else None
         st["workspace"] = bfp8.attn_latent_workspace(st["R"], st["max_new"], H, dev)
     bfp8.bfp8_attn_latent(st["q_latent"], st["q_rope"], *cache, st["block_table"], st["q_offsets"],
-                          st["kv_lens"], st["tile_offsets"], st["max_new"], st["scale"], st["out"],
-                          st["lse"], st["workspace"])
+                          st["kv_lens"], st["max_new"], st["scale"], st["out"], st["lse"],
+                          st["workspace"])
     return [st["out"], st["lse"]] if c["lse"] else [st["out"]]
 
 
