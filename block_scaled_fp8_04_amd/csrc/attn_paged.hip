@@ -23,6 +23,7 @@
 // is exact.
 #include <algorithm>
 
+#include "attn_common.hpp"
 #include "device_codec.hpp"
 #include "internal.hpp"
 #include "tile_common.hpp"
@@ -36,23 +37,6 @@ constexpr int kCols = 16;                     // query columns of a wave
 // others widen the codes once for 128 or 256 columns.  32 requests x 4096 tokens x 8 heads of 128:
 // 64 columns take 174 us by the former and 178 by the latter, 96 columns 260 and 182.
 constexpr int kSplitMaxCols = 64;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-__device__ __forceinline__ float neg_inf() { return __uint_as_float(0xFF800000u); }
-
-typedef __bf16 bf8v __attribute__((ext_vector_type(8)));
-typedef __bf16 bf2v __attribute__((ext_vector_type(2)));
-
-// Eight e4m3 codes (two registers) times a power of two, as bf16 (exact).
-__device__ __forceinline__ bf8v widen8(int w0, int w1, float scale) {
-    const bf2v a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, scale, false);
-    const bf2v b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, scale, true);
-    const bf2v c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, scale, false);
-    const bf2v d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, scale, true);
-    return bf8v{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
 // Eight fp32 as bf16 and the remainders as bf16.
 __device__ __forceinline__ void split8(const float (&p)[8], bf8v& hi, bf8v& lo) {
 #pragma unroll
@@ -60,24 +44,6 @@ __device__ __forceinline__ void split8(const float (&p)[8], bf8v& hi, bf8v& lo) 
         hi[j] = (__bf16)p[j];
         lo[j] = (__bf16)(p[j] - (float)hi[j]);
     }
-}
-
-// Eight elements of a bf16 query row (negated for a negative scale).
-__device__ __forceinline__ bf8v load_q8(const uint16_t* p, bool vec, bool negate) {
-    uint4 x;
-    if (vec) {
-        x = *(const uint4*)p;
-    } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = (uint32_t)p[2 * j] | ((uint32_t)p[2 * j + 1] << 16);
-        x = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    if (negate) {
-        asm volatile("");                                       // a branch: otherwise the load is waited for here
-        x = make_uint4(x.x ^ 0x80008000u, x.y ^ 0x80008000u, x.z ^ 0x80008000u, x.w ^ 0x80008000u);
-    }
-    return __builtin_bit_cast(bf8v, x);
 }
 
 // Reads through the scalar cache (uniform addresses): page numbers and scales.
@@ -88,21 +54,6 @@ typedef const __attribute__((address_space(4))) float* scalar_f32;
 __device__ __forceinline__ int64_t uniform(int64_t x) {
     return (int64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)x) |
            (int64_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32;
-}
-
-// x / y for 0 <= x < 2^52, 0 < y, a quotient below 2^31: by the reciprocal in 64-bit floating point,
-// refined twice, which is off by one at most.  The compiler's 64-bit division takes a kilobyte of
-// code, and what a short call spends its time on is code that it runs for the first time.
-__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
-    const double d = (double)y;
-    double inv = __builtin_amdgcn_rcp(d);
-    inv = __builtin_fma(__builtin_fma(-d, inv, 1.0), inv, inv);
-    inv = __builtin_fma(__builtin_fma(-d, inv, 1.0), inv, inv);
-    int64_t q = (uint32_t)((double)x * inv);
-    const int64_t left = x - q * y;
-    if (left < 0) q -= 1;
-    if (left >= y) q += 1;
-    return q;
 }
 
 // Lengths reach 2^31 - 32 (pages of 32 tokens).  Pieces of `per` tokens that hold `tokens`, and the
@@ -167,9 +118,6 @@ struct Requests {
     }
 };
 static_assert(kKvMaxRequests <= 64 * 64, "a request is found in two steps of 64");
-
-// How many of the lanes' conditions hold, from the first lane on, less one; at least 0.
-__device__ __forceinline__ int last_of(bool holds) { return max(__popcll(__ballot(holds)) - 1, 0); }
 
 __device__ __forceinline__ bool q_vec(const AttnArgs& a) {
     return ((uintptr_t)a.q % 16) == 0 && ((a.q_ts | a.q_hs) % 8) == 0;
@@ -810,15 +758,6 @@ constexpr int kPartTokens = 256;
 constexpr float kSlack = 8.f;
 
 // x of the two halves of the wave: their maximum, their sum
-__device__ __forceinline__ float half_max(float x) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-}
-__device__ __forceinline__ float half_sum(float x) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-
 // Sum and maximum of the wave's values, in scalar registers.
 template <int kCtrl, int kRows>
 __device__ __forceinline__ int dpp(int x) { return __builtin_amdgcn_update_dpp(0, x, kCtrl, kRows, 0xF, false); }

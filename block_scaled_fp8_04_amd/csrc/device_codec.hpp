@@ -130,6 +130,14 @@ __device__ __forceinline__ float quotient(float x, float s, float r) {
     return __builtin_copysignf(__builtin_fmaf(e, r, y0), x);
 }
 
+// Power-of-two scale of a block: the least one that keeps amax / scale (of max(amax, floor)) to 448.
+__device__ __forceinline__ float pow2_scale(float amax) {
+    const float y = fmaxf(amax, kAmaxFloor) / kE4m3Max;      // correctly rounded
+    uint32_t e = __float_as_uint(y) >> 23;
+    if (__float_as_uint(y) & 0x7FFFFFu) e += 1;
+    return __uint_as_float(e << 23);
+}
+
 // An fp32 value rounded to bf16 (nearest even, the conversion every bf16
 // output uses) and widened back.
 __device__ __forceinline__ float bf16_round_f32(float x) {

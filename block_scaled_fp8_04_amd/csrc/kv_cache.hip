@@ -225,13 +225,6 @@ hipError_t launch_kv_plan(const int32_t* ctx_lens, const int32_t* new_lens, int6
 // Values turned by words instead of bytes bought the most (121 us); 512 threads take 28.9 and 5.6 us.
 constexpr int kAppendThreads = 256;
 
-__device__ __forceinline__ float append_scale(float amax) {
-    const float y = fmaxf(amax, kAmaxFloor) / kE4m3Max;      // correctly rounded
-    uint32_t e = __float_as_uint(y) >> 23;
-    if (__float_as_uint(y) & 0x7FFFFFu) e += 1;
-    return __uint_as_float(e << 23);
-}
-
 // Eight bf16 of a token's row; kVec: one 16-byte load.
 template <bool kVec>
 __device__ __forceinline__ uint4 load8(const uint16_t* p) {
@@ -441,8 +434,8 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(
             km = max(km, red[0][w]);
             vm = max(vm, red[1][w]);
         }
-        float ks = append_scale(__uint_as_float(km << 16));
-        float vs = append_scale(__uint_as_float(vm << 16));
+        float ks = pow2_scale(__uint_as_float(km << 16));
+        float vs = pow2_scale(__uint_as_float(vm << 16));
         if (off > 0) {
             if (ks > ko) {
                 const float ratio = ko / ks;
