@@ -21,4 +21,7 @@ from ._lib import (  # noqa: F401
     KV_MAX_REQUESTS, KV_TILE, KVPlan, attn_paged, attn_paged_workspace, bfp8_attn_paged,
     bfp8_attn_paged_workspace_size, bfp8_kv_append, bfp8_kv_plan, kv_cache_buffers, kv_plan,
     kv_plan_buffers,
+    LATENT, LATENT_ROPE, ROPE_MAX_DIM, attn_latent, attn_latent_workspace, bfp8_attn_latent,
+    bfp8_attn_latent_workspace_size, bfp8_latent_append, bfp8_latent_gather, bfp8_rope, latent_cache_buffers,
+    latent_gather, rope, rope_frequencies,
 )

@@ -8,6 +8,7 @@ no fallback: if the library is missing the call raises.
 """
 import contextlib
 import ctypes
+import math
 import os
 from typing import NamedTuple
 
@@ -36,6 +37,11 @@ NOALLOC_SCRATCH_BYTES = 64 << 20
 KV_MAX_REQUESTS = 4096
 KV_TILE = 128
 
+# widths of the latent cache, and the largest head that bfp8_rope rotates (include/bfp8.h)
+LATENT = 512
+LATENT_ROPE = 64
+ROPE_MAX_DIM = 1024
+
 EXPORTS = ("bfp8_act_quant", "bfp8_weight_dequant", "bfp8_gemm", "bfp8_gemm_workspace_size",
            "bfp8_gemm_grouped", "bfp8_e4m3_encode_range", "bfp8_bf16_round_range",
            "bfp8_gemm_kernel_name", "bfp8_moe_dispatch_workspace_size", "bfp8_moe_dispatch",
@@ -43,6 +49,8 @@ EXPORTS = ("bfp8_act_quant", "bfp8_weight_dequant", "bfp8_gemm", "bfp8_gemm_work
            "bfp8_gemm_act_quant", "bfp8_gemm_swiglu_act_quant", "bfp8_act_quant_ue8m0",
            "bfp8_gemm_ue8m0", "bfp8_gemm_ue8m0_workspace_size", "bfp8_linear_fp8_workspace_size", "bfp8_linear_fp8", "bfp8_gemm_noalloc",
            "bfp8_kv_plan", "bfp8_kv_append", "bfp8_attn_paged", "bfp8_attn_paged_workspace_size",
+           "bfp8_rope", "bfp8_latent_append", "bfp8_latent_gather", "bfp8_attn_latent",
+           "bfp8_attn_latent_workspace_size",
            "bfp8_status_string", "bfp8_version")
 
 _lib = None
@@ -119,6 +127,17 @@ def library():
     lib.bfp8_attn_paged.restype = ctypes.c_int
     lib.bfp8_attn_paged_workspace_size.argtypes = [I64, I64, I32, I32, I32, I32]
     lib.bfp8_attn_paged_workspace_size.restype = SZ
+    lib.bfp8_rope.argtypes = [P, I64, I64, P, P, P, I64, I64, I64, I32, I32, I32, F32, P]
+    lib.bfp8_rope.restype = ctypes.c_int
+    lib.bfp8_latent_append.argtypes = [P, I64, P, F32, P, P, P, I32, F32, I64, P, P, P, I64, I32, P]
+    lib.bfp8_latent_append.restype = ctypes.c_int
+    lib.bfp8_latent_gather.argtypes = [P, P, P, I64, I32, P, I64, P, P, I64, I64, P, I64, P, I64, P]
+    lib.bfp8_latent_gather.restype = ctypes.c_int
+    lib.bfp8_attn_latent.argtypes = [P, I64, I64, P, I64, I64, P, P, P, I64, I32, P, I64, P, P, I64, I64,
+                                     I64, I32, F32, P, I64, I64, P, P, SZ, P]
+    lib.bfp8_attn_latent.restype = ctypes.c_int
+    lib.bfp8_attn_latent_workspace_size.argtypes = [I64, I64, I32]
+    lib.bfp8_attn_latent_workspace_size.restype = SZ
     lib.bfp8_status_string.argtypes = [ctypes.c_int]
     lib.bfp8_status_string.restype = ctypes.c_char_p
     lib.bfp8_version.argtypes = []
@@ -613,6 +632,169 @@ def bfp8_attn_paged(q, k_cache, k_scales, v_cache, v_scales, block_table, q_offs
         workspace.data_ptr() if workspace is not None else None, ws_bytes, _stream(stream, dev)))
 
 
+# ------------------------------------- rotary positions, attention over a shared latent
+
+def rope_frequencies(dim, base=10000.0, factor=1.0, trained_len=4096, fast=32.0, slow=1.0, device="cuda"):
+    """Inverse frequencies fp32 [dim / 2] of rotary positions, and the amplitude that goes with them.
+
+    factor > 1 stretches a model trained on trained_len tokens to factor times as many: a pair that
+    makes fewer than `slow` turns in trained_len has its frequency divided by factor, one that makes
+    more than `fast` keeps it, in between they are mixed linearly over the pair's number; the
+    amplitude is 0.1 ln(factor) + 1 (1 without scaling)."""
+    _need(dim >= 2 and dim % 2 == 0, "dim must be even")
+    _need(factor >= 1.0 and trained_len > 0 and fast >= slow > 0 and base > 1.0,
+          "factor >= 1, trained_len > 0, fast >= slow > 0 and base > 1")
+    i = torch.arange(dim // 2, dtype=torch.float64)
+    freq = float(base) ** (-2.0 * i / dim)
+    if factor == 1.0:
+        return freq.to(device, torch.float32), 1.0
+
+    def pair_with(turns):                  # the pair that makes this many turns, as a real number
+        return dim * math.log(trained_len / (turns * 2 * math.pi)) / (2 * math.log(base))
+    lo, hi = max(math.floor(pair_with(fast)), 0), min(math.ceil(pair_with(slow)), dim // 2 - 1)
+    stretched = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+    freq = freq / factor * stretched + freq * (1 - stretched)
+    return freq.to(device, torch.float32), 0.1 * math.log(factor) + 1.0
+
+
+def _need_rows(device, *named):
+    """bf16 tensors on the call's GPU, whose last dim is contiguous."""
+    gpu = device.index
+    for name, t in named:
+        if t.dtype is not torch.bfloat16 or t.get_device() != gpu:
+            raise ValueError(f"{name} must be bf16, on the call's GPU")
+        if t.shape[-1] > 1 and t.stride(-1) != 1 and t.numel() > 0:
+            raise ValueError(f"{name} must have contiguous rows")
+
+
+def bfp8_rope(x, positions, inv_freq, out, interleaved=False, amplitude=1.0, stream=None):
+    """out bf16 [T, H, D] = x bf16 [T, H, D] (any token and head strides) turned by positions int32 [T]
+    times inv_freq fp32 [D/2]; out may be x itself.  x[..., first:first + D] rotates part of a head."""
+    dev = x.device
+    _need(x.is_cuda, "all tensors must be on the GPU")
+    _need(x.dim() == 3 and out.shape == x.shape, "x and out must be [T, H, D]")
+    T, H, D = x.shape
+    _need_rows(dev, ("x", x), ("out", out))
+    _need_i32(dev, ("positions", positions, (T,)))
+    _need(inv_freq.dtype is torch.float32 and inv_freq.shape == (D // 2,) and inv_freq.device == dev and
+          inv_freq.is_contiguous(), "inv_freq must be a contiguous fp32 [D/2] on x's GPU")
+    xs, ys = x.stride(), out.stride()
+    _check("bfp8_rope", library().bfp8_rope(
+        x.data_ptr(), xs[0], xs[1], positions.data_ptr(), inv_freq.data_ptr(), out.data_ptr(), ys[0],
+        ys[1], T, H, D, 1 if interleaved else 0, amplitude, _stream(stream, dev)))
+
+
+def latent_cache_buffers(num_pages, page_size, device):
+    """(latent_cache uint8 [P, B, 512], latent_scales fp32 [P, B], rope_cache bf16 [P, B, 64]) of one layer."""
+    return (torch.empty(num_pages, page_size, LATENT, dtype=torch.uint8, device=device),
+            torch.empty(num_pages, page_size, dtype=torch.float32, device=device),
+            torch.empty(num_pages, page_size, LATENT_ROPE, dtype=torch.bfloat16, device=device))
+
+
+def _latent_shape(device, latent_cache, latent_scales, rope_cache):
+    """(P, B) of a layer's latent cache, checked."""
+    if latent_cache.dtype is not torch.uint8 and latent_cache.dtype is not torch.float8_e4m3fn:
+        raise TypeError(f"expected e4m3 codes (uint8 or float8_e4m3fn), got {latent_cache.dtype}")
+    _need(latent_cache.dim() == 3 and latent_cache.shape[2] == LATENT, "latent_cache must be [P, B, 512]")
+    P, B, _ = latent_cache.shape
+    _need(latent_scales.dtype is torch.float32 and latent_scales.shape == (P, B),
+          "latent_scales must be fp32 [P, B]")
+    _need(rope_cache.dtype is torch.bfloat16 and rope_cache.shape == (P, B, LATENT_ROPE),
+          "rope_cache must be bf16 [P, B, 64]")
+    gpu = device.index
+    for t in (latent_cache, latent_scales, rope_cache):
+        if t.get_device() != gpu or not t.is_contiguous():
+            raise ValueError("the cache must be contiguous, on the call's GPU")
+    return P, B
+
+
+def bfp8_latent_append(kv, slot_map, positions, inv_freq, latent_cache, latent_scales, rope_cache,
+                       norm_weight=None, eps=1e-6, interleaved=True, amplitude=1.0, stream=None):
+    """Rows kv bf16 [T, 576] (any token stride) into the slots of slot_map int32 [T] (in place): the
+    first 512 dims normed by norm_weight bf16 [512] (None: as they are) and quantized, the last 64
+    rotated as by bfp8_rope at positions int32 [T]."""
+    dev = kv.device
+    _need(kv.is_cuda, "all tensors must be on the GPU")
+    P, B = _latent_shape(dev, latent_cache, latent_scales, rope_cache)
+    T = slot_map.shape[0]
+    _need(kv.shape == (T, LATENT + LATENT_ROPE), "kv must be [T, 576]")
+    _need_rows(dev, ("kv", kv))
+    _need_i32(dev, ("slot_map", slot_map, (T,)), ("positions", positions, (T,)))
+    _need(inv_freq.dtype is torch.float32 and inv_freq.shape == (LATENT_ROPE // 2,) and inv_freq.device == dev and
+          inv_freq.is_contiguous(), "inv_freq must be a contiguous fp32 [32] on kv's GPU")
+    if norm_weight is not None:
+        _need(norm_weight.shape == (LATENT,) and norm_weight.is_contiguous(), "norm_weight must be a contiguous [512]")
+        _need_rows(dev, ("norm_weight", norm_weight))
+    _check("bfp8_latent_append", library().bfp8_latent_append(
+        kv.data_ptr(), kv.stride(0), norm_weight.data_ptr() if norm_weight is not None else None, eps,
+        slot_map.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), 1 if interleaved else 0, amplitude, T,
+        latent_cache.data_ptr(), latent_scales.data_ptr(), rope_cache.data_ptr(), P, B, _stream(stream, dev)))
+
+
+def bfp8_latent_gather(latent_cache, latent_scales, rope_cache, block_table, row_offsets, latent, rope,
+                       starts=None, stream=None):
+    """Request r's tokens (from starts[r] on) back to rows row_offsets[r] .. row_offsets[r+1] of latent
+    bf16 [N, 512] and rope bf16 [N, 64] (any row strides that are multiples of 8)."""
+    dev = latent_cache.device
+    _need(latent_cache.is_cuda, "all tensors must be on the GPU")
+    P, B = _latent_shape(dev, latent_cache, latent_scales, rope_cache)
+    _need(block_table.dim() == 2, "block_table must be [R, W]")
+    R, W = block_table.shape
+    N = latent.shape[0]
+    _need(latent.shape == (N, LATENT) and rope.shape == (N, LATENT_ROPE), "latent must be [N, 512], rope [N, 64]")
+    _need_rows(dev, ("latent", latent), ("rope", rope))
+    _need_i32(dev, ("block_table", block_table, None), ("row_offsets", row_offsets, (R + 1,)))
+    if starts is not None:
+        _need_i32(dev, ("starts", starts, (R,)))
+    _check("bfp8_latent_gather", library().bfp8_latent_gather(
+        latent_cache.data_ptr(), latent_scales.data_ptr(), rope_cache.data_ptr(), P, B, block_table.data_ptr(), W,
+        row_offsets.data_ptr(), starts.data_ptr() if starts is not None else None, R, N, latent.data_ptr(),
+        latent.stride(0), rope.data_ptr(), rope.stride(0), _stream(stream, dev)))
+
+
+def bfp8_attn_latent_workspace_size(R, max_new, heads) -> int:
+    return int(library().bfp8_attn_latent_workspace_size(int(R), int(max_new), int(heads)))
+
+
+def attn_latent_workspace(R, max_new, heads, device):
+    """A workspace for bfp8_attn_latent at these sizes."""
+    n = bfp8_attn_latent_workspace_size(R, max_new, heads)
+    return torch.empty(max(16, n), dtype=torch.uint8, device=device)
+
+
+def bfp8_attn_latent(q_latent, q_rope, latent_cache, latent_scales, rope_cache, block_table, q_offsets, kv_lens,
+                     max_new, scale, out, lse=None, workspace=None, stream=None):
+    """out bf16 [T, H, 512] (and lse fp32 [T, H]) = causal attention of each request's new tokens, q_latent
+    bf16 [T, H, 512] and q_rope bf16 [T, H, 64], over its latents.  q_offsets and kv_lens come from
+    bfp8_kv_plan; max_new bounds the requests' new tokens.  Any token and head strides."""
+    dev = q_latent.device
+    _need(q_latent.is_cuda, "all tensors must be on the GPU")
+    P, B = _latent_shape(dev, latent_cache, latent_scales, rope_cache)
+    _need(q_latent.dim() == 3 and q_latent.shape[2] == LATENT, "q_latent must be [T, H, 512]")
+    T, H, _ = q_latent.shape
+    _need(q_rope.shape == (T, H, LATENT_ROPE) and out.shape == (T, H, LATENT),
+          "q_rope must be [T, H, 64], out [T, H, 512]")
+    _need_rows(dev, ("q_latent", q_latent), ("q_rope", q_rope), ("out", out))
+    _need(block_table.dim() == 2, "block_table must be [R, W]")
+    R, W = block_table.shape
+    _need_i32(dev, ("block_table", block_table, None), ("q_offsets", q_offsets, (R + 1,)),
+              ("kv_lens", kv_lens, (R,)))
+    if lse is not None:
+        _need(lse.dtype is torch.float32 and lse.shape == (T, H) and lse.device == dev and
+              lse.is_contiguous(), "lse must be a contiguous fp32 [T, H] on q_latent's GPU")
+    ws_bytes = 0
+    if workspace is not None:
+        _need(workspace.device == dev and workspace.is_contiguous(), "workspace must be on q_latent's GPU")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    ql, qr, os_ = q_latent.stride(), q_rope.stride(), out.stride()
+    _check("bfp8_attn_latent", library().bfp8_attn_latent(
+        q_latent.data_ptr(), ql[0], ql[1], q_rope.data_ptr(), qr[0], qr[1], latent_cache.data_ptr(),
+        latent_scales.data_ptr(), rope_cache.data_ptr(), P, B, block_table.data_ptr(), W, q_offsets.data_ptr(),
+        kv_lens.data_ptr(), R, T, max_new, H, scale, out.data_ptr(), os_[0], os_[1],
+        lse.data_ptr() if lse is not None else None, workspace.data_ptr() if workspace is not None else None,
+        ws_bytes, _stream(stream, dev)))
+
+
 # ------------------------------------------------------- allocating conveniences
 #
 # New arrays belong to the stream that is given, as if made under torch.cuda.stream(stream).
@@ -764,4 +946,36 @@ def attn_paged(q, cache, block_table, plan, max_new, scale=None, workspace=None,
             workspace = attn_paged_workspace(block_table.shape[0], max_new, Hq, H, dk, dv, q.device)
         bfp8_attn_paged(q, *cache, block_table, plan.q_offsets, plan.kv_lens, plan.tile_offsets, max_new,
                         dk ** -0.5 if scale is None else scale, out, None, workspace, stream)
+        return out
+
+
+def rope(x, positions, inv_freq, interleaved=False, amplitude=1.0, stream=None):
+    """bfp8_rope into a new array; rows of tokens without a position (negative) are zero."""
+    with _allocating_on(stream, x.device):
+        out = torch.zeros(x.shape, dtype=torch.bfloat16, device=x.device)
+        bfp8_rope(x, positions, inv_freq, out, interleaved, amplitude, stream)
+        return out
+
+
+def latent_gather(cache, block_table, row_offsets, rows, starts=None, stream=None):
+    """bfp8_latent_gather of a layer's cache (latent_cache_buffers) into new arrays of `rows` rows:
+    (latent bf16 [rows, 512], rope bf16 [rows, 64]); rows of no request are zero."""
+    dev = block_table.device
+    with _allocating_on(stream, dev):
+        latent = torch.zeros((rows, LATENT), dtype=torch.bfloat16, device=dev)
+        rope_out = torch.zeros((rows, LATENT_ROPE), dtype=torch.bfloat16, device=dev)
+        bfp8_latent_gather(*cache, block_table, row_offsets, latent, rope_out, starts, stream)
+        return latent, rope_out
+
+
+def attn_latent(q_latent, q_rope, cache, block_table, plan, max_new, scale, workspace=None, stream=None):
+    """Attention over a layer's latent cache (latent_cache_buffers) as planned by kv_plan.  Returns out bf16
+    [T, H, 512]; rows of no request are zero."""
+    T, H, _ = q_latent.shape
+    with _allocating_on(stream, q_latent.device):
+        out = torch.zeros((T, H, LATENT), dtype=torch.bfloat16, device=q_latent.device)
+        if workspace is None:
+            workspace = attn_latent_workspace(block_table.shape[0], max_new, H, q_latent.device)
+        bfp8_attn_latent(q_latent, q_rope, *cache, block_table, plan.q_offsets, plan.kv_lens, max_new, scale, out,
+                         None, workspace, stream)
         return out

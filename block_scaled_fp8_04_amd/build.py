@@ -14,7 +14,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIBRARY = os.path.join(HERE, "libbfp8.so")
 SOURCES = ["api.hip", "quant.hip", "dequant.hip", "gemm.hip", "grouped.hip", "gemm_bf16.hip",
-           "moe.hip", "kv_cache.hip", "attn_paged.hip"]
+           "moe.hip", "kv_cache.hip", "attn_paged.hip", "rope.hip", "latent_cache.hip",
+           "attn_latent.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # -O3, no fast-math: fp32 division stays correctly rounded (act_quant relies on
@@ -22,8 +23,9 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-fno-gpu-rdc", "-Wall", "-Wno-unused-result"]
-# extra hipcc flags for single sources (none at present)
-PER_FILE = {}
+# extra hipcc flags for single sources.  attn_latent: matrix instructions write vector registers, and
+# the accumulation registers hold its queries; the other way round the loops spill.
+PER_FILE = {"attn_latent.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 # hipcc's host pass does not know the device-only packed-fp32 feature and says so
 NOISE = "is not a recognized feature for this target"
 

@@ -404,6 +404,148 @@ int bfp8_attn_paged(const void* q_bf16, int64_t q_token_stride, int64_t q_head_s
     return from_hip(bfp8::launch_attn_paged(a, dk, dv, (hipStream_t)stream));
 }
 
+static bool finite_f(float x) { return x - x == 0.0f; }
+
+int bfp8_rope(const void* x_bf16, int64_t x_token_stride, int64_t x_head_stride,
+              const int32_t* positions, const float* inv_freq, void* out_bf16,
+              int64_t out_token_stride, int64_t out_head_stride, int64_t T, int32_t heads,
+              int32_t dim, int32_t interleaved, float amplitude, void* stream) {
+    static_assert(BFP8_ROPE_MAX_DIM == bfp8::kRopeMaxDim, "largest rotated head");
+    if (!finite_f(amplitude)) return BFP8_ERR_ARG;
+    if (T < 0 || T >= ((int64_t)1 << 24) || heads < 1 || heads > 65535 || dim < 2 || dim % 2 != 0 ||
+        dim > BFP8_ROPE_MAX_DIM || x_token_stride < 0 || x_head_stride < 0 ||
+        out_token_stride < 0 || out_head_stride < 0)
+        return BFP8_ERR_SHAPE;
+    if (T == 0) return BFP8_OK;
+    if (!x_bf16 || !positions || !inv_freq || !out_bf16) return BFP8_ERR_NULL;
+    if (!aligned(x_bf16, 2) || !aligned(out_bf16, 2) || !aligned(positions, 4) ||
+        !aligned(inv_freq, 4))
+        return BFP8_ERR_ALIGN;
+    return from_hip(bfp8::launch_rope(x_bf16, x_token_stride, x_head_stride, positions, inv_freq,
+                                      out_bf16, out_token_stride, out_head_stride, T, heads, dim,
+                                      interleaved != 0, amplitude, (hipStream_t)stream));
+}
+
+int bfp8_latent_append(const void* kv_bf16, int64_t kv_token_stride, const void* norm_weight,
+                       float eps, const int32_t* slot_map, const int32_t* positions,
+                       const float* inv_freq, int32_t interleaved, float amplitude, int64_t T,
+                       void* latent_cache, float* latent_scales, void* rope_cache,
+                       int64_t num_pages, int32_t page_size, void* stream) {
+    static_assert(BFP8_LATENT == bfp8::kLatent && BFP8_LATENT_ROPE == bfp8::kLatentRope,
+                  "latent widths");
+    if (!kv_page_ok(page_size) || !finite_f(amplitude) || !finite_f(eps) || eps < 0.0f)
+        return BFP8_ERR_ARG;
+    if (T < 0 || T >= ((int64_t)1 << 26) || kv_token_stride < 0 || !kv_slots_ok(num_pages, page_size))
+        return BFP8_ERR_SHAPE;
+    if (T == 0 || num_pages == 0) return BFP8_OK;
+    if (!kv_bf16 || !slot_map || !positions || !inv_freq || !latent_cache || !latent_scales ||
+        !rope_cache)
+        return BFP8_ERR_NULL;
+    if (!aligned(kv_bf16, 2) || !aligned(norm_weight, 2) || !aligned(slot_map, 4) ||
+        !aligned(positions, 4) || !aligned(inv_freq, 4) || !aligned(latent_cache, 16) ||
+        !aligned(latent_scales, 4) || !aligned(rope_cache, 16))
+        return BFP8_ERR_ALIGN;
+    return from_hip(bfp8::launch_latent_append(kv_bf16, kv_token_stride, norm_weight, eps, slot_map,
+                                               positions, inv_freq, interleaved != 0, amplitude, T,
+                                               latent_cache, latent_scales, rope_cache,
+                                               num_pages * page_size, (hipStream_t)stream));
+}
+
+int bfp8_latent_gather(const void* latent_cache, const float* latent_scales,
+                       const void* rope_cache, int64_t num_pages, int32_t page_size,
+                       const int32_t* block_table, int64_t table_width,
+                       const int32_t* row_offsets, const int32_t* starts, int64_t R, int64_t rows,
+                       void* latent_out, int64_t latent_row_stride, void* rope_out,
+                       int64_t rope_row_stride, void* stream) {
+    if (!kv_page_ok(page_size)) return BFP8_ERR_ARG;
+    if (R < 0 || rows < 0 || rows >= ((int64_t)1 << 30) || !kv_slots_ok(num_pages, page_size) ||
+        !kv_slots_ok(table_width, page_size) || latent_row_stride < 0 || rope_row_stride < 0)
+        return BFP8_ERR_SHAPE;
+    if (R > BFP8_KV_MAX_REQUESTS) return BFP8_ERR_GROUPS;
+    if (R == 0 || rows == 0 || num_pages == 0 || table_width == 0) return BFP8_OK;
+    if (!latent_cache || !latent_scales || !rope_cache || !block_table || !row_offsets ||
+        !latent_out || !rope_out)
+        return BFP8_ERR_NULL;
+    if (!aligned(latent_cache, 16) || !aligned(latent_scales, 4) || !aligned(rope_cache, 16) ||
+        !aligned(block_table, 4) || !aligned(row_offsets, 4) || !aligned(starts, 4) ||
+        !aligned(latent_out, 16) || !aligned(rope_out, 16) || latent_row_stride % 8 != 0 ||
+        rope_row_stride % 8 != 0)
+        return BFP8_ERR_ALIGN;
+    return from_hip(bfp8::launch_latent_gather(latent_cache, latent_scales, rope_cache, num_pages,
+                                               page_size, block_table, table_width, row_offsets,
+                                               starts, R, rows, latent_out, latent_row_stride,
+                                               rope_out, rope_row_stride, (hipStream_t)stream));
+}
+
+static bool latent_sizes_ok(int64_t R, int64_t max_new, int32_t heads) {
+    return R >= 0 && max_new >= 0 && heads >= 1 && heads <= 65535 &&
+           max_new < ((int64_t)1 << 31) / heads;
+}
+
+size_t bfp8_attn_latent_workspace_size(int64_t R, int64_t max_new, int32_t heads) {
+    if (!latent_sizes_ok(R, max_new, heads) || R == 0 || max_new == 0 || R > BFP8_KV_MAX_REQUESTS)
+        return 0;
+    return bfp8::attn_latent_workspace_bytes(R, max_new, heads);
+}
+
+int bfp8_attn_latent(const void* q_latent_bf16, int64_t ql_token_stride, int64_t ql_head_stride,
+                     const void* q_rope_bf16, int64_t qr_token_stride, int64_t qr_head_stride,
+                     const void* latent_cache, const float* latent_scales, const void* rope_cache,
+                     int64_t num_pages, int32_t page_size, const int32_t* block_table,
+                     int64_t table_width, const int32_t* q_offsets, const int32_t* kv_lens,
+                     int64_t R, int64_t T, int64_t max_new, int32_t heads, float scale,
+                     void* out_bf16, int64_t out_token_stride, int64_t out_head_stride, float* lse,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+    if (!kv_page_ok(page_size) || !finite_f(scale)) return BFP8_ERR_ARG;
+    if (!latent_sizes_ok(R, max_new, heads) || T < 0 || T >= ((int64_t)1 << 29) / heads ||
+        ql_token_stride < 0 || ql_head_stride < 0 || qr_token_stride < 0 || qr_head_stride < 0 ||
+        out_token_stride < 0 || out_head_stride < 0 || !kv_slots_ok(num_pages, page_size) ||
+        !kv_slots_ok(table_width, page_size))
+        return BFP8_ERR_SHAPE;
+    if (R > BFP8_KV_MAX_REQUESTS) return BFP8_ERR_GROUPS;
+    if (R == 0 || T == 0) return BFP8_OK;
+    if (max_new < 1) return BFP8_ERR_SHAPE;
+    if (!q_latent_bf16 || !q_rope_bf16 || !q_offsets || !kv_lens || !out_bf16) return BFP8_ERR_NULL;
+    if (num_pages > 0 && table_width > 0 &&
+        (!latent_cache || !latent_scales || !rope_cache || !block_table))
+        return BFP8_ERR_NULL;
+    if (!aligned(q_latent_bf16, 2) || !aligned(q_rope_bf16, 2) || !aligned(latent_cache, 16) ||
+        !aligned(latent_scales, 4) || !aligned(rope_cache, 16) || !aligned(block_table, 4) ||
+        !aligned(q_offsets, 4) || !aligned(kv_lens, 4) || !aligned(out_bf16, 16) ||
+        out_token_stride % 8 != 0 || out_head_stride % 8 != 0 || !aligned(lse, 4) ||
+        !aligned(workspace, 16))
+        return BFP8_ERR_ALIGN;
+    if (workspace && workspace_bytes < bfp8::attn_latent_workspace_bytes(R, max_new, heads))
+        return BFP8_ERR_WORKSPACE;
+    bfp8::LatentArgs a;
+    a.q_latent = (const uint16_t*)q_latent_bf16;
+    a.ql_ts = ql_token_stride;
+    a.ql_hs = ql_head_stride;
+    a.q_rope = (const uint16_t*)q_rope_bf16;
+    a.qr_ts = qr_token_stride;
+    a.qr_hs = qr_head_stride;
+    a.codes = (const uint8_t*)latent_cache;
+    a.scales = latent_scales;
+    a.rope = (const uint16_t*)rope_cache;
+    a.pages = num_pages;
+    a.block_table = block_table;
+    a.width = num_pages > 0 ? table_width : 0;      // no pool: no request sees a token
+    a.q_offsets = q_offsets;
+    a.kv_lens = kv_lens;
+    a.R = (int)R;
+    a.heads = heads;
+    a.log_b = __builtin_ctz(page_size);
+    a.T = T;
+    a.max_new = max_new;
+    a.scale = scale;
+    a.out = (uint16_t*)out_bf16;
+    a.o_ts = out_token_stride;
+    a.o_hs = out_head_stride;
+    a.lse = lse;
+    a.ws = (float*)workspace;
+    return from_hip(bfp8::launch_attn_latent(a, (hipStream_t)stream));
+}
+
 const char* bfp8_gemm_kernel_name(int64_t M, int64_t N, int64_t K) {
     if (M <= 0 || N <= 0 || K <= 0 || K % BFP8_BLOCK != 0) return "none";
     return bfp8::gemm_config_name(bfp8::gemm_config(M, N, K));

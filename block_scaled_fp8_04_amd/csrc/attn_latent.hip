@@ -1,0 +1,772 @@
+// attn_latent.hip - attention whose keys and values are one shared latent per token (the absorbed
+// form of latent attention) over the paged latent cache, on gfx950.
+//
+//     x_t = scale (q_latent . c_t + q_rope . r_t),   out = sum_t p_t c_t / sum_t p_t,  p_t = exp(x_t - max)
+//
+// with c_t = 2^e_t times 512 e4m3 codes and r_t 64 bf16.  A query row is a (new token, head) pair:
+// every row of a request reads the same tokens, so a token is brought to LDS once and serves all
+// rows of a workgroup, as key and as value: 2176 operations per row for its 644 bytes.
+//
+// Both products are taken transposed, the cache as the first operand:
+//     S^T [token, row] = C Q^T + R Qr^T,     O^T [dim, row] += C^T P^T
+// so a lane holds one row's logits (lane & 31, tokens 8 i + 4 (lane / 32) + 0 .. 3 of 32), the softmax
+// needs one exchange between the wave's halves, and its results are the second product's operand
+// where they stand: that product sums over the tokens in the order in which the lanes hold them.
+// C^T comes from the same bytes of LDS through transposing reads (8 tokens of one dim a lane), whose
+// rows are given by address, so in that order too.
+//
+// Precision.  As keys, codes are widened to bf16 with their token's scale, exactly, and q is bf16 as
+// it comes.  As values they are widened to fp16 without it, exactly as well, and the scale goes into
+// the weight: the maximum is taken over x_t + e_t (in units of log 2), w_t = 2^(x_t + e_t - max) is
+// rounded to fp16 once (2^-12 of it, where a bf16 weight would lose 2^-9, as much as the rounding of
+// the output), and the norm sums w_t 2^-e_t before that rounding.  So a weight's size is that of the
+// token's contribution, and fp16's range is enough: what it drops is 2^-25 of the largest
+// contribution.  Logits, maxima, norms and sums are fp32; maxima are rounded up to integers, so that
+// rescaling by 2^(old - new) is exact.
+#include <algorithm>
+
+#include "attn_common.hpp"
+#include "device_codec.hpp"
+#include "internal.hpp"
+#include "tile_common.hpp"
+
+namespace bfp8 {
+
+typedef _Float16 h8v __attribute__((ext_vector_type(8)));
+typedef _Float16 h2v __attribute__((ext_vector_type(2)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) v2i* lds_v2i;
+
+constexpr int kLatThreads = 256;
+constexpr int kLatGroups = 256;               // workgroups of a split launch: one a CU (LDS, registers)
+constexpr int kLatItems = 512;                // most items of a split launch: beyond, they fill the chip
+constexpr int kLatTile = 64;                  // tokens of a tile
+constexpr int kLatCodes = kLatTile * kLatent; // its bytes of codes and of rotated keys
+constexpr int kLatLoads = 11;                 // a wave's reads of a tile that are counted
+constexpr int kLatStage = kLatCodes + kLatTile * kLatentRope * 2;
+// A maximum is followed only where it would be passed by more than this (in units of log 2): weights
+// reach 2^8, far inside fp16's range.
+constexpr float kLatSlack = 8.f;
+
+// The permutation of a row's 16-byte chunks in LDS: chunk c of row r lies at c ^ lat_swz(r).  Key
+// reads take the same chunk of 16 rows, all different here; transposing reads take two neighbouring
+// chunks of rows with equal bit 2, so that bit is the lowest and the other three keep pairs apart.
+__device__ __forceinline__ constexpr int lat_swz(int r) {
+    return (r & 3) << 1 | (r >> 3 & 1) << 3 | (r >> 2 & 1);
+}
+__device__ __forceinline__ constexpr int rope_swz(int r) { return r >> 1 & 7; }
+
+// Eight e4m3 codes as fp16 (exact).
+__device__ __forceinline__ h8v widen8_f16(int w0, int w1) {
+    const h2v a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.f, false);
+    const h2v b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w0, 1.f, true);
+    const h2v c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.f, false);
+    const h2v d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w1, 1.f, true);
+    return h8v{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// The workspace: parts of kLatSlots runs, (maximum, norm) of their rows, and the items' notes.
+constexpr int64_t kLatSlots = 2 * kLatGroups;
+__device__ __forceinline__ float2* latent_ml(const LatentArgs& a, int rows) {
+    return (float2*)(a.ws + kLatSlots * rows * kLatent);
+}
+__device__ __forceinline__ int2* latent_info(const LatentArgs& a, int rows) {
+    return (int2*)(latent_ml(a, rows) + kLatSlots * rows);
+}
+
+// Barrier behind everything that this wave wrote to LDS or has on its way there.
+__device__ __forceinline__ void barrier_all() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(7 << 4);                          // vmcnt 0, lgkmcnt 0
+    barrier_lds();
+}
+
+// A request's part in the launch: its first new token, its query rows and cached tokens.
+struct LatentItem {
+    int64_t q0;
+    int n, rows, kv_len;
+    static __device__ __forceinline__ LatentItem of(const LatentArgs& a, int from, int to, int kv_len) {
+        LatentItem it;
+        it.q0 = min(max((int64_t)from, (int64_t)0), a.T);
+        const int64_t q1 = min(max((int64_t)to, it.q0), a.T);
+        it.n = (int)(q1 - it.q0);
+        it.rows = (int)min((int64_t)it.n, a.max_new) * a.heads;
+        it.kv_len = (int)min(max((int64_t)kv_len, (int64_t)0), a.width << a.log_b);
+        return it;
+    }
+    // tokens that new token i sees
+    __device__ __forceinline__ int limit(int i) const { return min(kv_len, max(kv_len - n + i + 1, 0)); }
+};
+
+// Tiles of kLatTile tokens that hold this many (lengths reach 2^31 - 32).
+__device__ __forceinline__ int latent_tiles(int tokens) {
+    return (int)(((uint32_t)tokens + kLatTile - 1) / kLatTile);
+}
+
+// 64 consecutive requests, one per lane, and the units of work (tiles of their items) before each.
+template <int ROWS>
+struct LatentRequests {
+    int base, q0, q1, kv_len;
+    int64_t before, units;                           // before the lane's request; of it
+    __device__ __forceinline__ void load(const LatentArgs& a, int from) {
+        base = from;
+        const int mine = base + (int)(threadIdx.x & 63), r = min(mine, a.R - 1);
+        q0 = a.q_offsets[r];
+        q1 = a.q_offsets[r + 1];
+        kv_len = a.kv_lens[r];
+        const LatentItem it = LatentItem::of(a, q0, q1, kv_len);
+        units = mine < a.R ? (int64_t)((it.rows + ROWS - 1) / ROWS) * latent_tiles(it.kv_len) : 0;
+    }
+    // sums up the units, of which `start` come before the 64 requests; returns what comes before the next
+    __device__ __forceinline__ int64_t scan(int64_t start) {
+        const int lane = threadIdx.x & 63;
+        int64_t sum = units;
+#pragma unroll
+        for (int step = 1; step < 64; step <<= 1) {
+            const int64_t x = __shfl_up((long long)sum, step);
+            if (lane >= step) sum += x;
+        }
+        before = start + sum - units;
+        return start + from_lane(sum, 63);
+    }
+    static __device__ __forceinline__ int64_t from_lane(int64_t x, int lane) {
+        return (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)x, lane) |
+               (int64_t)__builtin_amdgcn_readlane((int)(x >> 32), lane) << 32;
+    }
+    __device__ __forceinline__ LatentItem item(const LatentArgs& a, int r) const {
+        return LatentItem::of(a, __builtin_amdgcn_readlane(q0, r - base), __builtin_amdgcn_readlane(q1, r - base),
+                              __builtin_amdgcn_readlane(kv_len, r - base));
+    }
+};
+
+// One workgroup's walk over a run of one item's tiles.  Its four waves are two by two:
+//   RW == 2 (64 rows): wave (rg, x) takes 32 rows; of each tile it forms the weights of half x of the
+//     tokens, trades them with the other wave of its rows through LDS, and sums half x of the dims
+//     over all tokens.
+//   RW == 1 (32 rows): wave (tg, x) takes half tg of each tile's tokens and sums half x of the dims
+//     over those; both waves of a half form its weights.  That is twice the work for the weights and
+//     no trade: with so few rows the cache's bytes are what counts.
+// (All dims in one wave would take 256 registers for O next to 144 for q: the compiler spills.)
+template <int RW>
+struct LatentWalk {
+    static constexpr int DT = 8;                     // blocks of 32 dims of a wave
+    static constexpr int ROWS = 32 * RW;
+
+    v16f o[DT];
+    float m, l;                                      // l: over this wave's tokens of this lane only
+    bf8v q[36];                                      // 32 of the latent, 4 of the rotated part
+    int rg, tg, dw;                                  // this wave's rows, tokens, dims
+
+    __device__ __forceinline__ void init() {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        dw = wave >> 1;
+        rg = RW == 2 ? wave & 1 : 0;
+        tg = RW == 2 ? dw : wave & 1;
+    }
+    // this lane's row, counted in the item
+    __device__ __forceinline__ int row(int rt) const { return rt * ROWS + rg * 32 + (threadIdx.x & 31); }
+
+    __device__ __forceinline__ void load_q(const LatentArgs& a, const LatentItem& it, int row) {
+        const int h = (threadIdx.x & 63) >> 5;
+        const bool negate = a.scale < 0.f;
+        if (row < it.rows) {
+            const int64_t t = it.q0 + row / a.heads;
+            const int j = row % a.heads;
+            const uint16_t* const ql = a.q_latent + t * a.ql_ts + (int64_t)j * a.ql_hs + 16 * h;
+            const uint16_t* const qr = a.q_rope + t * a.qr_ts + (int64_t)j * a.qr_hs + 8 * h;
+            const bool vl = ((uintptr_t)a.q_latent % 16) == 0 && ((a.ql_ts | a.ql_hs) % 8) == 0;
+            const bool vr = ((uintptr_t)a.q_rope % 16) == 0 && ((a.qr_ts | a.qr_hs) % 8) == 0;
+            // a 16-byte read of codes feeds two matrix instructions: dims 32 p + 16 h + 8 x ..
+#pragma unroll
+            for (int p = 0; p < 16; ++p)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) q[2 * p + x] = load_q8(ql + 32 * p + 8 * x, vl, negate);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) q[32 + s] = load_q8(qr + 16 * s, vr, negate);
+        } else {
+#pragma unroll
+            for (int s = 0; s < 36; ++s) q[s] = bf8v{0, 0, 0, 0, 0, 0, 0, 0};
+        }
+        // in accumulation registers, where the matrix instructions take them from
+#pragma unroll
+        for (int s = 0; s < 36; ++s) asm volatile("" : "+a"(q[s]));
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+        m = neg_inf();
+        l = 0.f;
+    }
+
+    // The table entry of the page that holds token `lane` of a tile (of the last page, behind the end).
+    static __device__ __forceinline__ int entry(const LatentArgs& a, int r, int tile, int kv_len) {
+        const int64_t pos = min((int64_t)tile * kLatTile + (threadIdx.x & 63), (int64_t)kv_len - 1);
+        return a.block_table[r * a.width + (pos >> a.log_b)];
+    }
+
+    // Requests a tile: each wave 16 of its tokens, by loads that go straight to LDS, and the scale of
+    // token `lane`.  not real: the loads lie outside their resource and read nothing.
+    static __device__ __forceinline__ float load(const LatentArgs& a, uint8_t* st, int tile, int entry, bool real) {
+        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int in_page = (1 << a.log_b) - 1;
+        const int64_t page = min(max((int64_t)entry, (int64_t)0), a.pages - 1);
+        const int64_t own = (int64_t)__builtin_amdgcn_readlane((int)page, 16 * wave) << a.log_b |
+                            ((int)((uint32_t)tile * kLatTile) + 16 * wave & in_page);
+        const __amdgpu_buffer_rsrc_t codes = make_rsrc(a.codes + own * kLatent, real ? 16 * kLatent : 0);
+        const __amdgpu_buffer_rsrc_t rope = make_rsrc(a.rope + own * kLatentRope, real ? 16 * kLatentRope * 2 : 0);
+        // row 2 k + hi of the wave's sixteen; the lane's place in LDS holds this chunk of it
+        const int hi = lane >> 5, at = hi * kLatent + (((lane & 31) ^ lat_swz(hi)) << 4);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            buf_lds16(codes, at ^ lat_swz(2 * k) << 4, k * 1024, st + wave * 8192 + k * 1024);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int row = 8 * k + (lane >> 3);
+            buf_lds16(rope, row * (kLatentRope * 2) + (((lane & 7) ^ rope_swz(row)) << 4), 0,
+                      st + kLatCodes + wave * 2048 + k * 1024);
+        }
+        return a.scales[real ? page << a.log_b | ((int)((uint32_t)tile * kLatTile) + lane & in_page) : 0];
+    }
+
+    // S^T of 32 tokens: rows of C are widened with their token's scale.
+    __device__ __forceinline__ v16f logits(const uint8_t* st, int b, float scale) const {
+        const int lane = threadIdx.x & 63, h = lane >> 5, row = 32 * b + (lane & 31);
+        const uint8_t* const c = st + row * kLatent;
+        const uint8_t* const r = st + kLatCodes + row * (kLatentRope * 2);
+        const int cs = lat_swz(row & 15), rs = rope_swz(row);
+        v16f s;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = 0.f;
+        constexpr int N = 20, AHEAD = 4;                         // reads, those on their way
+        uint4 w[N];
+        const auto read = [&](int p) {
+            return *(const uint4*)(p < 16 ? c + (((2 * p + h) ^ cs) << 4) : r + (((2 * (p - 16) + h) ^ rs) << 4));
+        };
+#pragma unroll
+        for (int p = 0; p < AHEAD; ++p) w[p] = read(p);
+#pragma unroll
+        for (int p = 0; p < N; ++p) {
+            __builtin_amdgcn_sched_barrier(0);                   // or all of them are read at once
+            if (p + AHEAD < N) w[p + AHEAD] = read(p + AHEAD);
+            if (p < 16) {
+                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen8((int)w[p].x, (int)w[p].y, scale), q[2 * p], s, 0,
+                                                            0, 0);
+                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen8((int)w[p].z, (int)w[p].w, scale), q[2 * p + 1], s,
+                                                            0, 0, 0);
+            } else {
+                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8v, w[p]), q[16 + p], s, 0, 0, 0);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        return s;
+    }
+
+    // Logits to exponents of two, with the tokens' scale exponents e (in LDS) added; tokens from
+    // `seen` on are hidden.  Returns the reference that this wave's next weights need.
+    __device__ __forceinline__ float exponents(v16f& s, const float* e, float c, int seen, bool masked) const {
+        const int h = (threadIdx.x & 63) >> 5;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const v4f ev = *(const v4f*)(e + 8 * i + 4 * h);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[4 * i + j] = __builtin_fmaf(s[4 * i + j], c, ev[j]);
+        }
+        if (masked) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (8 * (i >> 2) + 4 * h + (i & 3) >= seen) s[i] = neg_inf();
+        }
+        float top = s[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+        const float x = __builtin_ceilf(half_max(top));
+        return x > m + kLatSlack ? x : m;
+    }
+
+    // 2^(from - to) for references; 0 where there was none.
+    static __device__ __forceinline__ float shrink(float from, float to) {
+        return from == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(from - to);
+    }
+
+    // Weights of 32 tokens against the reference m, and their share of the norm (inv: inverse scales).
+    __device__ __forceinline__ void weights(const v16f& s, const float* inv, h8v (&w)[2]) {
+        const int h = (threadIdx.x & 63) >> 5;
+        const float ref = m == neg_inf() ? 0.f : m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const v4f iv = *(const v4f*)(inv + 8 * i + 4 * h);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float y = __builtin_amdgcn_exp2f(s[4 * i + j] - ref);
+                l = __builtin_fmaf(y, iv[j], l);
+                w[i >> 1][(i & 1) * 4 + j] = (_Float16)y;
+            }
+        }
+    }
+
+    // O^T += C^T P^T over N times 32 tokens, from block b on.
+    template <int N>
+    __device__ __forceinline__ void values(const uint8_t* st, int b, const h8v (&w)[2 * N]) {
+        const int lane = threadIdx.x & 63, h = lane >> 5, g = lane >> 4 & 1, i = lane >> 1 & 7;
+        // this lane's address is that of token T, 8 of 16 dims; it gets 8 tokens of dim lane & 31
+        const int T = (i & 3) + 8 * (i >> 2) + 4 * h;
+        const uint8_t* const c = st + (32 * b + T) * kLatent + (lane & 1) * 8;
+        const int cs = lat_swz(T) ^ g;
+        constexpr int READS = 2 * N * DT, AHEAD = 4;             // those on their way
+        v2i x[READS];
+        const auto read = [&](int n) {
+            const int chunk = 2 * (dw * DT + n % DT) ^ cs;
+            return __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i)(c + n / DT * 16 * kLatent + (chunk << 4)));
+        };
+#pragma unroll
+        for (int n = 0; n < AHEAD; ++n) x[n] = read(n);
+#pragma unroll
+        for (int n = 0; n < READS; ++n) {
+            __builtin_amdgcn_sched_barrier(0);
+            if (n + AHEAD < READS) x[n + AHEAD] = read(n + AHEAD);
+            o[n % DT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen8_f16(x[n][0], x[n][1]), w[n / DT], o[n % DT], 0,
+                                                               0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
+    // What a walk is about: everything but limit (tokens that this lane's row sees) is uniform.
+    struct Run {
+        int r, t0, t1, kv_len, limit, free_limit;    // free_limit: tokens that all rows see
+        float c;
+    };
+
+    // Bytes behind the last token may hold anything, and 0 * NaN is NaN.
+    static __device__ __forceinline__ void clear_tail(uint8_t* st, const Run& run, int tile) {
+        const int base = tile * kLatTile;
+        if (base <= run.kv_len - kLatTile) return;
+        const int from = max(run.kv_len - base, 0) * (kLatent / 16);
+        for (int x = from + threadIdx.x; x < kLatCodes / 16; x += kLatThreads)
+            *(uint4*)(st + x * 16) = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+    }
+
+    // A tile's exponents of this wave's half tg; the scale's exponents and inverses go to this wave's
+    // own bytes of LDS.
+    __device__ __forceinline__ float look(const uint8_t* st, float (*scale_lds)[kLatTile], const Run& run, int tile,
+                                          float sc, v16f& s) const {
+        const int lane = threadIdx.x & 63;
+        const uint32_t ex = __float_as_uint(sc) >> 23 & 255;
+        scale_lds[0][lane] = ex == 255 ? __uint_as_float(0x7FC00000u) : (float)((int)ex - 127);
+        scale_lds[1][lane] = ex == 255 ? 0.f : __uint_as_float((254 - ex) << 23);
+        __builtin_amdgcn_wave_barrier();
+        const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(sc), __float_as_uint(sc), false, false);
+        s = logits(st, tg, __uint_as_float(tg == 0 ? both[0] : both[1]));
+        const int base = tile * kLatTile;
+        return exponents(s, scale_lds[0] + 32 * tg, run.c, run.limit - base - 32 * tg, base > run.free_limit - kLatTile);
+    }
+
+    // RW == 1.  Two tiles are on their way while one is worked on.
+    __device__ __forceinline__ void walk_halves(const LatentArgs& a, uint8_t* st0, uint8_t* st1, uint8_t* st2,
+                                                float (*scale_lds)[kLatTile], const Run& run) {
+        const int t0 = run.t0, t1 = run.t1;
+        const int ent0 = entry(a, run.r, t0, run.kv_len), ent1 = entry(a, run.r, t0 + 1, run.kv_len);
+        int ent2 = entry(a, run.r, t0 + 2, run.kv_len);
+        float sc0 = load(a, st0, t0, ent0, true);
+        float sc1 = load(a, st1, t0 + 1, ent1, t0 + 1 < t1);
+        float sc2 = 0.f;
+        const auto step = [&](int tile, uint8_t* st, uint8_t* ahead, float sc, float& sc_ahead) __attribute__((always_inline)) {
+            wait_vmcnt<kLatLoads>();                             // all but the next tile's
+            barrier_lds();
+            __builtin_amdgcn_sched_barrier(0);
+            const int ent = ent2;
+            ent2 = entry(a, run.r, tile + 3, run.kv_len);
+            __builtin_amdgcn_sched_barrier(0);
+            sc_ahead = load(a, ahead, tile + 2, ent, tile + 2 < t1);
+            __builtin_amdgcn_sched_barrier(0);
+            clear_tail(st, run, tile);
+            v16f s;
+            const float m_new = look(st, scale_lds, run, tile, sc, s);
+            if (__any(m_new != m)) {
+                const float alpha = shrink(m, m_new);
+                l *= alpha;
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[d] *= alpha;
+                m = m_new;
+            }
+            h8v w[2];
+            weights(s, scale_lds[1] + 32 * tg, w);
+            values<1>(st, tg, w);
+        };
+        for (int tile = t0; tile < t1; tile += 3) {
+            step(tile, st0, st2, sc0, sc2);
+            if (tile + 1 < t1) step(tile + 1, st1, st0, sc1, sc0);
+            if (tile + 2 < t1) step(tile + 2, st2, st1, sc2, sc1);
+        }
+    }
+
+    // RW == 2.  The weights of a tile meet its values one step later, behind the step's one barrier;
+    // meanwhile the tile after that is on its way.  trade: [2 steps][2 rows][2 halves] of 64 lanes'
+    // weights, then the references that they were formed against.
+    __device__ __forceinline__ void walk_trade(const LatentArgs& a, uint8_t* st0, uint8_t* st1, uint8_t* st2,
+                                               float (*scale_lds)[kLatTile], uint4* trade, float* refs,
+                                               const Run& run) {
+        const int lane = threadIdx.x & 63, t0 = run.t0, t1 = run.t1;
+        float all = neg_inf();                                   // the reference of O
+        const int ent0 = entry(a, run.r, t0, run.kv_len);
+        int ent1 = entry(a, run.r, t0 + 1, run.kv_len);
+        float sc0 = load(a, st0, t0, ent0, true), sc1 = 0.f, sc2 = 0.f;
+        // weights of tile `tile`, to where the other wave finds them
+        const auto form = [&](int tile, uint8_t* st, float sc) __attribute__((always_inline)) {
+            v16f s;
+            const float m_new = look(st, scale_lds, run, tile, sc, s);
+            l *= m == m_new ? 1.f : shrink(m, m_new);
+            m = m_new;
+            h8v w[2];
+            weights(s, scale_lds[1] + 32 * tg, w);
+            const int at = ((tile & 1) * 2 + rg) * 2 + tg;
+            trade[at * 128 + lane] = __builtin_bit_cast(uint4, w[0]);
+            trade[at * 128 + 64 + lane] = __builtin_bit_cast(uint4, w[1]);
+            if (lane < 32) refs[at * 32 + lane] = m;
+        };
+        // values of tile `tile`
+        const auto sum = [&](int tile, uint8_t* st) __attribute__((always_inline)) {
+            const int at = ((tile & 1) * 2 + rg) * 2;
+            h8v w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) w[x] = __builtin_bit_cast(h8v, trade[at * 128 + x * 64 + lane]);
+            const float m0 = refs[at * 32 + (lane & 31)], m1 = refs[at * 32 + 32 + (lane & 31)], top = fmaxf(m0, m1);
+            if (__any(m0 != m1 || top != all)) {                 // the same in both waves
+                const float f0 = shrink(m0, top), f1 = shrink(m1, top), alpha = shrink(all, top);
+                w[0] *= (_Float16)f0;
+                w[1] *= (_Float16)f0;
+                w[2] *= (_Float16)f1;
+                w[3] *= (_Float16)f1;
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[d] *= alpha;
+                all = top;
+            }
+            values<2>(st, 0, w);
+        };
+        // the reference of O is that of the next weights at least
+        const auto follow = [&]() __attribute__((always_inline)) {
+            if (__any(m != all)) {
+                const float top = fmaxf(m, all);
+                l *= m == top ? 1.f : shrink(m, top);
+                m = top;
+            }
+        };
+        const auto step = [&](int tile, uint8_t* before, uint8_t* st, uint8_t* ahead, float sc, float& sc_ahead) __attribute__((always_inline)) {
+            barrier_all();
+            const int ent = ent1;
+            ent1 = entry(a, run.r, tile + 2, run.kv_len);
+            __builtin_amdgcn_sched_barrier(0);
+            sc_ahead = load(a, ahead, tile + 1, ent, tile + 1 < t1);
+            __builtin_amdgcn_sched_barrier(0);
+            clear_tail(st, run, tile);
+            sum(tile - 1, before);
+            follow();
+            form(tile, st, sc);
+        };
+        barrier_all();
+        const int ent = ent1;
+        ent1 = entry(a, run.r, t0 + 2, run.kv_len);
+        sc1 = load(a, st1, t0 + 1, ent, t0 + 1 < t1);
+        __builtin_amdgcn_sched_barrier(0);
+        clear_tail(st0, run, t0);
+        form(t0, st0, sc0);
+        int tile = t0 + 1;
+        for (; tile < t1; tile += 3) {
+            step(tile, st0, st1, st2, sc1, sc2);
+            if (tile + 1 < t1) step(tile + 1, st1, st2, st0, sc2, sc0);
+            if (tile + 2 < t1) step(tile + 2, st2, st0, st1, sc0, sc1);
+        }
+        barrier_all();
+        const int last = (t1 - 1 - t0) % 3;
+        if (last == 0) sum(t1 - 1, st0);
+        else if (last == 1) sum(t1 - 1, st1);
+        else sum(t1 - 1, st2);
+        follow();
+    }
+
+    // Tiles of an item, t0 < t1.
+    __device__ __forceinline__ void walk(const LatentArgs& a, uint8_t* st0, uint8_t* st1, uint8_t* st2,
+                                         float (*scale_lds)[kLatTile], uint4* trade, float* refs, const Run& run) {
+        if constexpr (RW == 2) walk_trade(a, st0, st1, st2, scale_lds, trade, refs, run);
+        else walk_halves(a, st0, st1, st2, scale_lds, run);
+        wait_vmcnt<0>();
+        __syncthreads();                                         // every wave is done with the stages
+    }
+
+    // Joins what the waves hold of a row: norms, and with RW == 1 O, into tg 0.  Leaves l as the row's
+    // sum in both of its lanes.
+    __device__ __forceinline__ void join(uint8_t* st0, uint8_t* st1, uint8_t* st2) {
+        l = half_sum(l);
+        const int lane = threadIdx.x & 63, other = RW == 2 ? rg : dw;
+        float* const ml = (float*)st2;
+        if (tg == 1 || RW == 2) {
+            ml[(other * 2 + tg) * 128 + lane] = m;
+            ml[(other * 2 + tg) * 128 + 64 + lane] = l;
+        }
+        float* const at = (float*)(dw == 0 ? st0 : st1);
+        if (RW == 1 && tg == 1) {
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) at[(d * 16 + i) * 64 + lane] = o[d][i];
+        }
+        __syncthreads();
+        if (RW == 2 || tg == 0) {
+            const float m1 = ml[(other * 2 + 1 - tg) * 128 + lane], l1 = ml[(other * 2 + 1 - tg) * 128 + 64 + lane];
+            const float top = fmaxf(m, m1), mine = shrink(m, top), theirs = shrink(m1, top);
+            m = top;
+            l = l * mine + l1 * theirs;
+            if (RW == 1) {
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        o[d][i] = o[d][i] * mine + at[(d * 16 + i) * 64 + lane] * theirs;
+            }
+        }
+        __syncthreads();
+    }
+
+    // The rows' results to out and lse.
+    __device__ __forceinline__ void store(const LatentArgs& a, const LatentItem& it, int row) const {
+        if ((RW == 1 && tg != 0) || row >= it.rows) return;
+        const int h = (threadIdx.x & 63) >> 5;
+        const int64_t t = it.q0 + row / a.heads;
+        const int j = row % a.heads;
+        const float f = l == 0.f ? 0.f : 1.f / l;
+        uint16_t* const out = a.out + t * a.o_ts + (int64_t)j * a.o_hs + dw * (32 * DT) + 4 * h;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *(uint2*)(out + 32 * d + 8 * i) =
+                    make_uint2(pack_bf16x2(o[d][4 * i] * f, o[d][4 * i + 1] * f),
+                               pack_bf16x2(o[d][4 * i + 2] * f, o[d][4 * i + 3] * f));
+        if (a.lse && h == 0 && dw == 0)
+            a.lse[t * a.heads + j] = l == 0.f ? neg_inf() : (m + __builtin_log2f(l)) * kLn2;
+    }
+
+    // Partial results of a slot: [RW][16 dims blocks][4][64 lanes] of four floats, then (m, l) a row.
+    __device__ __forceinline__ void store_part(const LatentArgs& a, int64_t slot) const {
+        if (RW == 1 && tg != 0) return;
+        const int lane = threadIdx.x & 63;
+        v4f* const ws = (v4f*)a.ws + ((slot * RW + rg) * 16 + dw * DT) * 256 + lane;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                ws[(d * 4 + i) * 64] = v4f{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+        if (lane < 32 && dw == 0) {
+            latent_ml(a, ROWS)[slot * ROWS + rg * 32 + lane] = make_float2(m, l);
+        }
+    }
+};
+
+// A split launch's units in even shares: the first unit of workgroup w, and the workgroup that has
+// unit u.  None between an item's first and last workgroup goes without.
+__device__ __forceinline__ int64_t latent_first(int64_t units, int w) {
+    return units < kLatGroups ? min((int64_t)w, units) : units * w / kLatGroups;
+}
+__device__ __forceinline__ int latent_owner(int64_t units, int64_t u) {
+    return (int)(units < kLatGroups ? u : quotient((u + 1) * kLatGroups - 1, units));
+}
+
+#define LATENT_LDS                                                             \
+    __shared__ __attribute__((aligned(1024))) uint8_t st0[kLatStage];          \
+    __shared__ __attribute__((aligned(1024))) uint8_t st1[kLatStage];          \
+    __shared__ __attribute__((aligned(1024))) uint8_t st2[kLatStage];          \
+    __shared__ __attribute__((aligned(16))) float scale_lds[4][2][kLatTile];   \
+    __shared__ uint4 trade[RW == 2 ? 2 * 4 * 128 : 1];                         \
+    __shared__ float refs[RW == 2 ? 2 * 4 * 32 : 1];                           \
+    const LatentLds lds = {st0, st1, st2, scale_lds[wave], trade, refs}
+
+struct LatentLds {
+    uint8_t *st0, *st1, *st2;
+    float (*scale_lds)[kLatTile];
+    uint4* trade;
+    float* refs;
+};
+
+// The rows of a run, or all rows of an item.
+template <class W>
+__device__ __forceinline__ void latent_run(const LatentArgs& a, W& w, const LatentLds& lds, const LatentItem& it, int r,
+                                           int rt, int t0, int t1) {
+    const int row = w.row(rt), last = min((rt + 1) * W::ROWS, it.rows) - 1;
+    t1 = min(t1, latent_tiles(it.limit(last / a.heads)));
+    w.load_q(a, it, row);
+    const typename W::Run run = {r,  t0, t1, it.kv_len, row < it.rows ? it.limit(row / a.heads) : 0,
+                                 it.limit(rt * W::ROWS / a.heads), __builtin_fabsf(a.scale) * kLog2e};
+    if (t0 < t1) w.walk(a, lds.st0, lds.st1, lds.st2, lds.scale_lds, lds.trade, lds.refs, run);
+    w.join(lds.st0, lds.st1, lds.st2);
+}
+
+// Every workgroup takes an even share of the tiles of all items (request, row tile), in that order.
+// Where it begins an item it notes for the join where the item's parts are: its own slot (of the two
+// that a workgroup has: its first run's and its last one's) and how many workgroups follow.
+template <int RW>
+__global__ __launch_bounds__(kLatThreads, 1) void attn_latent_split_kernel(LatentArgs a, int row_tiles) {
+    using W = LatentWalk<RW>;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    LATENT_LDS;
+    LatentRequests<W::ROWS> reqs;
+    int64_t units = 0;
+    for (int from = 0; from < a.R; from += 64) {
+        reqs.load(a, from);
+        units = reqs.scan(units);
+    }
+    int64_t u = latent_first(units, blockIdx.x);
+    const int64_t end = latent_first(units, blockIdx.x + 1);
+    if (u >= end) return;
+    if (a.R > 64) {                                              // back to the first unit's requests
+        int64_t next = 0;
+        for (int from = 0; from < a.R && next <= u; from += 64) {
+            reqs.load(a, from);
+            next = reqs.scan(next);
+        }
+    }
+    int r = __builtin_amdgcn_readfirstlane(reqs.base + last_of(reqs.base + lane < a.R && reqs.before <= u));
+    W w;
+    w.init();
+    bool first = true;
+    while (u < end) {
+        const int64_t begin = reqs.from_lane(reqs.before, r - reqs.base);
+        const int64_t after = begin + reqs.from_lane(reqs.units, r - reqs.base);
+        if (u >= after) {
+            if (++r >= a.R) break;
+            if (r - reqs.base >= 64) {
+                reqs.load(a, r);
+                reqs.scan(after);
+            }
+            continue;
+        }
+        const LatentItem it = reqs.item(a, r);
+        const int nt = latent_tiles(it.kv_len);
+        const int rt = __builtin_amdgcn_readfirstlane((int)quotient(u - begin, nt));
+        const int t0 = (int)(u - begin - (int64_t)rt * nt);
+        const int count = (int)min((int64_t)(nt - t0), end - u);
+        const int slot = (int)blockIdx.x * 2 + (first ? 0 : 1);
+        if (t0 == 0 && threadIdx.x == 0) {
+            const int last = count == nt ? (int)blockIdx.x : latent_owner(units, u + nt - 1);
+            latent_info(a, W::ROWS)[r * row_tiles + rt] = make_int2(slot, last - (int)blockIdx.x);
+        }
+        latent_run(a, w, lds, it, r, rt, t0, t0 + count);
+        if (count == nt) w.store(a, it, w.row(rt));
+        else w.store_part(a, slot);
+        u += count;
+        first = false;
+    }
+}
+
+// One workgroup per item: enough of them to fill the chip, or no workspace.  Request r's items are
+// numbered from q_offsets[r] * heads / ROWS + r on, where there is room for all of them.
+template <int RW>
+__global__ __launch_bounds__(kLatThreads, 1) void attn_latent_item_kernel(LatentArgs a) {
+    using W = LatentWalk<RW>;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    LATENT_LDS;
+    const int64_t b = blockIdx.x;
+    const auto start = [&](int q, int r) {
+        return min(max((int64_t)q, (int64_t)0), a.T) * a.heads / W::ROWS + r;
+    };
+    const int each64 = a.q_offsets[min(lane * 64, a.R)];
+    const int from = last_of(lane * 64 < a.R && start(each64, lane * 64) <= b) * 64;
+    const int mine = a.q_offsets[min(from + lane, a.R)];
+    const int r = __builtin_amdgcn_readfirstlane(from + last_of(from + lane < a.R && start(mine, from + lane) <= b));
+    const LatentItem it = LatentItem::of(a, a.q_offsets[r], a.q_offsets[r + 1], a.kv_lens[r]);
+    const int64_t at = b - start((int)it.q0, r);
+    if (at < 0 || at * W::ROWS >= it.rows) return;
+    const int rt = __builtin_amdgcn_readfirstlane((int)at);
+    W w;
+    w.init();
+    latent_run(a, w, lds, it, r, rt, 0, latent_tiles(it.kv_len));
+    w.store(a, it, w.row(rt));
+}
+static_assert(kKvMaxRequests <= 64 * 64, "a request is found in two steps of 64");
+
+// Adds the parts of items that several workgroups shared, in token order, and gives the rows of a
+// request without tokens their zeros.  A workgroup takes 32 rows x 32 dims.
+template <int RW>
+__global__ __launch_bounds__(kLatThreads) void attn_latent_join_kernel(LatentArgs a, int row_tiles) {
+    constexpr int ROWS = 32 * RW;
+    const int lane = threadIdx.x & 63, i = threadIdx.x >> 6, d = blockIdx.y;
+    const int rg = blockIdx.x % RW, item = blockIdx.x / RW;
+    const int r = item / row_tiles, rt = item % row_tiles;
+    const LatentItem it = LatentItem::of(a, a.q_offsets[r], a.q_offsets[r + 1], a.kv_lens[r]);
+    const int row = rt * ROWS + rg * 32 + (lane & 31);
+    if (rt * ROWS + rg * 32 >= it.rows) return;
+    v4f o = {0.f, 0.f, 0.f, 0.f};
+    float m = neg_inf(), l = 0.f;
+    if (it.kv_len > 0) {
+        const int2 info = latent_info(a, ROWS)[item];
+        if (info.y == 0) return;                                 // finished by its workgroup
+        const v4f* const ws = (const v4f*)a.ws + (rg * 16 + d) * 256 + i * 64 + lane;
+        const float2* const ml = latent_ml(a, ROWS) + rg * 32 + (lane & 31);
+#pragma unroll 4
+        for (int g = 0; g <= info.y; ++g) {
+            const int64_t slot = g == 0 ? info.x : (info.x / 2 + g) * 2;
+            const float2 part = ml[slot * ROWS];
+            const v4f x = ws[slot * (RW * 16 * 256)];
+            const float top = fmaxf(m, part.x);
+            const float old = m == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(m - top);
+            const float add = part.x == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(part.x - top);
+            o = o * old + x * add;
+            l = l * old + part.y * add;
+            m = top;
+        }
+    }
+    if (row >= it.rows) return;
+    const int64_t t = it.q0 + row / a.heads;
+    const int j = row % a.heads;
+    const float f = l == 0.f ? 0.f : 1.f / l;
+    *(uint2*)(a.out + t * a.o_ts + (int64_t)j * a.o_hs + 32 * d + 8 * i + 4 * (lane >> 5)) =
+        make_uint2(pack_bf16x2(o[0] * f, o[1] * f), pack_bf16x2(o[2] * f, o[3] * f));
+    if (a.lse && d == 0 && i == 0 && lane < 32)
+        a.lse[t * a.heads + j] = l == 0.f ? neg_inf() : (m + __builtin_log2f(l)) * kLn2;
+}
+
+// How a launch divides its rows: the waves of a workgroup that have rows of their own, and the row
+// tiles of a request.
+struct LatentPlan {
+    int rw;
+    int64_t row_tiles;
+    bool split;
+};
+static LatentPlan latent_plan(int64_t R, int64_t max_new, int32_t heads) {
+    const int64_t rows = max_new * heads;
+    LatentPlan p;
+    p.rw = rows <= 32 ? 1 : 2;
+    p.row_tiles = (rows + 32 * p.rw - 1) / (32 * p.rw);
+    p.split = R * p.row_tiles < kLatItems;
+    return p;
+}
+
+size_t attn_latent_workspace_bytes(int64_t R, int64_t max_new, int32_t heads) {
+    const LatentPlan p = latent_plan(R, max_new, heads);
+    if (!p.split) return 0;
+    return (size_t)kLatSlots * 32 * p.rw * (kLatent + 2) * sizeof(float) + (size_t)kLatItems * sizeof(int2);
+}
+
+template <int RW>
+static hipError_t latent_launch(const LatentArgs& a, const LatentPlan& p, hipStream_t stream) {
+    const int rt = (int)p.row_tiles;
+    if (!p.split || !a.ws) {
+        const int64_t items = a.T * a.heads / (32 * RW) + a.R;
+        attn_latent_item_kernel<RW><<<dim3((unsigned)items), dim3(kLatThreads), 0, stream>>>(a);
+        return hipGetLastError();
+    }
+    attn_latent_split_kernel<RW><<<dim3(kLatGroups), dim3(kLatThreads), 0, stream>>>(a, rt);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    attn_latent_join_kernel<RW><<<dim3((unsigned)(a.R * p.row_tiles * RW), 16), dim3(kLatThreads), 0, stream>>>(a, rt);
+    return hipGetLastError();
+}
+
+hipError_t launch_attn_latent(const LatentArgs& a, hipStream_t stream) {
+    const LatentPlan p = latent_plan(a.R, a.max_new, a.heads);
+    if (p.rw == 1) return latent_launch<1>(a, p, stream);
+    return latent_launch<2>(a, p, stream);
+}
+
+}  // namespace bfp8

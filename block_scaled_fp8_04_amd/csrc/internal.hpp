@@ -126,4 +126,49 @@ size_t attn_paged_workspace_bytes(int64_t R, int64_t max_new, int32_t heads_q, i
                                   int32_t dk, int32_t dv);
 hipError_t launch_attn_paged(const AttnArgs& a, int32_t dk, int32_t dv, hipStream_t stream);
 
+// Rotary positions (rope.hip) and the latent cache (latent_cache.hip, attn_latent.hip): a token's
+// latent and the rotated dims of its key.
+constexpr int kLatent = 512;
+constexpr int kLatentRope = 64;
+constexpr int kRopeMaxDim = 1024;
+hipError_t launch_rope(const void* x, int64_t x_ts, int64_t x_hs, const int32_t* positions,
+                       const float* inv_freq, void* out, int64_t o_ts, int64_t o_hs, int64_t T,
+                       int32_t heads, int32_t dim, bool interleaved, float amplitude,
+                       hipStream_t stream);
+hipError_t launch_latent_append(const void* kv, int64_t kv_ts, const void* norm_weight, float eps,
+                                const int32_t* slot_map, const int32_t* positions,
+                                const float* inv_freq, bool interleaved, float amplitude, int64_t T,
+                                void* codes, float* scales, void* rope, int64_t slots,
+                                hipStream_t stream);
+hipError_t launch_latent_gather(const void* codes, const float* scales, const void* rope,
+                                int64_t pages, int32_t page, const int32_t* block_table,
+                                int64_t width, const int32_t* row_offsets, const int32_t* starts,
+                                int64_t R, int64_t rows, void* latent, int64_t l_ts, void* rope_out,
+                                int64_t r_ts, hipStream_t stream);
+
+// Arguments of one call of attention over the latent cache (validated by the ABI layer).
+struct LatentArgs {
+    const uint16_t* q_latent;
+    int64_t ql_ts, ql_hs;
+    const uint16_t* q_rope;
+    int64_t qr_ts, qr_hs;
+    const uint8_t* codes;
+    const float* scales;
+    const uint16_t* rope;
+    int64_t pages;
+    const int32_t* block_table;
+    int64_t width;
+    const int32_t* q_offsets;
+    const int32_t* kv_lens;
+    int R, heads, log_b;
+    int64_t T, max_new;
+    float scale;
+    uint16_t* out;
+    int64_t o_ts, o_hs;
+    float* lse;
+    float* ws;
+};
+size_t attn_latent_workspace_bytes(int64_t R, int64_t max_new, int32_t heads);
+hipError_t launch_attn_latent(const LatentArgs& a, hipStream_t stream);
+
 }  // namespace bfp8

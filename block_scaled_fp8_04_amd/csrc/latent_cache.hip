@@ -1,0 +1,210 @@
+// latent_cache.hip - the paged cache of shared latents on gfx950: quantizing append and read back.
+//
+// A token's row in the cache is 512 e4m3 codes, one power-of-two scale (fp32) and 64 rotated bf16:
+// 644 bytes.  The scale is the token's own, so a token is written without a look at its page and
+// never touched again.
+//
+// append: one wave per token, eight latent elements a lane.
+//     y = c * rsqrt(mean c^2 + eps) * w        (or y = c), fp32, not rounded in between
+//     s = 2^ceil(log2(max(amax |y|, 1e-4) / 448)),   code = e4m3_rne(y / s)
+// The lower half's lanes each turn one pair of the key.
+//
+// gather: one wave per 16 rows: a row's codes are eight a lane, its key eight elements of eight lanes,
+// four rows on their way at a time.
+#include "attn_common.hpp"
+#include "device_codec.hpp"
+#include "internal.hpp"
+#include "rotary.hpp"
+
+namespace bfp8 {
+
+constexpr int kLatentThreads = 256;
+constexpr int kLatentWaves = kLatentThreads / 64;
+
+// Over the 64 lanes, to all of them.
+__device__ __forceinline__ float wave_add(float x) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
+    return x;
+}
+__device__ __forceinline__ uint32_t wave_most(uint32_t x) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) x = max(x, (uint32_t)__shfl_xor((int)x, d));
+    return x;
+}
+
+// Eight bf16 (kVec: 16-byte aligned).
+template <bool kVec>
+__device__ __forceinline__ void widen8_bf16(const uint16_t* p, float (&y)[8]) {
+    if constexpr (kVec) {
+        const uint4 v = *(const uint4*)p;
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            y[2 * i] = bf16_lo(w[i]);
+            y[2 * i + 1] = bf16_hi(w[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = bf16_lo(p[i]);
+    }
+}
+
+template <bool kVec>
+__global__ __launch_bounds__(kLatentThreads) void latent_append_kernel(
+    const uint16_t* __restrict__ kv, int64_t kv_ts, const uint16_t* __restrict__ norm_weight, float eps,
+    const int32_t* __restrict__ slot_map, const int32_t* __restrict__ positions,
+    const float* __restrict__ inv_freq, int interleaved, float amplitude, int64_t T,
+    uint8_t* __restrict__ codes, float* __restrict__ scales, uint16_t* __restrict__ rope, int64_t slots) {
+    const int lane = threadIdx.x & 63, pair = lane & 31;
+    const int64_t t = (int64_t)blockIdx.x * kLatentWaves + (threadIdx.x >> 6);
+    if (t >= T) return;
+    const int64_t slot = slot_map[t];
+    if (slot < 0 || slot >= slots) return;
+    const uint16_t* const row = kv + t * kv_ts;
+    float y[8], w[8];
+    widen8_bf16<kVec>(row + 8 * lane, y);
+    if (norm_weight) widen8_bf16<kVec>(norm_weight + 8 * lane, w);
+    // both halves of the wave turn the key, the lower one stores it
+    const int i0 = interleaved ? 2 * pair : pair, i1 = interleaved ? 2 * pair + 1 : pair + kLatentRope / 2;
+    const float a = bf16_lo(row[kLatent + i0]), b = bf16_lo(row[kLatent + i1]);
+    const float2 cs = rotary(positions[t], inv_freq[pair], amplitude);
+    const float r0 = __builtin_fmaf(a, cs.x, -b * cs.y), r1 = __builtin_fmaf(a, cs.y, b * cs.x);
+    if (norm_weight) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(y[i], y[i], sum);
+        const float f = 1.f / __builtin_sqrtf(wave_add(sum) * (1.f / kLatent) + eps);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = y[i] * f * w[i];
+    }
+    // by bit patterns: infinities and NaN are the largest
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+    most = wave_most(most);
+    const uint32_t rot = pack_bf16x2(r0, r1);
+    const bool odd = (rot & 0x7F80u) == 0x7F80u || (rot >> 16 & 0x7F80u) == 0x7F80u;
+    // not finite, or 2^127 and more: codes times the scale would pass bf16
+    const bool bad = most >= 0x7F000000u || __any(odd);
+    const float s = pow2_scale(__uint_as_float(most));
+    const float inv = __uint_as_float((254u << 23) - __float_as_uint(s));
+    uint2 q = make_uint2(e4m3_encode4<true>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                         e4m3_encode4<true>(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+    if (bad) q = make_uint2(0, 0);
+    *(uint2*)(codes + slot * kLatent + 8 * lane) = q;
+    if (lane == 0) scales[slot] = bad ? __uint_as_float(0x7FC00000u) : s;
+    if (lane < 32) {
+        uint16_t* const to = rope + slot * kLatentRope;
+        if (interleaved) {
+            *(uint32_t*)(to + i0) = bad ? 0u : rot;
+        } else {
+            to[i0] = bad ? 0 : (uint16_t)rot;
+            to[i1] = bad ? 0 : (uint16_t)(rot >> 16);
+        }
+    }
+}
+
+hipError_t launch_latent_append(const void* kv, int64_t kv_ts, const void* norm_weight, float eps,
+                                const int32_t* slot_map, const int32_t* positions,
+                                const float* inv_freq, bool interleaved, float amplitude, int64_t T,
+                                void* codes, float* scales, void* rope, int64_t slots,
+                                hipStream_t stream) {
+    const bool vec = ((uintptr_t)kv | (uintptr_t)norm_weight) % 16 == 0 && kv_ts % 8 == 0;
+    const unsigned grid = (unsigned)((T + kLatentWaves - 1) / kLatentWaves);
+    hipLaunchKernelGGL(vec ? latent_append_kernel<true> : latent_append_kernel<false>, dim3(grid), dim3(kLatentThreads),
+                       0, stream, (const uint16_t*)kv, kv_ts, (const uint16_t*)norm_weight, eps, slot_map, positions,
+                       inv_freq, (int)interleaved, amplitude, T, (uint8_t*)codes, scales, (uint16_t*)rope, slots);
+    return hipGetLastError();
+}
+
+// ------------------------------------------------------------------ gather
+
+constexpr int kGatherRows = 16;               // of a wave
+constexpr int kGatherAhead = 4;               // rows on their way
+
+struct GatherArgs {
+    const uint8_t* codes;
+    const float* scales;
+    const uint16_t* rope;
+    int64_t pages;
+    int log_b;
+    const int32_t* block_table;
+    int64_t width;
+    const int32_t *row_offsets, *starts;
+    int R;
+    int64_t rows;
+    uint16_t* latent;
+    int64_t l_ts;
+    uint16_t* rope_out;
+    int64_t r_ts;
+};
+
+__global__ __launch_bounds__(kLatentThreads) void latent_gather_kernel(GatherArgs a) {
+    const int lane = threadIdx.x & 63;
+    const int64_t row0 = ((int64_t)blockIdx.x * kLatentWaves + (threadIdx.x >> 6)) * kGatherRows;
+    if (row0 >= a.rows) return;
+    const int each64 = a.row_offsets[min(lane * 64, a.R)];
+    if (row0 >= a.row_offsets[a.R]) return;
+    // the request of the first row, in two steps of 64; those of the others follow
+    int from = last_of(lane * 64 < a.R && each64 <= row0) * 64;
+    int ends = a.row_offsets[min(from + 1 + lane, a.R)];          // of request from + lane
+    int r = a.R;                                                  // lane j < 16: row j's
+    for (int j = 0; j < kGatherRows; ++j) {
+        int before = __popcll(__ballot(from + lane < a.R && ends <= row0 + j));
+        while (before == 64 && from + 64 < a.R) {
+            from += 64;
+            ends = a.row_offsets[min(from + 1 + lane, a.R)];
+            before = __popcll(__ballot(from + lane < a.R && ends <= row0 + j));
+        }
+        if (lane == j) r = from + before;
+    }
+    // where it lies in the pool, -1 for nowhere
+    int64_t at = -1;
+    if (r < a.R && row0 + lane < a.rows) {
+        const int64_t pos = row0 + lane - a.row_offsets[r] + (a.starts ? a.starts[r] : 0);
+        if (pos >= 0 && pos < a.width << a.log_b) {
+            const int64_t page = a.block_table[r * a.width + (pos >> a.log_b)];
+            at = min(max(page, (int64_t)0), a.pages - 1) << a.log_b | (pos & ((1 << a.log_b) - 1));
+        }
+    }
+    const int64_t mine = max(at, (int64_t)0);
+    const float scale = lane < kGatherRows ? a.scales[mine] : 0.f;
+#pragma unroll
+    for (int j0 = 0; j0 < kGatherRows; j0 += kGatherAhead) {
+        uint2 c[kGatherAhead];
+        uint4 k[kGatherAhead];
+        int64_t slot[kGatherAhead];
+#pragma unroll
+        for (int j = 0; j < kGatherAhead; ++j) {
+            slot[j] = (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)at, j0 + j) |
+                      (int64_t)__builtin_amdgcn_readlane((int)(at >> 32), j0 + j) << 32;
+            const int64_t s = max(slot[j], (int64_t)0);
+            c[j] = *(const uint2*)(a.codes + s * kLatent + 8 * lane);
+            k[j] = *(const uint4*)(a.rope + s * kLatentRope + 8 * (lane & 7));
+        }
+#pragma unroll
+        for (int j = 0; j < kGatherAhead; ++j) {
+            if (slot[j] < 0) continue;
+            const float e = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(scale), j0 + j));
+            *(uint4*)(a.latent + (row0 + j0 + j) * a.l_ts + 8 * lane) =
+                __builtin_bit_cast(uint4, widen8((int)c[j].x, (int)c[j].y, e));
+            if (lane < 8) *(uint4*)(a.rope_out + (row0 + j0 + j) * a.r_ts + 8 * lane) = k[j];
+        }
+    }
+}
+
+hipError_t launch_latent_gather(const void* codes, const float* scales, const void* rope,
+                                int64_t pages, int32_t page, const int32_t* block_table,
+                                int64_t width, const int32_t* row_offsets, const int32_t* starts,
+                                int64_t R, int64_t rows, void* latent, int64_t l_ts, void* rope_out,
+                                int64_t r_ts, hipStream_t stream) {
+    const GatherArgs a = {(const uint8_t*)codes, scales, (const uint16_t*)rope, pages, __builtin_ctz(page), block_table,
+                          width, row_offsets, starts, (int)R, rows, (uint16_t*)latent, l_ts, (uint16_t*)rope_out, r_ts};
+    const int64_t waves = (rows + kGatherRows - 1) / kGatherRows;
+    hipLaunchKernelGGL(latent_gather_kernel, dim3((unsigned)((waves + kLatentWaves - 1) / kLatentWaves)),
+                       dim3(kLatentThreads), 0, stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace bfp8

@@ -495,6 +495,137 @@ int bfp8_attn_paged(const void* q_bf16, int64_t q_token_stride, int64_t q_head_s
 size_t bfp8_attn_paged_workspace_size(int64_t R, int64_t max_new, int32_t heads_q,
                                       int32_t heads_kv, int32_t dk, int32_t dv);
 
+/* ----------------------------------------------------------------------
+ * Rotary positions, and attention over a shared latent.  Keys and values of
+ * all heads come from one latent of 512 per token, next to 64 rotated dims
+ * that all heads share; with the heads' expansions absorbed into query and
+ * output projections, attention reads the latent alone.
+ *
+ * The latent cache of one layer is a pool of num_pages pages of B = page_size
+ * tokens (32, 64 or 128), with block tables and slots as above:
+ *   latent_cache  : e4m3 [num_pages, B, 512]
+ *   latent_scales : fp32 [num_pages, B], a power of two per token
+ *   rope_cache    : bf16 [num_pages, B, 64], the rotated dims
+ * value = e4m3(code) * scale; of any other scale only the exponent is used.
+ * Slots behind a request's last token, and pages that no request holds, may
+ * hold anything, NaN included.
+ * ---------------------------------------------------------------------- */
+
+/* a token's latent and its rotated dims; the largest head bfp8_rope rotates */
+#define BFP8_LATENT 512
+#define BFP8_LATENT_ROPE 64
+#define BFP8_ROPE_MAX_DIM 1024
+
+/* Rotary positions of heads: pair p < dim / 2 of every head of token t is
+ *     (a, b) -> amplitude * (a cos w - b sin w, a sin w + b cos w),  w = positions[t] * inv_freq[p]
+ * with (a, b) = (x[2p], x[2p + 1]) if interleaved, (x[p], x[p + dim/2]) if not.
+ * Angles are formed in 64 bits, products in fp32, results rounded to bf16 once.
+ * Scaled positions for long contexts are a matter of inv_freq and amplitude.  A
+ * part of a head is rotated by giving that part alone (a pointer to its first
+ * dim, its length as dim).
+ *   x_bf16    : bf16, element (t, h, d) at t * x_token_stride + h * x_head_stride + d
+ *   out_bf16  : bf16, likewise; x itself with its strides, or no overlap with it
+ *   positions : DEVICE int32 [T]; a token whose position is negative is skipped
+ *               (its rows of out are not written)
+ *   inv_freq  : DEVICE fp32 [dim / 2]
+ * 16-byte accesses are used where dim is a multiple of 8 (interleaved) or 16,
+ * pointers are 16-byte aligned and strides multiples of 8.
+ * Errors: BFP8_ERR_SHAPE if T < 0, T >= 2^24, heads < 1, heads > 65535, dim < 2,
+ * dim odd or above BFP8_ROPE_MAX_DIM, or a stride is negative; BFP8_ERR_ARG for an
+ * amplitude that is not finite; BFP8_ERR_NULL; BFP8_ERR_ALIGN. */
+int bfp8_rope(const void* x_bf16, int64_t x_token_stride, int64_t x_head_stride,
+              const int32_t* positions, const float* inv_freq, void* out_bf16,
+              int64_t out_token_stride, int64_t out_head_stride, int64_t T, int32_t heads,
+              int32_t dim, int32_t interleaved, float amplitude, void* stream);
+
+/* Writes the step's tokens into the latent cache.  For token t with slot
+ * slot_map[t], c = its row's first 512 elements, k = the 64 behind them:
+ *     y = c * rsqrt(mean(c^2) + eps) * norm_weight       (y = c without norm_weight)
+ *     s = 2^ceil(log2( max(amax |y|, 1e-4f) / 448 ))     (as bfp8_act_quant_ue8m0)
+ *     code = e4m3_rne_saturating(y / s),   rotated dims = bfp8_rope of k at positions[t]
+ * y is fp32 and not rounded in between.  A token with an element of y or of the
+ * rotated dims that is not finite, or with |y| >= 2^127, is stored with a scale
+ * of NaN and zeros: every query that sees it gets NaN, and no other query does.
+ *   kv_bf16     : bf16, element (t, d) at t * kv_token_stride + d, d < 576
+ *   norm_weight : DEVICE bf16 [512], or NULL
+ *   slot_map    : DEVICE int32 [T]; a slot outside [0, num_pages * page_size) is
+ *                 skipped, a slot named twice holds either token's parts
+ *   positions   : DEVICE int32 [T], inv_freq : DEVICE fp32 [32], interleaved and
+ *                 amplitude as for bfp8_rope
+ *   latent_cache, rope_cache : 16-byte aligned; latent_scales : 4-byte aligned
+ * Errors: BFP8_ERR_SHAPE if T < 0, T >= 2^26, kv_token_stride < 0, num_pages < 0 or
+ * num_pages * page_size >= 2^31; BFP8_ERR_ARG if page_size is not 32, 64 or 128, or eps
+ * or amplitude is not finite or eps is negative; BFP8_ERR_NULL; BFP8_ERR_ALIGN. */
+int bfp8_latent_append(const void* kv_bf16, int64_t kv_token_stride, const void* norm_weight,
+                       float eps, const int32_t* slot_map, const int32_t* positions,
+                       const float* inv_freq, int32_t interleaved, float amplitude, int64_t T,
+                       void* latent_cache, float* latent_scales, void* rope_cache,
+                       int64_t num_pages, int32_t page_size, void* stream);
+
+/* Reads cached tokens back to bf16 rows, e.g. to expand them to full heads for a
+ * prompt's chunks: rows row_offsets[r] .. row_offsets[r+1] - 1 are request r's tokens
+ * from starts[r] on (from its first one if starts is NULL),
+ *     latent_out[row] = bf16(code * scale)   (exact),   rope_out[row] = the rotated dims
+ *   row_offsets : DEVICE int32 [R+1], ascending; rows past `rows` or past
+ *                 row_offsets[R], and of tokens past the table's width, are not written
+ *   starts      : DEVICE int32 [R], or NULL
+ *   latent_out  : bf16 [rows, 512] at a row stride, 16-byte aligned; rope_out likewise [rows, 64]
+ * Table entries are clamped into the pool.  A token stored as not finite gives NaN latents.
+ * Errors: BFP8_ERR_SHAPE if R < 0, rows < 0, rows >= 2^30, num_pages < 0, a width or
+ * pool of 2^31 slots or more, or a stride is negative; BFP8_ERR_GROUPS if R >
+ * BFP8_KV_MAX_REQUESTS; BFP8_ERR_ARG for another page_size; BFP8_ERR_NULL; BFP8_ERR_ALIGN (also
+ * a stride that is not a multiple of 8). */
+int bfp8_latent_gather(const void* latent_cache, const float* latent_scales,
+                       const void* rope_cache, int64_t num_pages, int32_t page_size,
+                       const int32_t* block_table, int64_t table_width,
+                       const int32_t* row_offsets, const int32_t* starts, int64_t R, int64_t rows,
+                       void* latent_out, int64_t latent_row_stride, void* rope_out,
+                       int64_t rope_row_stride, void* stream);
+
+/* Attention of each request's new tokens over its latents, all heads on one
+ * cache.  Query i of request r (n = q_offsets[r+1] - q_offsets[r] of them) stands at
+ * position kv_lens[r] - n + i and sees the tokens up to and including it:
+ *     x_t = scale * (q_latent . c_t + q_rope . k_t)
+ *     out = bf16_rne( sum_t p_t c_t / sum_t p_t ),  p_t = exp(x_t - max),  lse = log sum_t exp(x_t)
+ * with c_t the token's 512 latent values and k_t its 64 rotated dims.  A row that
+ * sees nothing gets zeros, and -infinity.  Logits, sums and statistics are fp32; p_t
+ * enters its product with eleven significant bits (2^-12 of it at most is lost).
+ *   q_latent_bf16 : bf16, element (t, j, d) at t * ql_token_stride + j * ql_head_stride + d,
+ *              d < 512, rows 0 .. T-1; q_rope_bf16 likewise, d < 64
+ *   block_table : DEVICE int32 [R, table_width]; entries up to kv_len are read,
+ *              clamped into the pool
+ *   q_offsets : DEVICE int32 [R+1], kv_lens : DEVICE int32 [R], as bfp8_kv_plan
+ *              writes them (any values stay inside the buffers)
+ *   max_new  : host upper bound of the requests' new tokens; rows of a request
+ *              past it are not written
+ *   out_bf16 : bf16, element (t, j, d) at t * out_token_stride + j * out_head_stride + d,
+ *              16-byte aligned, strides multiples of 8, rows not overlapping; rows of
+ *              no request are not written
+ *   lse      : fp32 [T, heads], or NULL
+ *   workspace: DEVICE, at least bfp8_attn_latent_workspace_size(...) bytes, 16-byte
+ *              aligned, any contents: partial results of token ranges; NULL lets every
+ *              row's tokens be walked in one piece
+ * Sums are fp32 and p may reach 2^8 in them: latents beyond 2^100 may overflow in the
+ * rows that see them.  Deterministic.
+ * Errors: BFP8_ERR_SHAPE if a size or stride is negative, T * heads >= 2^29, max_new < 1 (with
+ * R, T > 0), heads < 1, heads > 65535, max_new * heads >= 2^31, or num_pages or table_width
+ * times page_size >= 2^31; BFP8_ERR_GROUPS if R > BFP8_KV_MAX_REQUESTS; BFP8_ERR_ARG for a
+ * page_size as above or a scale that is not finite; BFP8_ERR_NULL; BFP8_ERR_ALIGN;
+ * BFP8_ERR_WORKSPACE. */
+int bfp8_attn_latent(const void* q_latent_bf16, int64_t ql_token_stride, int64_t ql_head_stride,
+                     const void* q_rope_bf16, int64_t qr_token_stride, int64_t qr_head_stride,
+                     const void* latent_cache, const float* latent_scales, const void* rope_cache,
+                     int64_t num_pages, int32_t page_size, const int32_t* block_table,
+                     int64_t table_width, const int32_t* q_offsets, const int32_t* kv_lens,
+                     int64_t R, int64_t T, int64_t max_new, int32_t heads, float scale,
+                     void* out_bf16, int64_t out_token_stride, int64_t out_head_stride, float* lse,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace bfp8_attn_latent uses for these sizes (a multiple of 16; 0 for
+ * sizes it would refuse or that it never splits).  Pure host function (planned for the
+ * 256 CUs of MI355X). */
+size_t bfp8_attn_latent_workspace_size(int64_t R, int64_t max_new, int32_t heads);
+
 /* Test helper: encodes the 2^32 float32 bit patterns first .. first+count-1
  * to e4m3 codes with the same device routine act_quant uses (variant 0), or
  * with the alternative routine (variant 1), into out[count] (device).
