@@ -534,6 +534,7 @@ int bfp8_attn_latent(const void* q_latent_bf16, int64_t ql_token_stride, int64_t
     a.kv_lens = kv_lens;
     a.R = (int)R;
     a.heads = heads;
+    a.by_heads = bfp8::Divisor::by(heads);
     a.log_b = __builtin_ctz(page_size);
     a.T = T;
     a.max_new = max_new;

@@ -43,7 +43,6 @@ constexpr int kLatGroups = 256;               // workgroups of a split launch: o
 constexpr int kLatItems = 512;                // most items of a split launch: beyond, they fill the chip
 constexpr int kLatTile = 64;                  // tokens of a tile
 constexpr int kLatCodes = kLatTile * kLatent; // its bytes of codes and of rotated keys
-constexpr int kLatLoads = 11;                 // a wave's reads of a tile that are counted
 constexpr int kLatStage = kLatCodes + kLatTile * kLatentRope * 2;
 // A maximum is followed only where it would be passed by more than this (in units of log 2): weights
 // reach 2^8, far inside fp16's range.
@@ -141,55 +140,62 @@ struct LatentRequests {
     }
 };
 
-// One workgroup's walk over a run of one item's tiles.  Its four waves are two by two:
-//   RW == 2 (64 rows): wave (rg, x) takes 32 rows; of each tile it forms the weights of half x of the
-//     tokens, trades them with the other wave of its rows through LDS, and sums half x of the dims
-//     over all tokens.
-//   RW == 1 (32 rows): wave (tg, x) takes half tg of each tile's tokens and sums half x of the dims
-//     over those; both waves of a half form its weights.  That is twice the work for the weights and
-//     no trade: with so few rows the cache's bytes are what counts.
-// (All dims in one wave would take 256 registers for O next to 144 for q: the compiler spills.)
+struct LatentLds {
+    uint8_t *st0, *st1, *st2;                        // stages, a tile each
+    float (*scales)[kLatTile];                       // this wave's: exponents, inverses
+    uint4* trade;                                    // [row half][token half][2][64 lanes] weights
+    float* refs;                                     // [row half][token half][2][64 lanes] references, norms
+};
+
+// One workgroup's walk over a run of one item's tiles.  Its four waves form weights two by two, each
+// for 32 rows and half tg of a tile's tokens, trade them through LDS, and each sums its rows' values
+// over all of the tile's tokens for its share of the dims:
+//   RW == 2 (64 rows): wave (rg, x) has 32 rows, token half x and dim half x.
+//   RW == 1 (32 rows): wave x has all rows, token half x & 1 and dim quarter x; two waves form the
+//     same weights, which is work twice done, but with so few rows the cache's bytes are what counts.
+// (A wave with 32 rows and all dims would keep 256 registers of O next to 144 of q, which the compiler
+// does not manage without spills.)
 template <int RW>
 struct LatentWalk {
-    static constexpr int DT = 8;                     // blocks of 32 dims of a wave
+    static constexpr int DT = RW == 2 ? 8 : 4;       // blocks of 32 dims of a wave
     static constexpr int ROWS = 32 * RW;
 
     v16f o[DT];
     float m, l;                                      // l: over this wave's tokens of this lane only
     bf8v q[36];                                      // 32 of the latent, 4 of the rotated part
     int rg, tg, dw;                                  // this wave's rows, tokens, dims
+    bool gives;                                      // its weights are the ones that are traded
 
     __device__ __forceinline__ void init() {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        dw = wave >> 1;
         rg = RW == 2 ? wave & 1 : 0;
-        tg = RW == 2 ? dw : wave & 1;
+        tg = RW == 2 ? wave >> 1 : wave & 1;
+        dw = RW == 2 ? wave >> 1 : wave;
+        gives = RW == 2 || wave < 2;
     }
     // this lane's row, counted in the item
     __device__ __forceinline__ int row(int rt) const { return rt * ROWS + rg * 32 + (threadIdx.x & 31); }
 
+    // Queries of this lane's row (of the last one, where there is none: nothing of it is stored), into
+    // accumulation registers, where the matrix instructions take them from.
     __device__ __forceinline__ void load_q(const LatentArgs& a, const LatentItem& it, int row) {
         const int h = (threadIdx.x & 63) >> 5;
-        const bool negate = a.scale < 0.f;
-        if (row < it.rows) {
-            const int64_t t = it.q0 + row / a.heads;
-            const int j = row % a.heads;
-            const uint16_t* const ql = a.q_latent + t * a.ql_ts + (int64_t)j * a.ql_hs + 16 * h;
-            const uint16_t* const qr = a.q_rope + t * a.qr_ts + (int64_t)j * a.qr_hs + 8 * h;
-            const bool vl = ((uintptr_t)a.q_latent % 16) == 0 && ((a.ql_ts | a.ql_hs) % 8) == 0;
-            const bool vr = ((uintptr_t)a.q_rope % 16) == 0 && ((a.qr_ts | a.qr_hs) % 8) == 0;
-            // a 16-byte read of codes feeds two matrix instructions: dims 32 p + 16 h + 8 x ..
+        int j;
+        const int64_t t = it.q0 + a.by_heads.of(min(row, it.rows - 1), j);
+        const uint16_t* const ql = a.q_latent + t * a.ql_ts + (int64_t)j * a.ql_hs + 16 * h;
+        const uint16_t* const qr = a.q_rope + t * a.qr_ts + (int64_t)j * a.qr_hs + 8 * h;
+        const bool vec = ((uintptr_t)a.q_latent | (uintptr_t)a.q_rope) % 16 == 0 &&
+                         (a.ql_ts | a.ql_hs | a.qr_ts | a.qr_hs) % 8 == 0;
+        // dims of operand s: a 16-byte read of codes feeds two matrix instructions
+        const auto at = [&](int s) { return s < 32 ? ql + s / 2 * 32 + s % 2 * 8 : qr + (s - 32) * 16; };
+        // one branch for all of the loads: with one each, each is waited for
+        if (vec) {
 #pragma unroll
-            for (int p = 0; p < 16; ++p)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) q[2 * p + x] = load_q8(ql + 32 * p + 8 * x, vl, negate);
-#pragma unroll
-            for (int s = 0; s < 4; ++s) q[32 + s] = load_q8(qr + 16 * s, vr, negate);
+            for (int s = 0; s < 36; ++s) q[s] = *(const bf8v*)at(s);
         } else {
 #pragma unroll
-            for (int s = 0; s < 36; ++s) q[s] = bf8v{0, 0, 0, 0, 0, 0, 0, 0};
+            for (int s = 0; s < 36; ++s) q[s] = load_q8(at(s), false, false);
         }
-        // in accumulation registers, where the matrix instructions take them from
 #pragma unroll
         for (int s = 0; s < 36; ++s) asm volatile("" : "+a"(q[s]));
 #pragma unroll
@@ -206,32 +212,40 @@ struct LatentWalk {
         return a.block_table[r * a.width + (pos >> a.log_b)];
     }
 
-    // Requests a tile: each wave 16 of its tokens, by loads that go straight to LDS, and the scale of
-    // token `lane`.  not real: the loads lie outside their resource and read nothing.
-    static __device__ __forceinline__ float load(const LatentArgs& a, uint8_t* st, int tile, int entry, bool real) {
-        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const int in_page = (1 << a.log_b) - 1;
-        const int64_t page = min(max((int64_t)entry, (int64_t)0), a.pages - 1);
-        const int64_t own = (int64_t)__builtin_amdgcn_readlane((int)page, 16 * wave) << a.log_b |
-                            ((int)((uint32_t)tile * kLatTile) + 16 * wave & in_page);
-        const __amdgpu_buffer_rsrc_t codes = make_rsrc(a.codes + own * kLatent, real ? 16 * kLatent : 0);
-        const __amdgpu_buffer_rsrc_t rope = make_rsrc(a.rope + own * kLatentRope, real ? 16 * kLatentRope * 2 : 0);
-        // row 2 k + hi of the wave's sixteen; the lane's place in LDS holds this chunk of it
-        const int hi = lane >> 5, at = hi * kLatent + (((lane & 31) ^ lat_swz(hi)) << 4);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            buf_lds16(codes, at ^ lat_swz(2 * k) << 4, k * 1024, st + wave * 8192 + k * 1024);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int row = 8 * k + (lane >> 3);
-            buf_lds16(rope, row * (kLatentRope * 2) + (((lane & 7) ^ rope_swz(row)) << 4), 0,
-                      st + kLatCodes + wave * 2048 + k * 1024);
+    // A tile's way to LDS: each wave brings 16 of its tokens, by ten loads that bypass the registers.
+    // not real: the loads lie outside their resource and read nothing.
+    struct Fetch {
+        __amdgpu_buffer_rsrc_t codes, rope;
+        const float* scale;                          // of token `lane`
+        __device__ __forceinline__ Fetch(const LatentArgs& a, int tile, int entry, bool real) {
+            const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+            const int in_page = (1 << a.log_b) - 1, first = (int)((uint32_t)tile * kLatTile);
+            const int page = (int)min(max((int64_t)entry, (int64_t)0), a.pages - 1);
+            const int64_t own = (int64_t)__builtin_amdgcn_readlane(page, 16 * wave) << a.log_b |
+                                (first + 16 * wave & in_page);
+            codes = make_rsrc(a.codes + own * kLatent, real ? 16 * kLatent : 0);
+            rope = make_rsrc(a.rope + own * kLatentRope, real ? 16 * kLatentRope * 2 : 0);
+            scale = a.scales + (real ? (int64_t)page << a.log_b | (first + lane & in_page) : 0);
         }
-        return a.scales[real ? page << a.log_b | ((int)((uint32_t)tile * kLatTile) + lane & in_page) : 0];
-    }
+        __device__ __forceinline__ void load(uint8_t* st, int k) const {
+            const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+            if (k < 8) {
+                // row 2 k + hi of the wave's sixteen; the lane's place in LDS holds this chunk of it
+                const int hi = lane >> 5, at = hi * kLatent + (((lane & 31) ^ lat_swz(hi)) << 4);
+                buf_lds16(codes, at ^ lat_swz(2 * k) << 4, k * 1024, st + wave * 8192 + k * 1024);
+            } else {
+                const int row = 8 * (k - 8) + (lane >> 3);
+                buf_lds16(rope, row * (kLatentRope * 2) + (((lane & 7) ^ rope_swz(row)) << 4), 0,
+                          st + kLatCodes + wave * 2048 + (k - 8) * 1024);
+            }
+        }
+    };
+    static constexpr int FETCHES = 10;
 
-    // S^T of 32 tokens: rows of C are widened with their token's scale.
-    __device__ __forceinline__ v16f logits(const uint8_t* st, int b, float scale) const {
+    // S^T of 32 tokens: rows of C are widened with their token's scale.  Codes are read four chunks
+    // ahead and widened one ahead of the matrix instructions that take them, which would otherwise wait
+    // for the conversion; between them, the loads of a tile to come.
+    __device__ __forceinline__ v16f logits(const uint8_t* st, int b, float scale, const Fetch& fetch, uint8_t* to) const {
         const int lane = threadIdx.x & 63, h = lane >> 5, row = 32 * b + (lane & 31);
         const uint8_t* const c = st + row * kLatent;
         const uint8_t* const r = st + kLatCodes + row * (kLatentRope * 2);
@@ -246,20 +260,28 @@ struct LatentWalk {
         };
 #pragma unroll
         for (int p = 0; p < AHEAD; ++p) w[p] = read(p);
+        __builtin_amdgcn_sched_barrier(0);
+        bf8v lo = widen8((int)w[0].x, (int)w[0].y, scale), hi = widen8((int)w[0].z, (int)w[0].w, scale);
 #pragma unroll
         for (int p = 0; p < N; ++p) {
-            __builtin_amdgcn_sched_barrier(0);                   // or all of them are read at once
+            bf8v next_lo = lo, next_hi = hi;
+            if (p + 1 < 16) {
+                next_lo = widen8((int)w[p + 1].x, (int)w[p + 1].y, scale);
+                next_hi = widen8((int)w[p + 1].z, (int)w[p + 1].w, scale);
+            }
             if (p + AHEAD < N) w[p + AHEAD] = read(p + AHEAD);
+            if (p % 2 == 1) fetch.load(to, p / 2);
+            __builtin_amdgcn_sched_barrier(0);
             if (p < 16) {
-                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen8((int)w[p].x, (int)w[p].y, scale), q[2 * p], s, 0,
-                                                            0, 0);
-                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen8((int)w[p].z, (int)w[p].w, scale), q[2 * p + 1], s,
-                                                            0, 0, 0);
+                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lo, q[2 * p], s, 0, 0, 0);
+                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hi, q[2 * p + 1], s, 0, 0, 0);
             } else {
                 s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8v, w[p]), q[16 + p], s, 0, 0, 0);
             }
+            __builtin_amdgcn_sched_barrier(0);
+            lo = next_lo;
+            hi = next_hi;
         }
-        __builtin_amdgcn_sched_barrier(0);
         return s;
     }
 
@@ -306,30 +328,33 @@ struct LatentWalk {
         }
     }
 
-    // O^T += C^T P^T over N times 32 tokens, from block b on.
-    template <int N>
-    __device__ __forceinline__ void values(const uint8_t* st, int b, const h8v (&w)[2 * N]) {
+    // O^T += C^T P^T over a tile's tokens, 16 at a time; read and widened ahead as in logits().
+    __device__ __forceinline__ void values(const uint8_t* st, const h8v (&w)[4]) {
         const int lane = threadIdx.x & 63, h = lane >> 5, g = lane >> 4 & 1, i = lane >> 1 & 7;
         // this lane's address is that of token T, 8 of 16 dims; it gets 8 tokens of dim lane & 31
         const int T = (i & 3) + 8 * (i >> 2) + 4 * h;
-        const uint8_t* const c = st + (32 * b + T) * kLatent + (lane & 1) * 8;
+        const uint8_t* const c = st + T * kLatent + (lane & 1) * 8;
         const int cs = lat_swz(T) ^ g;
-        constexpr int READS = 2 * N * DT, AHEAD = 4;             // those on their way
-        v2i x[READS];
+        constexpr int N = 4 * DT, AHEAD = 6;                     // reads, those on their way
+        v2i x[N];
         const auto read = [&](int n) {
             const int chunk = 2 * (dw * DT + n % DT) ^ cs;
             return __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i)(c + n / DT * 16 * kLatent + (chunk << 4)));
         };
 #pragma unroll
         for (int n = 0; n < AHEAD; ++n) x[n] = read(n);
-#pragma unroll
-        for (int n = 0; n < READS; ++n) {
-            __builtin_amdgcn_sched_barrier(0);
-            if (n + AHEAD < READS) x[n + AHEAD] = read(n + AHEAD);
-            o[n % DT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen8_f16(x[n][0], x[n][1]), w[n / DT], o[n % DT], 0,
-                                                               0, 0);
-        }
         __builtin_amdgcn_sched_barrier(0);
+        h8v f = widen8_f16(x[0][0], x[0][1]);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            h8v next = f;
+            if (n + 1 < N) next = widen8_f16(x[n + 1][0], x[n + 1][1]);
+            if (n + AHEAD < N) x[n + AHEAD] = read(n + AHEAD);
+            __builtin_amdgcn_sched_barrier(0);
+            o[n % DT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, w[n / DT], o[n % DT], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            f = next;
+        }
     }
 
     // What a walk is about: everything but limit (tokens that this lane's row sees) is uniform.
@@ -348,193 +373,111 @@ struct LatentWalk {
         __syncthreads();
     }
 
-    // A tile's exponents of this wave's half tg; the scale's exponents and inverses go to this wave's
-    // own bytes of LDS.
-    __device__ __forceinline__ float look(const uint8_t* st, float (*scale_lds)[kLatTile], const Run& run, int tile,
-                                          float sc, v16f& s) const {
-        const int lane = threadIdx.x & 63;
-        const uint32_t ex = __float_as_uint(sc) >> 23 & 255;
-        scale_lds[0][lane] = ex == 255 ? __uint_as_float(0x7FC00000u) : (float)((int)ex - 127);
-        scale_lds[1][lane] = ex == 255 ? 0.f : __uint_as_float((254 - ex) << 23);
-        __builtin_amdgcn_wave_barrier();
-        const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(sc), __float_as_uint(sc), false, false);
-        s = logits(st, tg, __uint_as_float(tg == 0 ? both[0] : both[1]));
-        const int base = tile * kLatTile;
-        return exponents(s, scale_lds[0] + 32 * tg, run.c, run.limit - base - 32 * tg, base > run.free_limit - kLatTile);
-    }
-
-    // RW == 1.  Two tiles are on their way while one is worked on.
-    __device__ __forceinline__ void walk_halves(const LatentArgs& a, uint8_t* st0, uint8_t* st1, uint8_t* st2,
-                                                float (*scale_lds)[kLatTile], const Run& run) {
-        const int t0 = run.t0, t1 = run.t1;
+    // Tiles run.t0 < run.t1 of an item.  While one is worked on the next is on its way, and the one
+    // after that is asked for.
+    __device__ __forceinline__ void walk(const LatentArgs& a, const LatentLds& lds, const LatentItem& it, int row,
+                                         const Run& run) {
+        const int lane = threadIdx.x & 63, t0 = run.t0, t1 = run.t1;
+        uint8_t *const st0 = lds.st0, *const st1 = lds.st1, *const st2 = lds.st2;
         const int ent0 = entry(a, run.r, t0, run.kv_len), ent1 = entry(a, run.r, t0 + 1, run.kv_len);
         int ent2 = entry(a, run.r, t0 + 2, run.kv_len);
-        float sc0 = load(a, st0, t0, ent0, true);
-        float sc1 = load(a, st1, t0 + 1, ent1, t0 + 1 < t1);
-        float sc2 = 0.f;
+        const Fetch f0(a, t0, ent0, true), f1(a, t0 + 1, ent1, t0 + 1 < t1);
+        float sc0 = *f0.scale, sc1 = *f1.scale, sc2 = 0.f;
+#pragma unroll
+        for (int k = 0; k < FETCHES; ++k) f0.load(st0, k);
+        load_q(a, it, row);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int k = 0; k < FETCHES; ++k) f1.load(st1, k);
+        const int pair = (rg * 2 + tg) * 128 + lane, first = rg * 256 + lane;
         const auto step = [&](int tile, uint8_t* st, uint8_t* ahead, float sc, float& sc_ahead) __attribute__((always_inline)) {
-            wait_vmcnt<kLatLoads>();                             // all but the next tile's
+            wait_vmcnt<FETCHES>();                               // all but the next tile's loads
             barrier_lds();
             __builtin_amdgcn_sched_barrier(0);
-            const int ent = ent2;
+            const Fetch fetch(a, tile + 2, ent2, tile + 2 < t1);
             ent2 = entry(a, run.r, tile + 3, run.kv_len);
-            __builtin_amdgcn_sched_barrier(0);
-            sc_ahead = load(a, ahead, tile + 2, ent, tile + 2 < t1);
+            sc_ahead = *fetch.scale;
             __builtin_amdgcn_sched_barrier(0);
             clear_tail(st, run, tile);
-            v16f s;
-            const float m_new = look(st, scale_lds, run, tile, sc, s);
-            if (__any(m_new != m)) {
-                const float alpha = shrink(m, m_new);
-                l *= alpha;
-#pragma unroll
-                for (int d = 0; d < DT; ++d) o[d] *= alpha;
-                m = m_new;
-            }
-            h8v w[2];
-            weights(s, scale_lds[1] + 32 * tg, w);
-            values<1>(st, tg, w);
-        };
-        for (int tile = t0; tile < t1; tile += 3) {
-            step(tile, st0, st2, sc0, sc2);
-            if (tile + 1 < t1) step(tile + 1, st1, st0, sc1, sc0);
-            if (tile + 2 < t1) step(tile + 2, st2, st1, sc2, sc1);
-        }
-    }
-
-    // RW == 2.  The weights of a tile meet its values one step later, behind the step's one barrier;
-    // meanwhile the tile after that is on its way.  trade: [2 steps][2 rows][2 halves] of 64 lanes'
-    // weights, then the references that they were formed against.
-    __device__ __forceinline__ void walk_trade(const LatentArgs& a, uint8_t* st0, uint8_t* st1, uint8_t* st2,
-                                               float (*scale_lds)[kLatTile], uint4* trade, float* refs,
-                                               const Run& run) {
-        const int lane = threadIdx.x & 63, t0 = run.t0, t1 = run.t1;
-        float all = neg_inf();                                   // the reference of O
-        const int ent0 = entry(a, run.r, t0, run.kv_len);
-        int ent1 = entry(a, run.r, t0 + 1, run.kv_len);
-        float sc0 = load(a, st0, t0, ent0, true), sc1 = 0.f, sc2 = 0.f;
-        // weights of tile `tile`, to where the other wave finds them
-        const auto form = [&](int tile, uint8_t* st, float sc) __attribute__((always_inline)) {
-            v16f s;
-            const float m_new = look(st, scale_lds, run, tile, sc, s);
+            // the scale's exponents and inverses, in this wave's own bytes of LDS
+            const uint32_t ex = __float_as_uint(sc) >> 23 & 255;
+            lds.scales[0][lane] = ex == 255 ? __uint_as_float(0x7FC00000u) : (float)((int)ex - 127);
+            lds.scales[1][lane] = ex == 255 ? 0.f : __uint_as_float((254 - ex) << 23);
+            __builtin_amdgcn_wave_barrier();
+            const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(sc), __float_as_uint(sc), false, false);
+            v16f s = logits(st, tg, __uint_as_float(tg == 0 ? both[0] : both[1]), fetch, ahead);
+            const int base = tile * kLatTile;
+            const float m_new = exponents(s, lds.scales[0] + 32 * tg, run.c, run.limit - base - 32 * tg,
+                                          base > run.free_limit - kLatTile);
+            const float before = m;
             l *= m == m_new ? 1.f : shrink(m, m_new);
             m = m_new;
-            h8v w[2];
-            weights(s, scale_lds[1] + 32 * tg, w);
-            const int at = ((tile & 1) * 2 + rg) * 2 + tg;
-            trade[at * 128 + lane] = __builtin_bit_cast(uint4, w[0]);
-            trade[at * 128 + 64 + lane] = __builtin_bit_cast(uint4, w[1]);
-            if (lane < 32) refs[at * 32 + lane] = m;
-        };
-        // values of tile `tile`
-        const auto sum = [&](int tile, uint8_t* st) __attribute__((always_inline)) {
-            const int at = ((tile & 1) * 2 + rg) * 2;
             h8v w[4];
+            {
+                h8v mine[2];
+                weights(s, lds.scales[1] + 32 * tg, mine);
+                if (gives) {
+                    lds.trade[pair] = __builtin_bit_cast(uint4, mine[0]);
+                    lds.trade[pair + 64] = __builtin_bit_cast(uint4, mine[1]);
+                    lds.refs[pair] = m;
+                }
+            }
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(15 | 7 << 4 | 3 << 14);   // lgkmcnt 0
+            barrier_lds();
+            const float m0 = lds.refs[first], m1 = lds.refs[first + 128];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) w[x] = __builtin_bit_cast(h8v, trade[at * 128 + x * 64 + lane]);
-            const float m0 = refs[at * 32 + (lane & 31)], m1 = refs[at * 32 + 32 + (lane & 31)], top = fmaxf(m0, m1);
-            if (__any(m0 != m1 || top != all)) {                 // the same in both waves
-                const float f0 = shrink(m0, top), f1 = shrink(m1, top), alpha = shrink(all, top);
+            for (int x = 0; x < 4; ++x) w[x] = __builtin_bit_cast(h8v, lds.trade[first + 64 * x]);
+            // the wave's rows' reference is that of O in all waves: the larger of the two
+            if (__any(m0 != m1 || m0 != before)) {
+                const float top = fmaxf(m0, m1), f0 = shrink(m0, top), f1 = shrink(m1, top), alpha = shrink(before, top);
                 w[0] *= (_Float16)f0;
                 w[1] *= (_Float16)f0;
                 w[2] *= (_Float16)f1;
                 w[3] *= (_Float16)f1;
 #pragma unroll
                 for (int d = 0; d < DT; ++d) o[d] *= alpha;
-                all = top;
-            }
-            values<2>(st, 0, w);
-        };
-        // the reference of O is that of the next weights at least
-        const auto follow = [&]() __attribute__((always_inline)) {
-            if (__any(m != all)) {
-                const float top = fmaxf(m, all);
                 l *= m == top ? 1.f : shrink(m, top);
                 m = top;
             }
+            values(st, w);
         };
-        const auto step = [&](int tile, uint8_t* before, uint8_t* st, uint8_t* ahead, float sc, float& sc_ahead) __attribute__((always_inline)) {
-            barrier_all();
-            const int ent = ent1;
-            ent1 = entry(a, run.r, tile + 2, run.kv_len);
-            __builtin_amdgcn_sched_barrier(0);
-            sc_ahead = load(a, ahead, tile + 1, ent, tile + 1 < t1);
-            __builtin_amdgcn_sched_barrier(0);
-            clear_tail(st, run, tile);
-            sum(tile - 1, before);
-            follow();
-            form(tile, st, sc);
-        };
-        barrier_all();
-        const int ent = ent1;
-        ent1 = entry(a, run.r, t0 + 2, run.kv_len);
-        sc1 = load(a, st1, t0 + 1, ent, t0 + 1 < t1);
-        __builtin_amdgcn_sched_barrier(0);
-        clear_tail(st0, run, t0);
-        form(t0, st0, sc0);
-        int tile = t0 + 1;
-        for (; tile < t1; tile += 3) {
-            step(tile, st0, st1, st2, sc1, sc2);
-            if (tile + 1 < t1) step(tile + 1, st1, st2, st0, sc2, sc0);
-            if (tile + 2 < t1) step(tile + 2, st2, st0, st1, sc0, sc1);
+        for (int tile = t0; tile < t1; tile += 3) {
+            step(tile, st0, st2, sc0, sc2);
+            if (tile + 1 < t1) step(tile + 1, st1, st0, sc1, sc0);
+            if (tile + 2 < t1) step(tile + 2, st2, st1, sc2, sc1);
         }
-        barrier_all();
-        const int last = (t1 - 1 - t0) % 3;
-        if (last == 0) sum(t1 - 1, st0);
-        else if (last == 1) sum(t1 - 1, st1);
-        else sum(t1 - 1, st2);
-        follow();
-    }
-
-    // Tiles of an item, t0 < t1.
-    __device__ __forceinline__ void walk(const LatentArgs& a, uint8_t* st0, uint8_t* st1, uint8_t* st2,
-                                         float (*scale_lds)[kLatTile], uint4* trade, float* refs, const Run& run) {
-        if constexpr (RW == 2) walk_trade(a, st0, st1, st2, scale_lds, trade, refs, run);
-        else walk_halves(a, st0, st1, st2, scale_lds, run);
         wait_vmcnt<0>();
         __syncthreads();                                         // every wave is done with the stages
     }
 
-    // Joins what the waves hold of a row: norms, and with RW == 1 O, into tg 0.  Leaves l as the row's
-    // sum in both of its lanes.
-    __device__ __forceinline__ void join(uint8_t* st0, uint8_t* st1, uint8_t* st2) {
+    // No tiles: rows that see nothing.
+    __device__ __forceinline__ void nothing() {
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+        m = neg_inf();
+        l = 0.f;
+    }
+
+    // The rows' norms, over both halves of the tokens (which have one reference).
+    __device__ __forceinline__ void join(const LatentLds& lds) {
         l = half_sum(l);
-        const int lane = threadIdx.x & 63, other = RW == 2 ? rg : dw;
-        float* const ml = (float*)st2;
-        if (tg == 1 || RW == 2) {
-            ml[(other * 2 + tg) * 128 + lane] = m;
-            ml[(other * 2 + tg) * 128 + 64 + lane] = l;
-        }
-        float* const at = (float*)(dw == 0 ? st0 : st1);
-        if (RW == 1 && tg == 1) {
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) at[(d * 16 + i) * 64 + lane] = o[d][i];
-        }
+        const int at = rg * 256 + (threadIdx.x & 63);
+        if (gives) lds.refs[at + 128 * tg + 64] = l;
         __syncthreads();
-        if (RW == 2 || tg == 0) {
-            const float m1 = ml[(other * 2 + 1 - tg) * 128 + lane], l1 = ml[(other * 2 + 1 - tg) * 128 + 64 + lane];
-            const float top = fmaxf(m, m1), mine = shrink(m, top), theirs = shrink(m1, top);
-            m = top;
-            l = l * mine + l1 * theirs;
-            if (RW == 1) {
-#pragma unroll
-                for (int d = 0; d < DT; ++d)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        o[d][i] = o[d][i] * mine + at[(d * 16 + i) * 64 + lane] * theirs;
-            }
-        }
+        l = lds.refs[at + 64] + lds.refs[at + 192];
         __syncthreads();
     }
 
     // The rows' results to out and lse.
     __device__ __forceinline__ void store(const LatentArgs& a, const LatentItem& it, int row) const {
-        if ((RW == 1 && tg != 0) || row >= it.rows) return;
+        if (row >= it.rows) return;
         const int h = (threadIdx.x & 63) >> 5;
-        const int64_t t = it.q0 + row / a.heads;
-        const int j = row % a.heads;
+        int j;
+        const int64_t t = it.q0 + a.by_heads.of(row, j);
         const float f = l == 0.f ? 0.f : 1.f / l;
         uint16_t* const out = a.out + t * a.o_ts + (int64_t)j * a.o_hs + dw * (32 * DT) + 4 * h;
 #pragma unroll
@@ -550,7 +493,6 @@ struct LatentWalk {
 
     // Partial results of a slot: [RW][16 dims blocks][4][64 lanes] of four floats, then (m, l) a row.
     __device__ __forceinline__ void store_part(const LatentArgs& a, int64_t slot) const {
-        if (RW == 1 && tg != 0) return;
         const int lane = threadIdx.x & 63;
         v4f* const ws = (v4f*)a.ws + ((slot * RW + rg) * 16 + dw * DT) * 256 + lane;
 #pragma unroll
@@ -573,33 +515,29 @@ __device__ __forceinline__ int latent_owner(int64_t units, int64_t u) {
     return (int)(units < kLatGroups ? u : quotient((u + 1) * kLatGroups - 1, units));
 }
 
-#define LATENT_LDS                                                             \
+#define LATENT_LDS(RW)                                                         \
     __shared__ __attribute__((aligned(1024))) uint8_t st0[kLatStage];          \
     __shared__ __attribute__((aligned(1024))) uint8_t st1[kLatStage];          \
     __shared__ __attribute__((aligned(1024))) uint8_t st2[kLatStage];          \
-    __shared__ __attribute__((aligned(16))) float scale_lds[4][2][kLatTile];   \
-    __shared__ uint4 trade[RW == 2 ? 2 * 4 * 128 : 1];                         \
-    __shared__ float refs[RW == 2 ? 2 * 4 * 32 : 1];                           \
-    const LatentLds lds = {st0, st1, st2, scale_lds[wave], trade, refs}
-
-struct LatentLds {
-    uint8_t *st0, *st1, *st2;
-    float (*scale_lds)[kLatTile];
-    uint4* trade;
-    float* refs;
-};
+    __shared__ __attribute__((aligned(16))) float scales[4][2][kLatTile];      \
+    __shared__ uint4 trade[RW * 256];                                          \
+    __shared__ float refs[RW * 256];                                           \
+    const LatentLds lds = {st0, st1, st2, scales[wave], trade, refs}
 
 // The rows of a run, or all rows of an item.
 template <class W>
 __device__ __forceinline__ void latent_run(const LatentArgs& a, W& w, const LatentLds& lds, const LatentItem& it, int r,
                                            int rt, int t0, int t1) {
-    const int row = w.row(rt), last = min((rt + 1) * W::ROWS, it.rows) - 1;
-    t1 = min(t1, latent_tiles(it.limit(last / a.heads)));
-    w.load_q(a, it, row);
-    const typename W::Run run = {r,  t0, t1, it.kv_len, row < it.rows ? it.limit(row / a.heads) : 0,
-                                 it.limit(rt * W::ROWS / a.heads), __builtin_fabsf(a.scale) * kLog2e};
-    if (t0 < t1) w.walk(a, lds.st0, lds.st1, lds.st2, lds.scale_lds, lds.trade, lds.refs, run);
-    w.join(lds.st0, lds.st1, lds.st2);
+    const int row = w.row(rt);
+    t1 = min(t1, latent_tiles(it.limit(a.by_heads.of(min((rt + 1) * W::ROWS, it.rows) - 1))));
+    if (t0 < t1) {
+        const typename W::Run run = {r,  t0, t1, it.kv_len, row < it.rows ? it.limit(a.by_heads.of(row)) : 0,
+                                     it.limit(a.by_heads.of(rt * W::ROWS)), a.scale * kLog2e};
+        w.walk(a, lds, it, row, run);
+        w.join(lds);
+    } else {
+        w.nothing();
+    }
 }
 
 // Every workgroup takes an even share of the tiles of all items (request, row tile), in that order.
@@ -609,7 +547,7 @@ template <int RW>
 __global__ __launch_bounds__(kLatThreads, 1) void attn_latent_split_kernel(LatentArgs a, int row_tiles) {
     using W = LatentWalk<RW>;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    LATENT_LDS;
+    LATENT_LDS(RW);
     LatentRequests<W::ROWS> reqs;
     int64_t units = 0;
     for (int from = 0; from < a.R; from += 64) {
@@ -665,7 +603,7 @@ template <int RW>
 __global__ __launch_bounds__(kLatThreads, 1) void attn_latent_item_kernel(LatentArgs a) {
     using W = LatentWalk<RW>;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    LATENT_LDS;
+    LATENT_LDS(RW);
     const int64_t b = blockIdx.x;
     const auto start = [&](int q, int r) {
         return min(max((int64_t)q, (int64_t)0), a.T) * a.heads / W::ROWS + r;
@@ -717,8 +655,8 @@ __global__ __launch_bounds__(kLatThreads) void attn_latent_join_kernel(LatentArg
         }
     }
     if (row >= it.rows) return;
-    const int64_t t = it.q0 + row / a.heads;
-    const int j = row % a.heads;
+    int j;
+    const int64_t t = it.q0 + a.by_heads.of(row, j);
     const float f = l == 0.f ? 0.f : 1.f / l;
     *(uint2*)(a.out + t * a.o_ts + (int64_t)j * a.o_hs + 32 * d + 8 * i + 4 * (lane >> 5)) =
         make_uint2(pack_bf16x2(o[0] * f, o[1] * f), pack_bf16x2(o[2] * f, o[3] * f));

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 namespace bfp8 {
 
 // Largest number of local experts the MoE dispatch handles (LDS counters).
@@ -146,6 +148,26 @@ hipError_t launch_latent_gather(const void* codes, const float* scales, const vo
                                 int64_t R, int64_t rows, void* latent, int64_t l_ts, void* rope_out,
                                 int64_t r_ts, hipStream_t stream);
 
+// Quotient and remainder by a number that is the same for a whole launch: the quotient by
+// m = 2^32 / d rounded down is short by one at most.
+struct Divisor {
+    uint32_t d, m;
+    static Divisor by(int32_t d) { return {(uint32_t)d, (uint32_t)std::min<uint64_t>(((uint64_t)1 << 32) / d, UINT32_MAX)}; }
+    __device__ __forceinline__ int of(int x, int& rest) const {
+        uint32_t q = __umulhi((uint32_t)x, m), r = (uint32_t)x - q * d;
+        if (r >= d) {
+            q += 1;
+            r -= d;
+        }
+        rest = (int)r;
+        return (int)q;
+    }
+    __device__ __forceinline__ int of(int x) const {
+        int rest;
+        return of(x, rest);
+    }
+};
+
 // Arguments of one call of attention over the latent cache (validated by the ABI layer).
 struct LatentArgs {
     const uint16_t* q_latent;
@@ -161,6 +183,7 @@ struct LatentArgs {
     const int32_t* q_offsets;
     const int32_t* kv_lens;
     int R, heads, log_b;
+    Divisor by_heads;
     int64_t T, max_new;
     float scale;
     uint16_t* out;

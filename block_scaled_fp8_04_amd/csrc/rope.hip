@@ -18,13 +18,6 @@ constexpr int kRopeThreads = 256;
 
 static_assert(kRopeMaxDim / 2 * sizeof(float2) <= 65536 && kRopeMaxDim / 2 <= 65536, "a token's angles fit LDS");
 
-// Whole quotient x / d for x < 2^16 by one multiplication: m = ceil(2^32 / d) (0 stands for d = 1).
-struct Divisor {
-    uint32_t d, m;
-    __device__ __forceinline__ uint32_t of(uint32_t x) const { return m ? __umulhi(x, m) : x; }
-};
-static Divisor divisor(uint32_t d) { return {d, d == 1 ? 0 : (uint32_t)((((uint64_t)1 << 32) + d - 1) / d)}; }
-
 struct RopeArgs {
     const uint16_t* x;
     int64_t x_ts, x_hs;
@@ -56,14 +49,15 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a) {
     const int n = (int)min((int64_t)a.tokens, a.T - t0);
     const int h0 = blockIdx.y * a.block_heads, heads = min(a.block_heads, a.heads - h0);
     for (int i = tid; i < n * a.pairs; i += kRopeThreads) {
-        const int t = a.by_pairs.of(i);
-        angles[i] = rotary(a.positions[t0 + t], a.inv_freq[i - t * a.pairs], a.amplitude);
+        int p;
+        const int t = a.by_pairs.of(i, p);
+        angles[i] = rotary(a.positions[t0 + t], a.inv_freq[p], a.amplitude);
     }
     __syncthreads();
     const int groups = a.by_groups.d, all = n * (int)a.by_heads.d * groups;
     for (int i = tid; i < all; i += kRopeThreads) {
-        const int th = a.by_groups.of(i), g = i - th * groups;
-        const int t = a.by_heads.of(th), h = th - t * (int)a.by_heads.d;
+        int g, h;
+        const int t = a.by_heads.of(a.by_groups.of(i, g), h);
         if (h >= heads || a.positions[t0 + t] < 0) continue;
         const uint16_t* const x = a.x + (t0 + t) * a.x_ts + (int64_t)(h0 + h) * a.x_hs;
         uint16_t* const y = a.out + (t0 + t) * a.o_ts + (int64_t)(h0 + h) * a.o_hs;
@@ -143,9 +137,9 @@ hipError_t launch_rope(const void* x, int64_t x_ts, int64_t x_hs, const int32_t*
     a.amplitude = amplitude;
     a.tokens = tokens;
     a.block_heads = block_heads;
-    a.by_pairs = divisor(pairs);
-    a.by_groups = divisor(groups);
-    a.by_heads = divisor(block_heads);
+    a.by_pairs = Divisor::by(pairs);
+    a.by_groups = Divisor::by(groups);
+    a.by_heads = Divisor::by(block_heads);
     const dim3 grid((unsigned)((T + tokens - 1) / tokens), (unsigned)((heads + block_heads - 1) / block_heads));
     const size_t lds = (size_t)tokens * pairs * sizeof(float2);
     auto* const kernel = interleaved ? (vec ? rope_kernel<true, true> : rope_kernel<true, false>)
