@@ -74,11 +74,11 @@ __device__ __forceinline__ int2* latent_info(const LatentArgs& a, int rows) {
     return (int2*)(latent_ml(a, rows) + kLatSlots * rows);
 }
 
-// Barrier behind everything that this wave wrote to LDS or has on its way there.
-__device__ __forceinline__ void barrier_all() {
+// Barrier behind what this wave wrote to LDS, but not behind its loads that are on their way there.
+__device__ __forceinline__ void barrier_written() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(7 << 4);                          // vmcnt 0, lgkmcnt 0
+    __builtin_amdgcn_s_waitcnt(15 | 7 << 4 | 3 << 14);           // lgkmcnt 0
     barrier_lds();
 }
 
@@ -140,15 +140,57 @@ struct LatentRequests {
     }
 };
 
+// A unit of work: a tile of an item (request, row tile).  Uniform.
+struct LatentUnit {
+    int r, rt, tile, tiles;                          // tiles: of the item
+    LatentItem it;
+};
+
+// A workgroup's units, one after the other.  It is ahead of the work: loads are asked for by it.
+template <int ROWS>
+struct LatentStream {
+    LatentRequests<ROWS> reqs;
+    LatentUnit at;
+    int64_t left;                                    // units behind this one
+
+    // From unit `local` of request r (one of reqs) on.
+    __device__ __forceinline__ void begin(const LatentArgs& a, int r, int64_t local, int64_t count) {
+        at.r = r;
+        at.it = reqs.item(a, r);
+        at.tiles = latent_tiles(at.it.kv_len);
+        at.rt = __builtin_amdgcn_readfirstlane((int)quotient(local, at.tiles));
+        at.tile = (int)(local - (int64_t)at.rt * at.tiles);
+        left = count - 1;
+    }
+    // To the next unit; none: stays.
+    __device__ __forceinline__ bool step(const LatentArgs& a) {
+        if (left <= 0) return false;
+        --left;
+        if (++at.tile < at.tiles) return true;
+        at.tile = 0;
+        if (++at.rt * ROWS < at.it.rows) return true;
+        at.rt = 0;
+        uint64_t later = __ballot(reqs.units > 0) & ~((2ull << (at.r - reqs.base)) - 1);
+        while (later == 0 && reqs.base + 64 < a.R) {
+            reqs.load(a, reqs.base + 64);
+            later = __ballot(reqs.units > 0);
+        }
+        if (later == 0) return false;                            // (not with units left)
+        at.r = reqs.base + __ffsll((unsigned long long)later) - 1;
+        at.it = reqs.item(a, at.r);
+        at.tiles = latent_tiles(at.it.kv_len);
+        return true;
+    }
+};
+
 struct LatentLds {
     uint8_t *st0, *st1, *st2;                        // stages, a tile each
-    float (*scales)[kLatTile];                       // this wave's: exponents, inverses
+    float2* scales;                                  // this wave's [64 tokens] exponents and inverses
     uint4* trade;                                    // [row half][token half][2][64 lanes] weights
     float* refs;                                     // [row half][token half][2][64 lanes] references, norms
 };
 
-// One workgroup's walk over a run of one item's tiles.  Its four waves form weights two by two, each
-// for 32 rows and half tg of a tile's tokens, trade them through LDS, and each sums its rows' values
+// One workgroup's way through its units.  Its four waves form weights two by two, each for 32 rows and half tg of a tile's tokens, trade them through LDS, and each sums its rows' values
 // over all of the tile's tokens for its share of the dims:
 //   RW == 2 (64 rows): wave (rg, x) has 32 rows, token half x and dim half x.
 //   RW == 1 (32 rows): wave x has all rows, token half x & 1 and dim quarter x; two waves form the
@@ -165,6 +207,8 @@ struct LatentWalk {
     bf8v q[36];                                      // 32 of the latent, 4 of the rotated part
     int rg, tg, dw;                                  // this wave's rows, tokens, dims
     bool gives;                                      // its weights are the ones that are traded
+    int limit, free_limit;                           // tokens that this lane's row sees; that all rows see
+    int from;                                        // the run's first tile
 
     __device__ __forceinline__ void init() {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -176,12 +220,13 @@ struct LatentWalk {
     // this lane's row, counted in the item
     __device__ __forceinline__ int row(int rt) const { return rt * ROWS + rg * 32 + (threadIdx.x & 31); }
 
-    // Queries of this lane's row (of the last one, where there is none: nothing of it is stored), into
-    // accumulation registers, where the matrix instructions take them from.
-    __device__ __forceinline__ void load_q(const LatentArgs& a, const LatentItem& it, int row) {
+    // To an item's first unit here: queries of this lane's row (of the last one, where there is none:
+    // nothing of it is stored) go into accumulation registers, where the matrix instructions take them
+    // from.
+    __device__ __forceinline__ void ask_q(const LatentArgs& a, const LatentUnit& u) {
         const int h = (threadIdx.x & 63) >> 5;
         int j;
-        const int64_t t = it.q0 + a.by_heads.of(min(row, it.rows - 1), j);
+        const int64_t t = u.it.q0 + a.by_heads.of(min(row(u.rt), u.it.rows - 1), j);
         const uint16_t* const ql = a.q_latent + t * a.ql_ts + (int64_t)j * a.ql_hs + 16 * h;
         const uint16_t* const qr = a.q_rope + t * a.qr_ts + (int64_t)j * a.qr_hs + 8 * h;
         const bool vec = ((uintptr_t)a.q_latent | (uintptr_t)a.q_rope) % 16 == 0 &&
@@ -196,6 +241,8 @@ struct LatentWalk {
 #pragma unroll
             for (int s = 0; s < 36; ++s) q[s] = load_q8(at(s), false, false);
         }
+    }
+    __device__ __forceinline__ void begin(const LatentArgs& a, const LatentUnit& u) {
 #pragma unroll
         for (int s = 0; s < 36; ++s) asm volatile("" : "+a"(q[s]));
 #pragma unroll
@@ -204,28 +251,32 @@ struct LatentWalk {
             for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
         m = neg_inf();
         l = 0.f;
+        const int mine = row(u.rt);
+        limit = mine < u.it.rows ? u.it.limit(a.by_heads.of(mine)) : 0;
+        free_limit = u.it.limit(a.by_heads.of(u.rt * ROWS));
+        from = u.tile;
     }
 
-    // The table entry of the page that holds token `lane` of a tile (of the last page, behind the end).
-    static __device__ __forceinline__ int entry(const LatentArgs& a, int r, int tile, int kv_len) {
-        const int64_t pos = min((int64_t)tile * kLatTile + (threadIdx.x & 63), (int64_t)kv_len - 1);
-        return a.block_table[r * a.width + (pos >> a.log_b)];
+    // The table entry of the page that holds token `lane` of a unit (of the last page, behind the end).
+    static __device__ __forceinline__ int entry(const LatentArgs& a, const LatentUnit& u) {
+        const uint32_t pos = min((uint32_t)u.tile * kLatTile + (threadIdx.x & 63), (uint32_t)u.it.kv_len - 1);
+        return (a.block_table + u.r * a.width)[pos >> a.log_b];
     }
 
-    // A tile's way to LDS: each wave brings 16 of its tokens, by ten loads that bypass the registers.
+    // A unit's way to LDS: each wave brings 16 of its tokens, by ten loads that bypass the registers.
     // not real: the loads lie outside their resource and read nothing.
     struct Fetch {
         __amdgpu_buffer_rsrc_t codes, rope;
         const float* scale;                          // of token `lane`
-        __device__ __forceinline__ Fetch(const LatentArgs& a, int tile, int entry, bool real) {
+        __device__ __forceinline__ Fetch(const LatentArgs& a, const LatentUnit& u, int entry, bool real) {
             const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-            const int in_page = (1 << a.log_b) - 1, first = (int)((uint32_t)tile * kLatTile);
-            const int page = (int)min(max((int64_t)entry, (int64_t)0), a.pages - 1);
-            const int64_t own = (int64_t)__builtin_amdgcn_readlane(page, 16 * wave) << a.log_b |
-                                (first + 16 * wave & in_page);
-            codes = make_rsrc(a.codes + own * kLatent, real ? 16 * kLatent : 0);
-            rope = make_rsrc(a.rope + own * kLatentRope, real ? 16 * kLatentRope * 2 : 0);
-            scale = a.scales + (real ? (int64_t)page << a.log_b | (first + lane & in_page) : 0);
+            const uint32_t in_page = (1u << a.log_b) - 1, first = (uint32_t)u.tile * kLatTile;
+            const uint32_t page = (uint32_t)min(max(entry, 0), (int)a.pages - 1);        // slots have 31 bits
+            const uint32_t own = (uint32_t)__builtin_amdgcn_readlane((int)page, 16 * wave) << a.log_b |
+                                 (first + 16 * wave & in_page);
+            codes = make_rsrc(a.codes + (uint64_t)own * kLatent, real ? 16 * kLatent : 0);
+            rope = make_rsrc(a.rope + (uint64_t)own * kLatentRope, real ? 16 * kLatentRope * 2 : 0);
+            scale = a.scales + (page << a.log_b | (first + lane & in_page));
         }
         __device__ __forceinline__ void load(uint8_t* st, int k) const {
             const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -245,7 +296,9 @@ struct LatentWalk {
     // S^T of 32 tokens: rows of C are widened with their token's scale.  Codes are read four chunks
     // ahead and widened one ahead of the matrix instructions that take them, which would otherwise wait
     // for the conversion; between them, the loads of a tile to come.
-    __device__ __forceinline__ v16f logits(const uint8_t* st, int b, float scale, const Fetch& fetch, uint8_t* to) const {
+    // tokens: exponents and inverses of the scales of this lane's tokens, read when there is room.
+    __device__ __forceinline__ v16f logits(const uint8_t* st, int b, float scale, const Fetch& fetch, uint8_t* to,
+                                           const float2* scales, v4f (&tokens)[8]) const {
         const int lane = threadIdx.x & 63, h = lane >> 5, row = 32 * b + (lane & 31);
         const uint8_t* const c = st + row * kLatent;
         const uint8_t* const r = st + kLatCodes + row * (kLatentRope * 2);
@@ -271,6 +324,10 @@ struct LatentWalk {
             }
             if (p + AHEAD < N) w[p + AHEAD] = read(p + AHEAD);
             if (p % 2 == 1) fetch.load(to, p / 2);
+            if (p == 16) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) tokens[i] = *(const v4f*)(scales + 8 * (i >> 1) + 4 * h + 2 * (i & 1));
+            }
             __builtin_amdgcn_sched_barrier(0);
             if (p < 16) {
                 s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lo, q[2 * p], s, 0, 0, 0);
@@ -285,25 +342,21 @@ struct LatentWalk {
         return s;
     }
 
-    // Logits to exponents of two, with the tokens' scale exponents e (in LDS) added; tokens from
-    // `seen` on are hidden.  Returns the reference that this wave's next weights need.
-    __device__ __forceinline__ float exponents(v16f& s, const float* e, float c, int seen, bool masked) const {
+    // Logits to exponents of two, with the tokens' scale exponents added; tokens from `seen` on are
+    // hidden.  Returns the reference that this wave's next weights need.
+    __device__ __forceinline__ float exponents(v16f& s, const v4f (&tokens)[8], float c, int seen, bool masked) const {
         const int h = (threadIdx.x & 63) >> 5;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const v4f ev = *(const v4f*)(e + 8 * i + 4 * h);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[4 * i + j] = __builtin_fmaf(s[4 * i + j], c, ev[j]);
-        }
+        for (int i = 0; i < 16; ++i) s[i] = __builtin_fmaf(s[i], c, tokens[i >> 1][2 * (i & 1)]);
         if (masked) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 if (8 * (i >> 2) + 4 * h + (i & 3) >= seen) s[i] = neg_inf();
         }
-        float top = s[0];
+        float top[4];
 #pragma unroll
-        for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
-        const float x = __builtin_ceilf(half_max(top));
+        for (int i = 0; i < 4; ++i) top[i] = fmaxf(fmaxf(s[i], s[i + 4]), fmaxf(s[i + 8], s[i + 12]));
+        const float x = __builtin_ceilf(half_max(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]))));
         return x > m + kLatSlack ? x : m;
     }
 
@@ -312,20 +365,17 @@ struct LatentWalk {
         return from == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(from - to);
     }
 
-    // Weights of 32 tokens against the reference m, and their share of the norm (inv: inverse scales).
-    __device__ __forceinline__ void weights(const v16f& s, const float* inv, h8v (&w)[2]) {
-        const int h = (threadIdx.x & 63) >> 5;
+    // Weights of 32 tokens against the reference m, and their share of the norm.
+    __device__ __forceinline__ void weights(const v16f& s, const v4f (&tokens)[8], h8v (&w)[2]) {
         const float ref = m == neg_inf() ? 0.f : m;
+        float sum[4] = {l, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const v4f iv = *(const v4f*)(inv + 8 * i + 4 * h);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float y = __builtin_amdgcn_exp2f(s[4 * i + j] - ref);
-                l = __builtin_fmaf(y, iv[j], l);
-                w[i >> 1][(i & 1) * 4 + j] = (_Float16)y;
-            }
+        for (int i = 0; i < 16; ++i) {
+            const float y = __builtin_amdgcn_exp2f(s[i] - ref);
+            sum[i & 3] = __builtin_fmaf(y, tokens[i >> 1][2 * (i & 1) + 1], sum[i & 3]);
+            w[i >> 3][i & 7] = (_Float16)y;
         }
+        l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
 
     // O^T += C^T P^T over a tile's tokens, 16 at a time; read and widened ahead as in logits().
@@ -357,109 +407,59 @@ struct LatentWalk {
         }
     }
 
-    // What a walk is about: everything but limit (tokens that this lane's row sees) is uniform.
-    struct Run {
-        int r, t0, t1, kv_len, limit, free_limit;    // free_limit: tokens that all rows see
-        float c;
-    };
-
     // Bytes behind the last token may hold anything, and 0 * NaN is NaN.
-    static __device__ __forceinline__ void clear_tail(uint8_t* st, const Run& run, int tile) {
-        const int base = tile * kLatTile;
-        if (base <= run.kv_len - kLatTile) return;
-        const int from = max(run.kv_len - base, 0) * (kLatent / 16);
-        for (int x = from + threadIdx.x; x < kLatCodes / 16; x += kLatThreads)
+    static __device__ __forceinline__ void clear_tail(uint8_t* st, const LatentUnit& u) {
+        const int base = u.tile * kLatTile;
+        if (base <= u.it.kv_len - kLatTile) return;
+        for (int x = (u.it.kv_len - base) * (kLatent / 16) + threadIdx.x; x < kLatCodes / 16; x += kLatThreads)
             *(uint4*)(st + x * 16) = make_uint4(0, 0, 0, 0);
-        __syncthreads();
+        barrier_written();
     }
 
-    // Tiles run.t0 < run.t1 of an item.  While one is worked on the next is on its way, and the one
-    // after that is asked for.
-    __device__ __forceinline__ void walk(const LatentArgs& a, const LatentLds& lds, const LatentItem& it, int row,
-                                         const Run& run) {
-        const int lane = threadIdx.x & 63, t0 = run.t0, t1 = run.t1;
-        uint8_t *const st0 = lds.st0, *const st1 = lds.st1, *const st2 = lds.st2;
-        const int ent0 = entry(a, run.r, t0, run.kv_len), ent1 = entry(a, run.r, t0 + 1, run.kv_len);
-        int ent2 = entry(a, run.r, t0 + 2, run.kv_len);
-        const Fetch f0(a, t0, ent0, true), f1(a, t0 + 1, ent1, t0 + 1 < t1);
-        float sc0 = *f0.scale, sc1 = *f1.scale, sc2 = 0.f;
-#pragma unroll
-        for (int k = 0; k < FETCHES; ++k) f0.load(st0, k);
-        load_q(a, it, row);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int k = 0; k < FETCHES; ++k) f1.load(st1, k);
-        const int pair = (rg * 2 + tg) * 128 + lane, first = rg * 256 + lane;
-        const auto step = [&](int tile, uint8_t* st, uint8_t* ahead, float sc, float& sc_ahead) __attribute__((always_inline)) {
-            wait_vmcnt<FETCHES>();                               // all but the next tile's loads
-            barrier_lds();
-            __builtin_amdgcn_sched_barrier(0);
-            const Fetch fetch(a, tile + 2, ent2, tile + 2 < t1);
-            ent2 = entry(a, run.r, tile + 3, run.kv_len);
-            sc_ahead = *fetch.scale;
-            __builtin_amdgcn_sched_barrier(0);
-            clear_tail(st, run, tile);
-            // the scale's exponents and inverses, in this wave's own bytes of LDS
-            const uint32_t ex = __float_as_uint(sc) >> 23 & 255;
-            lds.scales[0][lane] = ex == 255 ? __uint_as_float(0x7FC00000u) : (float)((int)ex - 127);
-            lds.scales[1][lane] = ex == 255 ? 0.f : __uint_as_float((254 - ex) << 23);
-            __builtin_amdgcn_wave_barrier();
-            const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(sc), __float_as_uint(sc), false, false);
-            v16f s = logits(st, tg, __uint_as_float(tg == 0 ? both[0] : both[1]), fetch, ahead);
-            const int base = tile * kLatTile;
-            const float m_new = exponents(s, lds.scales[0] + 32 * tg, run.c, run.limit - base - 32 * tg,
-                                          base > run.free_limit - kLatTile);
-            const float before = m;
-            l *= m == m_new ? 1.f : shrink(m, m_new);
-            m = m_new;
-            h8v w[4];
-            {
-                h8v mine[2];
-                weights(s, lds.scales[1] + 32 * tg, mine);
-                if (gives) {
-                    lds.trade[pair] = __builtin_bit_cast(uint4, mine[0]);
-                    lds.trade[pair + 64] = __builtin_bit_cast(uint4, mine[1]);
-                    lds.refs[pair] = m;
-                }
+    // One unit, whose tile has landed in st.
+    __device__ __forceinline__ void work(const LatentLds& lds, const LatentUnit& u, uint8_t* st, float sc, float c,
+                                         const Fetch& fetch, uint8_t* to) {
+        const int lane = threadIdx.x & 63, pair = (rg * 2 + tg) * 128 + lane, first = rg * 256 + lane;
+        clear_tail(st, u);
+        const uint32_t ex = __float_as_uint(sc) >> 23 & 255;     // 255: a token that is not finite
+        lds.scales[lane] = make_float2(ex == 255 ? __uint_as_float(0x7FC00000u) : (float)((int)ex - 127),
+                                       ex == 255 ? 0.f : __uint_as_float((254 - ex) << 23));
+        __builtin_amdgcn_wave_barrier();
+        const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(sc), __float_as_uint(sc), false, false);
+        v4f tokens[8];
+        v16f s = logits(st, tg, __uint_as_float(tg == 0 ? both[0] : both[1]), fetch, to, lds.scales + 32 * tg, tokens);
+        const int base = u.tile * kLatTile;
+        const float m_new = exponents(s, tokens, c, limit - base - 32 * tg, base > free_limit - kLatTile);
+        const float before = m;
+        l *= m == m_new ? 1.f : shrink(m, m_new);
+        m = m_new;
+        h8v w[4];
+        {
+            h8v mine[2];
+            weights(s, tokens, mine);
+            if (gives) {
+                lds.trade[pair] = __builtin_bit_cast(uint4, mine[0]);
+                lds.trade[pair + 64] = __builtin_bit_cast(uint4, mine[1]);
+                lds.refs[pair] = m;
             }
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_waitcnt(15 | 7 << 4 | 3 << 14);   // lgkmcnt 0
-            barrier_lds();
-            const float m0 = lds.refs[first], m1 = lds.refs[first + 128];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) w[x] = __builtin_bit_cast(h8v, lds.trade[first + 64 * x]);
-            // the wave's rows' reference is that of O in all waves: the larger of the two
-            if (__any(m0 != m1 || m0 != before)) {
-                const float top = fmaxf(m0, m1), f0 = shrink(m0, top), f1 = shrink(m1, top), alpha = shrink(before, top);
-                w[0] *= (_Float16)f0;
-                w[1] *= (_Float16)f0;
-                w[2] *= (_Float16)f1;
-                w[3] *= (_Float16)f1;
-#pragma unroll
-                for (int d = 0; d < DT; ++d) o[d] *= alpha;
-                l *= m == top ? 1.f : shrink(m, top);
-                m = top;
-            }
-            values(st, w);
-        };
-        for (int tile = t0; tile < t1; tile += 3) {
-            step(tile, st0, st2, sc0, sc2);
-            if (tile + 1 < t1) step(tile + 1, st1, st0, sc1, sc0);
-            if (tile + 2 < t1) step(tile + 2, st2, st1, sc2, sc1);
         }
-        wait_vmcnt<0>();
-        __syncthreads();                                         // every wave is done with the stages
-    }
-
-    // No tiles: rows that see nothing.
-    __device__ __forceinline__ void nothing() {
+        barrier_written();
+        const float m0 = lds.refs[first], m1 = lds.refs[first + 128];
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
+        for (int x = 0; x < 4; ++x) w[x] = __builtin_bit_cast(h8v, lds.trade[first + 64 * x]);
+        // the rows' reference is that of O in all waves: the larger of the two
+        if (__any(m0 != m1 || m0 != before)) {
+            const float top = fmaxf(m0, m1), f0 = shrink(m0, top), f1 = shrink(m1, top), alpha = shrink(before, top);
+            w[0] *= (_Float16)f0;
+            w[1] *= (_Float16)f0;
+            w[2] *= (_Float16)f1;
+            w[3] *= (_Float16)f1;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
-        m = neg_inf();
-        l = 0.f;
+            for (int d = 0; d < DT; ++d) o[d] *= alpha;
+            l *= m == top ? 1.f : shrink(m, top);
+            m = top;
+        }
+        values(st, w);
     }
 
     // The rows' norms, over both halves of the tokens (which have one reference).
@@ -467,9 +467,18 @@ struct LatentWalk {
         l = half_sum(l);
         const int at = rg * 256 + (threadIdx.x & 63);
         if (gives) lds.refs[at + 128 * tg + 64] = l;
-        __syncthreads();
+        barrier_written();
         l = lds.refs[at + 64] + lds.refs[at + 192];
-        __syncthreads();
+    }
+
+    // Rows that see nothing.
+    __device__ __forceinline__ void nothing() {
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+        m = neg_inf();
+        l = 0.f;
     }
 
     // The rows' results to out and lse.
@@ -515,47 +524,100 @@ __device__ __forceinline__ int latent_owner(int64_t units, int64_t u) {
     return (int)(units < kLatGroups ? u : quotient((u + 1) * kLatGroups - 1, units));
 }
 
-#define LATENT_LDS(RW)                                                         \
-    __shared__ __attribute__((aligned(1024))) uint8_t st0[kLatStage];          \
-    __shared__ __attribute__((aligned(1024))) uint8_t st1[kLatStage];          \
-    __shared__ __attribute__((aligned(1024))) uint8_t st2[kLatStage];          \
-    __shared__ __attribute__((aligned(16))) float scales[4][2][kLatTile];      \
-    __shared__ uint4 trade[RW * 256];                                          \
-    __shared__ float refs[RW * 256];                                           \
-    const LatentLds lds = {st0, st1, st2, scales[wave], trade, refs}
-
-// The rows of a run, or all rows of an item.
-template <class W>
-__device__ __forceinline__ void latent_run(const LatentArgs& a, W& w, const LatentLds& lds, const LatentItem& it, int r,
-                                           int rt, int t0, int t1) {
-    const int row = w.row(rt);
-    t1 = min(t1, latent_tiles(it.limit(a.by_heads.of(min((rt + 1) * W::ROWS, it.rows) - 1))));
-    if (t0 < t1) {
-        const typename W::Run run = {r,  t0, t1, it.kv_len, row < it.rows ? it.limit(a.by_heads.of(row)) : 0,
-                                     it.limit(a.by_heads.of(rt * W::ROWS)), a.scale * kLog2e};
-        w.walk(a, lds, it, row, run);
-        w.join(lds);
-    } else {
-        w.nothing();
+// A workgroup's units, of items whose rows it stores, or whose parts.  While one is worked on the next
+// is on its way to LDS, and the one after that is asked for: also over the items' ends, where a walk
+// that began anew for each item spent 5 us a time on loads that followed one another.
+template <int RW, bool kSplit>
+__device__ __forceinline__ void latent_walk(const LatentArgs& a, LatentStream<32 * RW>& stream, int64_t units, int64_t at,
+                                            int row_tiles) {
+    using W = LatentWalk<RW>;
+    __shared__ __attribute__((aligned(1024))) uint8_t st0[kLatStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t st1[kLatStage];
+    __shared__ __attribute__((aligned(1024))) uint8_t st2[kLatStage];
+    __shared__ __attribute__((aligned(16))) float2 scales[4][kLatTile];
+    __shared__ uint4 trade[RW * 256];
+    __shared__ float refs[RW * 256];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const LatentLds lds = {st0, st1, st2, scales[wave], trade, refs};
+    const float c = a.scale * kLog2e;
+    W w;
+    w.init();
+    bool first = true;
+    // unit 0 is worked on, 1 on its way, 2 asked for
+    LatentUnit u0 = stream.at;
+    bool real1 = stream.step(a);
+    LatentUnit u1 = stream.at;
+    bool real2 = real1 && stream.step(a);
+    LatentUnit u2 = stream.at;
+    const int ent0 = w.entry(a, u0), ent1 = w.entry(a, u1);
+    int ent2 = w.entry(a, u2);
+    float sc0, sc1, sc2 = 0.f;
+    {
+        const typename W::Fetch f0(a, u0, ent0, true), f1(a, u1, ent1, real1);
+        sc0 = *f0.scale;
+        sc1 = *f1.scale;
+#pragma unroll
+        for (int k = 0; k < W::FETCHES; ++k) f0.load(st0, k);
+        w.ask_q(a, u0);
+        w.begin(a, u0);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int k = 0; k < W::FETCHES; ++k) f1.load(st1, k);
+    }
+    const auto step = [&](uint8_t* st, uint8_t* ahead, float sc, float& sc_ahead) __attribute__((always_inline)) {
+        wait_vmcnt<W::FETCHES>();                                // all but the next unit's loads
+        barrier_lds();
+        __builtin_amdgcn_sched_barrier(0);
+        const typename W::Fetch fetch(a, u2, ent2, real2);
+        const bool real3 = real2 && stream.step(a);
+        const LatentUnit u3 = stream.at;
+        ent2 = w.entry(a, u3);
+        sc_ahead = *fetch.scale;
+        __builtin_amdgcn_sched_barrier(0);
+        w.work(lds, u0, st, sc, c, fetch, ahead);
+        ++at;
+        if (!real1 || u1.tile == 0) {                            // the run's last unit
+            const bool whole = !kSplit || (w.from == 0 && u0.tile + 1 == u0.tiles);
+            const int slot = (int)blockIdx.x * 2 + (first ? 0 : 1);
+            if (kSplit && w.from == 0 && threadIdx.x == 0)
+                latent_info(a, W::ROWS)[u0.r * row_tiles + u0.rt] =
+                    make_int2(slot, whole ? 0 : latent_owner(units, at - 1 - u0.tile + u0.tiles - 1) - (int)blockIdx.x);
+            if (real1) w.ask_q(a, u1);
+            w.join(lds);
+            if (whole) w.store(a, u0.it, w.row(u0.rt));
+            else w.store_part(a, slot);
+            if (!real1) {
+                wait_vmcnt<0>();                                 // no load outlives its LDS
+                return false;
+            }
+            first = false;
+            w.begin(a, u1);
+        }
+        u0 = u1;
+        u1 = u2;
+        u2 = u3;
+        real1 = real2;
+        real2 = real3;
+        return true;
+    };
+    while (step(st0, st2, sc0, sc2) && step(st1, st0, sc1, sc0) && step(st2, st1, sc2, sc1)) {
     }
 }
 
-// Every workgroup takes an even share of the tiles of all items (request, row tile), in that order.
-// Where it begins an item it notes for the join where the item's parts are: its own slot (of the two
-// that a workgroup has: its first run's and its last one's) and how many workgroups follow.
+// Every workgroup takes an even share of the units of all items, in their order.  Where it begins an
+// item it notes for the join where the item's parts are: its own slot (of the two that a workgroup has:
+// its first run's and its last one's) and how many workgroups follow.
 template <int RW>
 __global__ __launch_bounds__(kLatThreads, 1) void attn_latent_split_kernel(LatentArgs a, int row_tiles) {
-    using W = LatentWalk<RW>;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    LATENT_LDS(RW);
-    LatentRequests<W::ROWS> reqs;
+    const int lane = threadIdx.x & 63;
+    LatentStream<32 * RW> stream;
+    auto& reqs = stream.reqs;
     int64_t units = 0;
     for (int from = 0; from < a.R; from += 64) {
         reqs.load(a, from);
         units = reqs.scan(units);
     }
-    int64_t u = latent_first(units, blockIdx.x);
-    const int64_t end = latent_first(units, blockIdx.x + 1);
+    const int64_t u = latent_first(units, blockIdx.x), end = latent_first(units, blockIdx.x + 1);
     if (u >= end) return;
     if (a.R > 64) {                                              // back to the first unit's requests
         int64_t next = 0;
@@ -564,37 +626,9 @@ __global__ __launch_bounds__(kLatThreads, 1) void attn_latent_split_kernel(Laten
             next = reqs.scan(next);
         }
     }
-    int r = __builtin_amdgcn_readfirstlane(reqs.base + last_of(reqs.base + lane < a.R && reqs.before <= u));
-    W w;
-    w.init();
-    bool first = true;
-    while (u < end) {
-        const int64_t begin = reqs.from_lane(reqs.before, r - reqs.base);
-        const int64_t after = begin + reqs.from_lane(reqs.units, r - reqs.base);
-        if (u >= after) {
-            if (++r >= a.R) break;
-            if (r - reqs.base >= 64) {
-                reqs.load(a, r);
-                reqs.scan(after);
-            }
-            continue;
-        }
-        const LatentItem it = reqs.item(a, r);
-        const int nt = latent_tiles(it.kv_len);
-        const int rt = __builtin_amdgcn_readfirstlane((int)quotient(u - begin, nt));
-        const int t0 = (int)(u - begin - (int64_t)rt * nt);
-        const int count = (int)min((int64_t)(nt - t0), end - u);
-        const int slot = (int)blockIdx.x * 2 + (first ? 0 : 1);
-        if (t0 == 0 && threadIdx.x == 0) {
-            const int last = count == nt ? (int)blockIdx.x : latent_owner(units, u + nt - 1);
-            latent_info(a, W::ROWS)[r * row_tiles + rt] = make_int2(slot, last - (int)blockIdx.x);
-        }
-        latent_run(a, w, lds, it, r, rt, t0, t0 + count);
-        if (count == nt) w.store(a, it, w.row(rt));
-        else w.store_part(a, slot);
-        u += count;
-        first = false;
-    }
+    const int in = last_of(reqs.base + lane < a.R && reqs.before <= u);
+    stream.begin(a, __builtin_amdgcn_readfirstlane(reqs.base + in), u - reqs.from_lane(reqs.before, in), end - u);
+    latent_walk<RW, true>(a, stream, units, u, row_tiles);
 }
 
 // One workgroup per item: enough of them to fill the chip, or no workspace.  Request r's items are
@@ -602,24 +636,32 @@ __global__ __launch_bounds__(kLatThreads, 1) void attn_latent_split_kernel(Laten
 template <int RW>
 __global__ __launch_bounds__(kLatThreads, 1) void attn_latent_item_kernel(LatentArgs a) {
     using W = LatentWalk<RW>;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    LATENT_LDS(RW);
+    const int lane = threadIdx.x & 63;
     const int64_t b = blockIdx.x;
     const auto start = [&](int q, int r) {
         return min(max((int64_t)q, (int64_t)0), a.T) * a.heads / W::ROWS + r;
     };
     const int each64 = a.q_offsets[min(lane * 64, a.R)];
     const int from = last_of(lane * 64 < a.R && start(each64, lane * 64) <= b) * 64;
-    const int mine = a.q_offsets[min(from + lane, a.R)];
-    const int r = __builtin_amdgcn_readfirstlane(from + last_of(from + lane < a.R && start(mine, from + lane) <= b));
-    const LatentItem it = LatentItem::of(a, a.q_offsets[r], a.q_offsets[r + 1], a.kv_lens[r]);
+    LatentStream<W::ROWS> stream;
+    stream.reqs.load(a, from);
+    const int r = __builtin_amdgcn_readfirstlane(from + last_of(from + lane < a.R && start(stream.reqs.q0, from + lane) <= b));
+    const LatentItem it = stream.reqs.item(a, r);
     const int64_t at = b - start((int)it.q0, r);
     if (at < 0 || at * W::ROWS >= it.rows) return;
     const int rt = __builtin_amdgcn_readfirstlane((int)at);
-    W w;
-    w.init();
-    latent_run(a, w, lds, it, r, rt, 0, latent_tiles(it.kv_len));
-    w.store(a, it, w.row(rt));
+    const int last = min((rt + 1) * W::ROWS, it.rows) - 1;
+    const int tiles = latent_tiles(it.limit(a.by_heads.of(last)));         // that its rows see
+    if (tiles == 0) {
+        W w;
+        w.init();
+        w.nothing();
+        w.store(a, it, w.row(rt));
+        return;
+    }
+    stream.at = {r, rt, 0, tiles, it};
+    stream.left = tiles - 1;
+    latent_walk<RW, false>(a, stream, 0, 0, 0);
 }
 static_assert(kKvMaxRequests <= 64 * 64, "a request is found in two steps of 64");
 
