@@ -74,6 +74,14 @@ __device__ __forceinline__ int2* latent_info(const LatentArgs& a, int rows) {
     return (int2*)(latent_ml(a, rows) + kLatSlots * rows);
 }
 
+// Barrier behind everything that this wave wrote to LDS or has on its way there.
+__device__ __forceinline__ void barrier_all() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(7 << 4);                          // vmcnt 0, lgkmcnt 0
+    barrier_lds();
+}
+
 // Barrier behind what this wave wrote to LDS, but not behind its loads that are on their way there.
 __device__ __forceinline__ void barrier_written() {
     asm volatile("" ::: "memory");
@@ -220,31 +228,83 @@ struct LatentWalk {
     // this lane's row, counted in the item
     __device__ __forceinline__ int row(int rt) const { return rt * ROWS + rg * 32 + (threadIdx.x & 31); }
 
-    // To an item's first unit here: queries of this lane's row (of the last one, where there is none:
-    // nothing of it is stored) go into accumulation registers, where the matrix instructions take them
-    // from.
-    __device__ __forceinline__ void ask_q(const LatentArgs& a, const LatentUnit& u) {
-        const int h = (threadIdx.x & 63) >> 5;
-        int j;
-        const int64_t t = u.it.q0 + a.by_heads.of(min(row(u.rt), u.it.rows - 1), j);
-        const uint16_t* const ql = a.q_latent + t * a.ql_ts + (int64_t)j * a.ql_hs + 16 * h;
-        const uint16_t* const qr = a.q_rope + t * a.qr_ts + (int64_t)j * a.qr_hs + 8 * h;
-        const bool vec = ((uintptr_t)a.q_latent | (uintptr_t)a.q_rope) % 16 == 0 &&
-                         (a.ql_ts | a.ql_hs | a.qr_ts | a.qr_hs) % 8 == 0;
-        // dims of operand s: a 16-byte read of codes feeds two matrix instructions
-        const auto at = [&](int s) { return s < 32 ? ql + s / 2 * 32 + s % 2 * 8 : qr + (s - 32) * 16; };
-        // one branch for all of the loads: with one each, each is waited for
-        if (vec) {
+    // An item's queries come by way of a free stage, 512 / RW dims of all rows at a time, as whole rows,
+    // and go from there into accumulation registers, where the matrix instructions take them from.
+    // (Straight from memory a wave's lanes read 32 bytes of 32 rows at a time: 14000 cycles for 64 rows.)
+    // Rows behind the item's last are copies of that one: nothing of them is stored.  Rows that are not
+    // 16-byte aligned, or far apart, go the slow way, by load_q.
+    static constexpr int QROW = 1024 / RW;           // bytes of a staged row; the rotated dims come last
+    // (chunk c of row r lies at c ^ (r & 15), or at rope_swz(r): sixteen rows' same chunk is spread)
+    template <int X>
+    static __device__ __forceinline__ void stage_q(const LatentArgs& a, const LatentUnit& u, uint8_t* st) {
+        constexpr int MINE = ROWS / 4, C = QROW / 16;            // rows of a wave; chunks of a row
+        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int first = u.rt * ROWS + wave * MINE, last = u.it.rows - 1;
+        const int t0 = a.by_heads.of(min(first, last));
+        const int64_t t = u.it.q0 + t0;
+        // a lane's row steps by `by`; offsets from the first row's token have 32 bits (a.q_near)
+        const auto rows = [&](uint32_t ts, uint32_t hs, int r, int by, int n, auto&& put) {
+            int j, dj, lj;
+            const uint32_t end = (a.by_heads.of(last, lj) - t0) * ts + lj * hs;
+            uint32_t at = (a.by_heads.of(min(first + r, last), j) - t0) * ts;
+            at += j * hs;
+            const int dt = a.by_heads.of(by, dj);
+            const uint32_t step = dt * ts + dj * hs, wrap = ts - a.heads * hs;
 #pragma unroll
-            for (int s = 0; s < 36; ++s) q[s] = *(const bf8v*)at(s);
-        } else {
-#pragma unroll
-            for (int s = 0; s < 36; ++s) q[s] = load_q8(at(s), false, false);
-        }
+            for (int k = 0; k < n; ++k) {
+                put(k, r, first + r < last ? at : end);
+                r += by;
+                j += dj;
+                at += step;
+                if (j >= a.heads) {
+                    j -= a.heads;
+                    at += wrap;
+                }
+            }
+        };
+        const __amdgpu_buffer_rsrc_t latents = make_rsrc(a.q_latent + t * a.ql_ts, ~0ull);
+        rows((uint32_t)a.ql_ts * 2, (uint32_t)a.ql_hs * 2, lane / C, RW, MINE / RW,
+             [&](int k, int r, uint32_t at) __attribute__((always_inline)) {
+                 buf_lds16(latents, at + ((lane % C ^ (wave * MINE + r & 15)) << 4),
+                           X * 512, st + wave * (MINE * QROW) + k * 1024);
+             });
+        const __amdgpu_buffer_rsrc_t ropes = make_rsrc(a.q_rope + t * a.qr_ts, ~0ull);
+        if (X == RW - 1)
+            rows((uint32_t)a.qr_ts * 2, (uint32_t)a.qr_hs * 2, lane / 8, 8, MINE / 8,
+                 [&](int k, int r, uint32_t at) __attribute__((always_inline)) {
+                     buf_lds16(ropes, at + ((lane % 8 ^ rope_swz(wave * MINE + r)) << 4),
+                               0, st + kLatCodes + wave * (MINE * 128) + k * 1024);
+                 });
     }
-    __device__ __forceinline__ void begin(const LatentArgs& a, const LatentUnit& u) {
+    template <int X>
+    __device__ __forceinline__ void read_q(const uint8_t* st) {
+        const int h = (threadIdx.x & 63) >> 5, r = rg * 32 + (threadIdx.x & 31);
+        // operand s: dims 32 (s / 2) + 16 h + 8 (s % 2) .., as a 16-byte read of codes feeds two
+#pragma unroll
+        for (int s = X * 16; s < X * 16 + 32 / RW; ++s) {
+            const int chunk = s / 2 * 4 + 2 * h + s % 2 - X * 32;
+            q[s] = *(const bf8v*)(st + r * QROW + ((chunk ^ (r & 15)) << 4));
+        }
+        if (X == RW - 1) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                q[32 + s] = *(const bf8v*)(st + kLatCodes + r * 128 + (((2 * s + h) ^ rope_swz(r)) << 4));
+        }
+#pragma unroll
+        for (int s = X * 16; s < (X == RW - 1 ? 36 : X * 16 + 32 / RW); ++s) asm volatile("" : "+a"(q[s]));
+    }
+    __device__ __forceinline__ void load_q(const LatentArgs& a, const LatentUnit& u) {
+        const int h = (threadIdx.x & 63) >> 5, r = row(u.rt);
+        int j;
+        const int64_t t = u.it.q0 + a.by_heads.of(min(r, u.it.rows - 1), j);
+        const uint16_t* const ql = a.q_latent + t * a.ql_ts + j * a.ql_hs + 16 * h;
+        const uint16_t* const qr = a.q_rope + t * a.qr_ts + j * a.qr_hs + 8 * h;
+#pragma unroll
+        for (int s = 0; s < 36; ++s) q[s] = load_q8(s < 32 ? ql + s / 2 * 32 + s % 2 * 8 : qr + (s - 32) * 16, false, false);
 #pragma unroll
         for (int s = 0; s < 36; ++s) asm volatile("" : "+a"(q[s]));
+    }
+    __device__ __forceinline__ void begin(const LatentArgs& a, const LatentUnit& u) {
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -551,19 +611,26 @@ __device__ __forceinline__ void latent_walk(const LatentArgs& a, LatentStream<32
     LatentUnit u2 = stream.at;
     const int ent0 = w.entry(a, u0), ent1 = w.entry(a, u1);
     int ent2 = w.entry(a, u2);
-    float sc0, sc1, sc2 = 0.f;
-    {
-        const typename W::Fetch f0(a, u0, ent0, true), f1(a, u1, ent1, real1);
-        sc0 = *f0.scale;
-        sc1 = *f1.scale;
-#pragma unroll
-        for (int k = 0; k < W::FETCHES; ++k) f0.load(st0, k);
-        w.ask_q(a, u0);
-        w.begin(a, u0);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int k = 0; k < W::FETCHES; ++k) f1.load(st1, k);
+    const bool aligned = a.q_near;
+    if (aligned) {
+        w.template stage_q<0>(a, u0, st1);
+        if constexpr (RW == 2) w.template stage_q<1>(a, u0, st2);
     }
+    const typename W::Fetch f0(a, u0, ent0, true), f1(a, u1, ent1, real1);
+    float sc0 = *f0.scale, sc1 = *f1.scale, sc2 = 0.f;
+#pragma unroll
+    for (int k = 0; k < W::FETCHES; ++k) f0.load(st0, k);
+    if (aligned) {
+        barrier_all();
+        w.template read_q<0>(st1);
+        if constexpr (RW == 2) w.template read_q<1>(st2);
+        barrier_written();
+    } else {
+        w.load_q(a, u0);
+    }
+    w.begin(a, u0);
+#pragma unroll
+    for (int k = 0; k < W::FETCHES; ++k) f1.load(st1, k);
     const auto step = [&](uint8_t* st, uint8_t* ahead, float sc, float& sc_ahead) __attribute__((always_inline)) {
         wait_vmcnt<W::FETCHES>();                                // all but the next unit's loads
         barrier_lds();
@@ -582,8 +649,8 @@ __device__ __forceinline__ void latent_walk(const LatentArgs& a, LatentStream<32
             if (kSplit && w.from == 0 && threadIdx.x == 0)
                 latent_info(a, W::ROWS)[u0.r * row_tiles + u0.rt] =
                     make_int2(slot, whole ? 0 : latent_owner(units, at - 1 - u0.tile + u0.tiles - 1) - (int)blockIdx.x);
-            if (real1) w.ask_q(a, u1);
-            w.join(lds);
+            w.join(lds);                                         // and all waves are done with st
+            if (real1 && aligned) w.template stage_q<0>(a, u1, st);
             if (whole) w.store(a, u0.it, w.row(u0.rt));
             else w.store_part(a, slot);
             if (!real1) {
@@ -591,6 +658,19 @@ __device__ __forceinline__ void latent_walk(const LatentArgs& a, LatentStream<32
                 return false;
             }
             first = false;
+            if (aligned) {
+                barrier_all();
+                w.template read_q<0>(st);
+                barrier_written();
+                if constexpr (RW == 2) {
+                    w.template stage_q<1>(a, u1, st);
+                    barrier_all();
+                    w.template read_q<1>(st);
+                    barrier_written();
+                }
+            } else {
+                w.load_q(a, u1);
+            }
             w.begin(a, u1);
         }
         u0 = u1;
@@ -743,8 +823,13 @@ static hipError_t latent_launch(const LatentArgs& a, const LatentPlan& p, hipStr
     return hipGetLastError();
 }
 
-hipError_t launch_attn_latent(const LatentArgs& a, hipStream_t stream) {
+hipError_t launch_attn_latent(LatentArgs a, hipStream_t stream) {
     const LatentPlan p = latent_plan(a.R, a.max_new, a.heads);
+    // sixteen rows of queries, in memory, span at most so many tokens
+    const auto near = [&](int64_t ts, int64_t hs) {
+        return ts < (1 << 26) && hs < ((int64_t)1 << 30) / a.heads && (ts | hs) % 8 == 0;
+    };
+    a.q_near = ((uintptr_t)a.q_latent | (uintptr_t)a.q_rope) % 16 == 0 && near(a.ql_ts, a.ql_hs) && near(a.qr_ts, a.qr_hs);
     if (p.rw == 1) return latent_launch<1>(a, p, stream);
     return latent_launch<2>(a, p, stream);
 }

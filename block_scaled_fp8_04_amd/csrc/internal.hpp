@@ -190,8 +190,9 @@ struct LatentArgs {
     int64_t o_ts, o_hs;
     float* lse;
     float* ws;
+    bool q_near;             // set by the launcher: queries are aligned and rows' offsets small
 };
 size_t attn_latent_workspace_bytes(int64_t R, int64_t max_new, int32_t heads);
-hipError_t launch_attn_latent(const LatentArgs& a, hipStream_t stream);
+hipError_t launch_attn_latent(LatentArgs a, hipStream_t stream);
 
 }  // namespace bfp8
