@@ -92,13 +92,11 @@ __device__ __forceinline__ void barrier_written() {
 
 // A request's part in the launch: its first new token, its query rows and cached tokens.
 struct LatentItem {
-    int64_t q0;
-    int n, rows, kv_len;
+    int q0, n, rows, kv_len;
     static __device__ __forceinline__ LatentItem of(const LatentArgs& a, int from, int to, int kv_len) {
         LatentItem it;
-        it.q0 = min(max((int64_t)from, (int64_t)0), a.T);
-        const int64_t q1 = min(max((int64_t)to, it.q0), a.T);
-        it.n = (int)(q1 - it.q0);
+        it.q0 = min(max(from, 0), (int)a.T);                     // (T has 29 bits)
+        it.n = min(max(to, it.q0), (int)a.T) - it.q0;
         it.rows = (int)min((int64_t)it.n, a.max_new) * a.heads;
         it.kv_len = (int)min(max((int64_t)kv_len, (int64_t)0), a.width << a.log_b);
         return it;
@@ -148,45 +146,69 @@ struct LatentRequests {
     }
 };
 
-// A unit of work: a tile of an item (request, row tile).  Uniform.
-struct LatentUnit {
-    int r, rt, tile, tiles;                          // tiles: of the item
+// An item, that is a request's row tile, and its tiles.  Uniform.
+struct LatentJob {
+    int r, rt, tiles;
     LatentItem it;
+    __device__ __forceinline__ void put(int4* to) const {
+        if ((threadIdx.x & 63) == 0) {
+            to[0] = make_int4(r, rt, tiles, it.q0);
+            to[1] = make_int4(it.n, it.rows, it.kv_len, 0);
+        }
+    }
+    static __device__ __forceinline__ LatentJob get(const int4* from) {
+        const int4 x = from[0], y = from[1];
+        const auto u = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+        return {u(x.x), u(x.y), u(x.z), {u(x.w), u(y.x), u(y.y), u(y.z)}};
+    }
 };
 
-// A workgroup's units, one after the other.  It is ahead of the work: loads are asked for by it.
+// A workgroup's units of work, tiles of its items, one after the other.  It is up to three units ahead of
+// the work: loads are asked for by it.  Its items are left in LDS, four at a time, for the work to find
+// them: held in scalar registers for each unit, they would be most of what these spill.
 template <int ROWS>
 struct LatentStream {
     LatentRequests<ROWS> reqs;
-    LatentUnit at;
+    LatentJob job;
+    int tile;
     int64_t left;                                    // units behind this one
+    int4* jobs;                                      // this wave's
+    int turn;                                        // number of the item
 
     // From unit `local` of request r (one of reqs) on.
     __device__ __forceinline__ void begin(const LatentArgs& a, int r, int64_t local, int64_t count) {
-        at.r = r;
-        at.it = reqs.item(a, r);
-        at.tiles = latent_tiles(at.it.kv_len);
-        at.rt = __builtin_amdgcn_readfirstlane((int)quotient(local, at.tiles));
-        at.tile = (int)(local - (int64_t)at.rt * at.tiles);
+        job.r = r;
+        job.it = reqs.item(a, r);
+        job.tiles = latent_tiles(job.it.kv_len);
+        job.rt = __builtin_amdgcn_readfirstlane((int)quotient(local, job.tiles));
+        tile = (int)(local - (int64_t)job.rt * job.tiles);
         left = count - 1;
+    }
+    __device__ __forceinline__ void keep(int4* to) {
+        jobs = to;
+        turn = 0;
+        job.put(jobs);
     }
     // To the next unit; none: stays.
     __device__ __forceinline__ bool step(const LatentArgs& a) {
         if (left <= 0) return false;
         --left;
-        if (++at.tile < at.tiles) return true;
-        at.tile = 0;
-        if (++at.rt * ROWS < at.it.rows) return true;
-        at.rt = 0;
-        uint64_t later = __ballot(reqs.units > 0) & ~((2ull << (at.r - reqs.base)) - 1);
-        while (later == 0 && reqs.base + 64 < a.R) {
-            reqs.load(a, reqs.base + 64);
-            later = __ballot(reqs.units > 0);
+        if (++tile < job.tiles) return true;
+        tile = 0;
+        if (++job.rt * ROWS >= job.it.rows) {
+            job.rt = 0;
+            uint64_t later = __ballot(reqs.units > 0) & ~((2ull << (job.r - reqs.base)) - 1);
+            while (later == 0 && reqs.base + 64 < a.R) {
+                reqs.load(a, reqs.base + 64);
+                later = __ballot(reqs.units > 0);
+            }
+            if (later == 0) return false;                        // (not with units left)
+            job.r = reqs.base + __ffsll((unsigned long long)later) - 1;
+            job.it = reqs.item(a, job.r);
+            job.tiles = latent_tiles(job.it.kv_len);
         }
-        if (later == 0) return false;                            // (not with units left)
-        at.r = reqs.base + __ffsll((unsigned long long)later) - 1;
-        at.it = reqs.item(a, at.r);
-        at.tiles = latent_tiles(at.it.kv_len);
+        ++turn;
+        job.put(jobs + (turn & 3) * 2);
         return true;
     }
 };
@@ -196,6 +218,7 @@ struct LatentLds {
     float2* scales;                                  // this wave's [64 tokens] exponents and inverses
     uint4* trade;                                    // [row half][token half][2][64 lanes] weights
     float* refs;                                     // [row half][token half][2][64 lanes] references, norms
+    int4* jobs;                                      // this wave's four items
 };
 
 // One workgroup's way through its units.  Its four waves form weights two by two, each for 32 rows and half tg of a tile's tokens, trade them through LDS, and each sums its rows' values
@@ -216,7 +239,7 @@ struct LatentWalk {
     int rg, tg, dw;                                  // this wave's rows, tokens, dims
     bool gives;                                      // its weights are the ones that are traded
     int limit, free_limit;                           // tokens that this lane's row sees; that all rows see
-    int from;                                        // the run's first tile
+    int from, kv_len;                                // the run's first tile; cached tokens
 
     __device__ __forceinline__ void init() {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -236,7 +259,7 @@ struct LatentWalk {
     static constexpr int QROW = 1024 / RW;           // bytes of a staged row; the rotated dims come last
     // (chunk c of row r lies at c ^ (r & 15), or at rope_swz(r): sixteen rows' same chunk is spread)
     template <int X>
-    static __device__ __forceinline__ void stage_q(const LatentArgs& a, const LatentUnit& u, uint8_t* st) {
+    static __device__ __forceinline__ void stage_q(const LatentArgs& a, const LatentJob& u, uint8_t* st) {
         constexpr int MINE = ROWS / 4, C = QROW / 16;            // rows of a wave; chunks of a row
         const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         const int first = u.rt * ROWS + wave * MINE, last = u.it.rows - 1;
@@ -293,7 +316,7 @@ struct LatentWalk {
 #pragma unroll
         for (int s = X * 16; s < (X == RW - 1 ? 36 : X * 16 + 32 / RW); ++s) asm volatile("" : "+a"(q[s]));
     }
-    __device__ __forceinline__ void load_q(const LatentArgs& a, const LatentUnit& u) {
+    __device__ __forceinline__ void load_q(const LatentArgs& a, const LatentJob& u) {
         const int h = (threadIdx.x & 63) >> 5, r = row(u.rt);
         int j;
         const int64_t t = u.it.q0 + a.by_heads.of(min(r, u.it.rows - 1), j);
@@ -304,7 +327,7 @@ struct LatentWalk {
 #pragma unroll
         for (int s = 0; s < 36; ++s) asm volatile("" : "+a"(q[s]));
     }
-    __device__ __forceinline__ void begin(const LatentArgs& a, const LatentUnit& u) {
+    __device__ __forceinline__ void begin(const LatentArgs& a, const LatentJob& u, int tile) {
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -314,13 +337,14 @@ struct LatentWalk {
         const int mine = row(u.rt);
         limit = mine < u.it.rows ? u.it.limit(a.by_heads.of(mine)) : 0;
         free_limit = u.it.limit(a.by_heads.of(u.rt * ROWS));
-        from = u.tile;
+        from = tile;
+        kv_len = u.it.kv_len;
     }
 
     // The table entry of the page that holds token `lane` of a unit (of the last page, behind the end).
-    static __device__ __forceinline__ int entry(const LatentArgs& a, const LatentUnit& u) {
-        const uint32_t pos = min((uint32_t)u.tile * kLatTile + (threadIdx.x & 63), (uint32_t)u.it.kv_len - 1);
-        return (a.block_table + u.r * a.width)[pos >> a.log_b];
+    static __device__ __forceinline__ int entry(const LatentArgs& a, const LatentStream<ROWS>& s) {
+        const uint32_t pos = min((uint32_t)s.tile * kLatTile + (threadIdx.x & 63), (uint32_t)s.job.it.kv_len - 1);
+        return (a.block_table + s.job.r * a.width)[pos >> a.log_b];
     }
 
     // A unit's way to LDS: each wave brings 16 of its tokens, by ten loads that bypass the registers.
@@ -328,9 +352,9 @@ struct LatentWalk {
     struct Fetch {
         __amdgpu_buffer_rsrc_t codes, rope;
         const float* scale;                          // of token `lane`
-        __device__ __forceinline__ Fetch(const LatentArgs& a, const LatentUnit& u, int entry, bool real) {
+        __device__ __forceinline__ Fetch(const LatentArgs& a, int tile, int entry, bool real) {
             const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-            const uint32_t in_page = (1u << a.log_b) - 1, first = (uint32_t)u.tile * kLatTile;
+            const uint32_t in_page = (1u << a.log_b) - 1, first = (uint32_t)tile * kLatTile;
             const uint32_t page = (uint32_t)min(max(entry, 0), (int)a.pages - 1);        // slots have 31 bits
             const uint32_t own = (uint32_t)__builtin_amdgcn_readlane((int)page, 16 * wave) << a.log_b |
                                  (first + 16 * wave & in_page);
@@ -468,19 +492,19 @@ struct LatentWalk {
     }
 
     // Bytes behind the last token may hold anything, and 0 * NaN is NaN.
-    static __device__ __forceinline__ void clear_tail(uint8_t* st, const LatentUnit& u) {
-        const int base = u.tile * kLatTile;
-        if (base <= u.it.kv_len - kLatTile) return;
-        for (int x = (u.it.kv_len - base) * (kLatent / 16) + threadIdx.x; x < kLatCodes / 16; x += kLatThreads)
+    __device__ __forceinline__ void clear_tail(uint8_t* st, int base) const {
+        if (base <= kv_len - kLatTile) return;
+        for (int x = (kv_len - base) * (kLatent / 16) + threadIdx.x; x < kLatCodes / 16; x += kLatThreads)
             *(uint4*)(st + x * 16) = make_uint4(0, 0, 0, 0);
         barrier_written();
     }
 
     // One unit, whose tile has landed in st.
-    __device__ __forceinline__ void work(const LatentLds& lds, const LatentUnit& u, uint8_t* st, float sc, float c,
+    __device__ __forceinline__ void work(const LatentLds& lds, int tile, uint8_t* st, float sc, float c,
                                          const Fetch& fetch, uint8_t* to) {
+        const int base = tile * kLatTile;
         const int lane = threadIdx.x & 63, pair = (rg * 2 + tg) * 128 + lane, first = rg * 256 + lane;
-        clear_tail(st, u);
+        clear_tail(st, base);
         const uint32_t ex = __float_as_uint(sc) >> 23 & 255;     // 255: a token that is not finite
         lds.scales[lane] = make_float2(ex == 255 ? __uint_as_float(0x7FC00000u) : (float)((int)ex - 127),
                                        ex == 255 ? 0.f : __uint_as_float((254 - ex) << 23));
@@ -488,7 +512,6 @@ struct LatentWalk {
         const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(sc), __float_as_uint(sc), false, false);
         v4f tokens[8];
         v16f s = logits(st, tg, __uint_as_float(tg == 0 ? both[0] : both[1]), fetch, to, lds.scales + 32 * tg, tokens);
-        const int base = u.tile * kLatTile;
         const float m_new = exponents(s, tokens, c, limit - base - 32 * tg, base > free_limit - kLatTile);
         const float before = m;
         l *= m == m_new ? 1.f : shrink(m, m_new);
@@ -597,26 +620,31 @@ __device__ __forceinline__ void latent_walk(const LatentArgs& a, LatentStream<32
     __shared__ __attribute__((aligned(16))) float2 scales[4][kLatTile];
     __shared__ uint4 trade[RW * 256];
     __shared__ float refs[RW * 256];
+    __shared__ int4 jobs[4][8];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const LatentLds lds = {st0, st1, st2, scales[wave], trade, refs};
+    const LatentLds lds = {st0, st1, st2, scales[wave], trade, refs, jobs[wave]};
     const float c = a.scale * kLog2e;
     W w;
     w.init();
     bool first = true;
+    int turn = 0;                                                // the item that is worked on
     // unit 0 is worked on, 1 on its way, 2 asked for
-    LatentUnit u0 = stream.at;
+    stream.keep(lds.jobs);
+    const LatentJob job0 = stream.job;
+    int tile0 = stream.tile;
+    const int ent0 = w.entry(a, stream);
     bool real1 = stream.step(a);
-    LatentUnit u1 = stream.at;
+    int tile1 = stream.tile;
+    const int ent1 = w.entry(a, stream);
     bool real2 = real1 && stream.step(a);
-    LatentUnit u2 = stream.at;
-    const int ent0 = w.entry(a, u0), ent1 = w.entry(a, u1);
-    int ent2 = w.entry(a, u2);
+    int tile2 = stream.tile;
+    int ent2 = w.entry(a, stream);
     const bool aligned = a.q_near;
     if (aligned) {
-        w.template stage_q<0>(a, u0, st1);
-        if constexpr (RW == 2) w.template stage_q<1>(a, u0, st2);
+        w.template stage_q<0>(a, job0, st1);
+        if constexpr (RW == 2) w.template stage_q<1>(a, job0, st2);
     }
-    const typename W::Fetch f0(a, u0, ent0, true), f1(a, u1, ent1, real1);
+    const typename W::Fetch f0(a, tile0, ent0, true), f1(a, tile1, ent1, real1);
     float sc0 = *f0.scale, sc1 = *f1.scale, sc2 = 0.f;
 #pragma unroll
     for (int k = 0; k < W::FETCHES; ++k) f0.load(st0, k);
@@ -626,29 +654,29 @@ __device__ __forceinline__ void latent_walk(const LatentArgs& a, LatentStream<32
         if constexpr (RW == 2) w.template read_q<1>(st2);
         barrier_written();
     } else {
-        w.load_q(a, u0);
+        w.load_q(a, job0);
     }
-    w.begin(a, u0);
+    w.begin(a, job0, tile0);
 #pragma unroll
     for (int k = 0; k < W::FETCHES; ++k) f1.load(st1, k);
     const auto step = [&](uint8_t* st, uint8_t* ahead, float sc, float& sc_ahead) __attribute__((always_inline)) {
         wait_vmcnt<W::FETCHES>();                                // all but the next unit's loads
         barrier_lds();
         __builtin_amdgcn_sched_barrier(0);
-        const typename W::Fetch fetch(a, u2, ent2, real2);
+        const typename W::Fetch fetch(a, tile2, ent2, real2);
         const bool real3 = real2 && stream.step(a);
-        const LatentUnit u3 = stream.at;
-        ent2 = w.entry(a, u3);
+        ent2 = w.entry(a, stream);
         sc_ahead = *fetch.scale;
         __builtin_amdgcn_sched_barrier(0);
-        w.work(lds, u0, st, sc, c, fetch, ahead);
+        w.work(lds, tile0, st, sc, c, fetch, ahead);
         ++at;
-        if (!real1 || u1.tile == 0) {                            // the run's last unit
-            const bool whole = !kSplit || (w.from == 0 && u0.tile + 1 == u0.tiles);
+        if (!real1 || tile1 == 0) {                              // the run's last unit
+            const LatentJob u0 = LatentJob::get(lds.jobs + (turn & 3) * 2), u1 = LatentJob::get(lds.jobs + (turn + 1 & 3) * 2);
+            const bool whole = !kSplit || (w.from == 0 && tile0 + 1 == u0.tiles);
             const int slot = (int)blockIdx.x * 2 + (first ? 0 : 1);
             if (kSplit && w.from == 0 && threadIdx.x == 0)
                 latent_info(a, W::ROWS)[u0.r * row_tiles + u0.rt] =
-                    make_int2(slot, whole ? 0 : latent_owner(units, at - 1 - u0.tile + u0.tiles - 1) - (int)blockIdx.x);
+                    make_int2(slot, whole ? 0 : latent_owner(units, at - 1 - tile0 + u0.tiles - 1) - (int)blockIdx.x);
             w.join(lds);                                         // and all waves are done with st
             if (real1 && aligned) w.template stage_q<0>(a, u1, st);
             if (whole) w.store(a, u0.it, w.row(u0.rt));
@@ -671,11 +699,12 @@ __device__ __forceinline__ void latent_walk(const LatentArgs& a, LatentStream<32
             } else {
                 w.load_q(a, u1);
             }
-            w.begin(a, u1);
+            w.begin(a, u1, tile1);
+            ++turn;
         }
-        u0 = u1;
-        u1 = u2;
-        u2 = u3;
+        tile0 = tile1;
+        tile1 = tile2;
+        tile2 = stream.tile;
         real1 = real2;
         real2 = real3;
         return true;
@@ -739,7 +768,8 @@ __global__ __launch_bounds__(kLatThreads, 1) void attn_latent_item_kernel(Latent
         w.store(a, it, w.row(rt));
         return;
     }
-    stream.at = {r, rt, 0, tiles, it};
+    stream.job = {r, rt, tiles, it};
+    stream.tile = 0;
     stream.left = tiles - 1;
     latent_walk<RW, false>(a, stream, 0, 0, 0);
 }
