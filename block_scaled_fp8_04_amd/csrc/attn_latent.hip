@@ -255,7 +255,7 @@ struct LatentWalk {
     // and go from there into accumulation registers, where the matrix instructions take them from.
     // (Straight from memory a wave's lanes read 32 bytes of 32 rows at a time: 14000 cycles for 64 rows.)
     // Rows behind the item's last are copies of that one: nothing of them is stored.  Rows that are not
-    // 16-byte aligned, or far apart, go the slow way, by load_q.
+    // 16-byte aligned, or far apart, are read by elements.
     static constexpr int QROW = 1024 / RW;           // bytes of a staged row; the rotated dims come last
     // (chunk c of row r lies at c ^ (r & 15), or at rope_swz(r): sixteen rows' same chunk is spread)
     template <int X>
@@ -263,6 +263,20 @@ struct LatentWalk {
         constexpr int MINE = ROWS / 4, C = QROW / 16;            // rows of a wave; chunks of a row
         const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         const int first = u.rt * ROWS + wave * MINE, last = u.it.rows - 1;
+        if (!a.q_near) {                                         // by elements
+            constexpr int N = X == RW - 1 ? C + 8 : C;
+#pragma unroll 1
+            for (int i = lane; i < MINE * N; i += 64) {
+                const int r = i / N, c = i % N, at = wave * MINE + r;
+                int j;
+                const int64_t t = u.it.q0 + a.by_heads.of(min(first + r, last), j);
+                const uint16_t* const from = c < C ? a.q_latent + t * a.ql_ts + j * a.ql_hs + X * 256 + c * 8
+                                                   : a.q_rope + t * a.qr_ts + j * a.qr_hs + (c - C) * 8;
+                *(bf8v*)(c < C ? st + at * QROW + ((c ^ (at & 15)) << 4)
+                               : st + kLatCodes + at * 128 + ((c - C ^ rope_swz(at)) << 4)) = load_q8(from, false, false);
+            }
+            return;
+        }
         const int t0 = a.by_heads.of(min(first, last));
         const int64_t t = u.it.q0 + t0;
         // a lane's row steps by `by`; offsets from the first row's token have 32 bits (a.q_near)
@@ -315,17 +329,6 @@ struct LatentWalk {
         }
 #pragma unroll
         for (int s = X * 16; s < (X == RW - 1 ? 36 : X * 16 + 32 / RW); ++s) asm volatile("" : "+a"(q[s]));
-    }
-    __device__ __forceinline__ void load_q(const LatentArgs& a, const LatentJob& u) {
-        const int h = (threadIdx.x & 63) >> 5, r = row(u.rt);
-        int j;
-        const int64_t t = u.it.q0 + a.by_heads.of(min(r, u.it.rows - 1), j);
-        const uint16_t* const ql = a.q_latent + t * a.ql_ts + j * a.ql_hs + 16 * h;
-        const uint16_t* const qr = a.q_rope + t * a.qr_ts + j * a.qr_hs + 8 * h;
-#pragma unroll
-        for (int s = 0; s < 36; ++s) q[s] = load_q8(s < 32 ? ql + s / 2 * 32 + s % 2 * 8 : qr + (s - 32) * 16, false, false);
-#pragma unroll
-        for (int s = 0; s < 36; ++s) asm volatile("" : "+a"(q[s]));
     }
     __device__ __forceinline__ void begin(const LatentArgs& a, const LatentJob& u, int tile) {
 #pragma unroll
@@ -639,23 +642,16 @@ __device__ __forceinline__ void latent_walk(const LatentArgs& a, LatentStream<32
     bool real2 = real1 && stream.step(a);
     int tile2 = stream.tile;
     int ent2 = w.entry(a, stream);
-    const bool aligned = a.q_near;
-    if (aligned) {
-        w.template stage_q<0>(a, job0, st1);
-        if constexpr (RW == 2) w.template stage_q<1>(a, job0, st2);
-    }
+    w.template stage_q<0>(a, job0, st1);
+    if constexpr (RW == 2) w.template stage_q<1>(a, job0, st2);
     const typename W::Fetch f0(a, tile0, ent0, true), f1(a, tile1, ent1, real1);
     float sc0 = *f0.scale, sc1 = *f1.scale, sc2 = 0.f;
 #pragma unroll
     for (int k = 0; k < W::FETCHES; ++k) f0.load(st0, k);
-    if (aligned) {
-        barrier_all();
-        w.template read_q<0>(st1);
-        if constexpr (RW == 2) w.template read_q<1>(st2);
-        barrier_written();
-    } else {
-        w.load_q(a, job0);
-    }
+    barrier_all();
+    w.template read_q<0>(st1);
+    if constexpr (RW == 2) w.template read_q<1>(st2);
+    barrier_written();
     w.begin(a, job0, tile0);
 #pragma unroll
     for (int k = 0; k < W::FETCHES; ++k) f1.load(st1, k);
@@ -678,7 +674,7 @@ __device__ __forceinline__ void latent_walk(const LatentArgs& a, LatentStream<32
                 latent_info(a, W::ROWS)[u0.r * row_tiles + u0.rt] =
                     make_int2(slot, whole ? 0 : latent_owner(units, at - 1 - tile0 + u0.tiles - 1) - (int)blockIdx.x);
             w.join(lds);                                         // and all waves are done with st
-            if (real1 && aligned) w.template stage_q<0>(a, u1, st);
+            if (real1) w.template stage_q<0>(a, u1, st);
             if (whole) w.store(a, u0.it, w.row(u0.rt));
             else w.store_part(a, slot);
             if (!real1) {
@@ -686,18 +682,14 @@ __device__ __forceinline__ void latent_walk(const LatentArgs& a, LatentStream<32
                 return false;
             }
             first = false;
-            if (aligned) {
+            barrier_all();
+            w.template read_q<0>(st);
+            barrier_written();
+            if constexpr (RW == 2) {
+                w.template stage_q<1>(a, u1, st);
                 barrier_all();
-                w.template read_q<0>(st);
+                w.template read_q<1>(st);
                 barrier_written();
-                if constexpr (RW == 2) {
-                    w.template stage_q<1>(a, u1, st);
-                    barrier_all();
-                    w.template read_q<1>(st);
-                    barrier_written();
-                }
-            } else {
-                w.load_q(a, u1);
             }
             w.begin(a, u1, tile1);
             ++turn;
@@ -775,43 +767,65 @@ __global__ __launch_bounds__(kLatThreads, 1) void attn_latent_item_kernel(Latent
 }
 static_assert(kKvMaxRequests <= 64 * 64, "a request is found in two steps of 64");
 
-// Adds the parts of items that several workgroups shared, in token order, and gives the rows of a
-// request without tokens their zeros.  A workgroup takes 32 rows x 32 dims.
+// Adds the parts of items that several workgroups shared, and gives the rows of a request without
+// tokens their zeros.  A workgroup takes 32 rows x 32 dims; each of its waves takes every fourth part,
+// in token order, then the waves' sums are added in order.
 template <int RW>
 __global__ __launch_bounds__(kLatThreads) void attn_latent_join_kernel(LatentArgs a, int row_tiles) {
     constexpr int ROWS = 32 * RW;
-    const int lane = threadIdx.x & 63, i = threadIdx.x >> 6, d = blockIdx.y;
+    __shared__ v4f sums[4][4][64];
+    __shared__ float2 stats[4][32];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, d = blockIdx.y;
     const int rg = blockIdx.x % RW, item = blockIdx.x / RW;
     const int r = item / row_tiles, rt = item % row_tiles;
+    const int2 info = latent_info(a, ROWS)[item];                // of no meaning where there are no tokens
     const LatentItem it = LatentItem::of(a, a.q_offsets[r], a.q_offsets[r + 1], a.kv_lens[r]);
-    const int row = rt * ROWS + rg * 32 + (lane & 31);
     if (rt * ROWS + rg * 32 >= it.rows) return;
-    v4f o = {0.f, 0.f, 0.f, 0.f};
+    v4f o[4] = {};
     float m = neg_inf(), l = 0.f;
     if (it.kv_len > 0) {
-        const int2 info = latent_info(a, ROWS)[item];
         if (info.y == 0) return;                                 // finished by its workgroup
-        const v4f* const ws = (const v4f*)a.ws + (rg * 16 + d) * 256 + i * 64 + lane;
+        const v4f* const ws = (const v4f*)a.ws + (rg * 16 + d) * 256 + lane;
         const float2* const ml = latent_ml(a, ROWS) + rg * 32 + (lane & 31);
-#pragma unroll 4
-        for (int g = 0; g <= info.y; ++g) {
+#pragma unroll 2
+        for (int g = wave; g <= info.y; g += 4) {
             const int64_t slot = g == 0 ? info.x : (info.x / 2 + g) * 2;
             const float2 part = ml[slot * ROWS];
-            const v4f x = ws[slot * (RW * 16 * 256)];
+            v4f x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = ws[slot * (RW * 16 * 256) + i * 64];
             const float top = fmaxf(m, part.x);
             const float old = m == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(m - top);
             const float add = part.x == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(part.x - top);
-            o = o * old + x * add;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = o[i] * old + x[i] * add;
             l = l * old + part.y * add;
             m = top;
         }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sums[wave][i][lane] = o[i];
+    if (lane < 32) stats[wave][lane] = make_float2(m, l);
+    __syncthreads();
+    const int i = wave, row = rt * ROWS + rg * 32 + (lane & 31);
     if (row >= it.rows) return;
+    float2 part[4];
+#pragma unroll
+    for (int z = 0; z < 4; ++z) part[z] = stats[z][lane & 31];
+    m = fmaxf(fmaxf(part[0].x, part[1].x), fmaxf(part[2].x, part[3].x));
+    v4f sum = {0.f, 0.f, 0.f, 0.f};
+    l = 0.f;
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+        const float f = part[z].x == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(part[z].x - m);
+        sum += sums[z][i][lane] * f;
+        l += part[z].y * f;
+    }
     int j;
     const int64_t t = it.q0 + a.by_heads.of(row, j);
     const float f = l == 0.f ? 0.f : 1.f / l;
     *(uint2*)(a.out + t * a.o_ts + (int64_t)j * a.o_hs + 32 * d + 8 * i + 4 * (lane >> 5)) =
-        make_uint2(pack_bf16x2(o[0] * f, o[1] * f), pack_bf16x2(o[2] * f, o[3] * f));
+        make_uint2(pack_bf16x2(sum[0] * f, sum[1] * f), pack_bf16x2(sum[2] * f, sum[3] * f));
     if (a.lse && d == 0 && i == 0 && lane < 32)
         a.lse[t * a.heads + j] = l == 0.f ? neg_inf() : (m + __builtin_log2f(l)) * kLn2;
 }
