@@ -39,7 +39,8 @@ typedef int v2i __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) v2i* lds_v2i;
 
 constexpr int kLatThreads = 256;
-constexpr int kLatGroups = 256;               // workgroups of a split launch: one a CU (LDS, registers)
+constexpr int kLatGroups = 256;               // most workgroups of a split launch: one a CU (LDS, registers)
+constexpr int kLatItemCost = 2;               // what an item's queries and results cost, in tiles
 constexpr int kLatItems = 512;                // most items of a split launch: beyond, they fill the chip
 constexpr int kLatTile = 64;                  // tokens of a tile
 constexpr int kLatCodes = kLatTile * kLatent; // its bytes of codes and of rotated keys
@@ -110,11 +111,12 @@ __device__ __forceinline__ int latent_tiles(int tokens) {
     return (int)(((uint32_t)tokens + kLatTile - 1) / kLatTile);
 }
 
-// 64 consecutive requests, one per lane, and the units of work (tiles of their items) before each.
+// 64 consecutive requests, one per lane, and the cost of their work before each: for each item its tiles
+// and kLatItemCost.
 template <int ROWS>
 struct LatentRequests {
     int base, q0, q1, kv_len;
-    int64_t before, units;                           // before the lane's request; of it
+    int64_t before, cost;                            // before the lane's request; of it
     __device__ __forceinline__ void load(const LatentArgs& a, int from) {
         base = from;
         const int mine = base + (int)(threadIdx.x & 63), r = min(mine, a.R - 1);
@@ -122,18 +124,19 @@ struct LatentRequests {
         q1 = a.q_offsets[r + 1];
         kv_len = a.kv_lens[r];
         const LatentItem it = LatentItem::of(a, q0, q1, kv_len);
-        units = mine < a.R ? (int64_t)((it.rows + ROWS - 1) / ROWS) * latent_tiles(it.kv_len) : 0;
+        cost = mine < a.R && it.kv_len > 0
+                   ? (int64_t)((it.rows + ROWS - 1) / ROWS) * (latent_tiles(it.kv_len) + kLatItemCost) : 0;
     }
-    // sums up the units, of which `start` come before the 64 requests; returns what comes before the next
+    // sums up the costs, with `start` before the 64 requests; returns what comes before the next
     __device__ __forceinline__ int64_t scan(int64_t start) {
         const int lane = threadIdx.x & 63;
-        int64_t sum = units;
+        int64_t sum = cost;
 #pragma unroll
         for (int step = 1; step < 64; step <<= 1) {
             const int64_t x = __shfl_up((long long)sum, step);
             if (lane >= step) sum += x;
         }
-        before = start + sum - units;
+        before = start + sum - cost;
         return start + from_lane(sum, 63);
     }
     static __device__ __forceinline__ int64_t from_lane(int64_t x, int lane) {
@@ -171,18 +174,23 @@ struct LatentStream {
     LatentRequests<ROWS> reqs;
     LatentJob job;
     int tile;
-    int64_t left;                                    // units behind this one
+    int64_t at, left;                                // cost before this unit; behind it
     int4* jobs;                                      // this wave's
     int turn;                                        // number of the item
 
-    // From unit `local` of request r (one of reqs) on.
-    __device__ __forceinline__ void begin(const LatentArgs& a, int r, int64_t local, int64_t count) {
+    // From cost `from` to `to`, beginning in request r (one of reqs); false: no unit begins there.
+    __device__ __forceinline__ bool begin(const LatentArgs& a, int r, int64_t from, int64_t to) {
         job.r = r;
         job.it = reqs.item(a, r);
         job.tiles = latent_tiles(job.it.kv_len);
-        job.rt = __builtin_amdgcn_readfirstlane((int)quotient(local, job.tiles));
-        tile = (int)(local - (int64_t)job.rt * job.tiles);
-        left = count - 1;
+        const int64_t local = from - reqs.from_lane(reqs.before, r - reqs.base);
+        const int per = job.tiles + kLatItemCost;
+        job.rt = __builtin_amdgcn_readfirstlane((int)quotient(local, per));
+        const int x = (int)(local - (int64_t)job.rt * per);
+        tile = max(x - kLatItemCost, 0);
+        at = from + tile + kLatItemCost - x;
+        left = to - at - 1;
+        return left >= 0;
     }
     __device__ __forceinline__ void keep(int4* to) {
         jobs = to;
@@ -191,18 +199,19 @@ struct LatentStream {
     }
     // To the next unit; none: stays.
     __device__ __forceinline__ bool step(const LatentArgs& a) {
-        if (left <= 0) return false;
-        --left;
+        const int pay = tile + 1 < job.tiles ? 1 : kLatItemCost + 1;
+        if (left < pay) return false;
+        left -= pay;
         if (++tile < job.tiles) return true;
         tile = 0;
         if (++job.rt * ROWS >= job.it.rows) {
             job.rt = 0;
-            uint64_t later = __ballot(reqs.units > 0) & ~((2ull << (job.r - reqs.base)) - 1);
+            uint64_t later = __ballot(reqs.cost > 0) & ~((2ull << (job.r - reqs.base)) - 1);
             while (later == 0 && reqs.base + 64 < a.R) {
                 reqs.load(a, reqs.base + 64);
-                later = __ballot(reqs.units > 0);
+                later = __ballot(reqs.cost > 0);
             }
-            if (later == 0) return false;                        // (not with units left)
+            if (later == 0) return false;                        // (not with cost left)
             job.r = reqs.base + __ffsll((unsigned long long)later) - 1;
             job.it = reqs.item(a, job.r);
             job.tiles = latent_tiles(job.it.kv_len);
@@ -601,20 +610,21 @@ struct LatentWalk {
     }
 };
 
-// A split launch's units in even shares: the first unit of workgroup w, and the workgroup that has
-// unit u.  None between an item's first and last workgroup goes without.
-__device__ __forceinline__ int64_t latent_first(int64_t units, int w) {
-    return units < kLatGroups ? min((int64_t)w, units) : units * w / kLatGroups;
+// A split launch's cost is shared evenly by this many workgroups (no share is empty).
+__device__ __forceinline__ int latent_groups(int64_t cost, int rw) {
+    return (int)min(cost, (int64_t)kLatGroups);
 }
-__device__ __forceinline__ int latent_owner(int64_t units, int64_t u) {
-    return (int)(units < kLatGroups ? u : quotient((u + 1) * kLatGroups - 1, units));
+// Where workgroup w's share begins, and the workgroup whose share holds position `at`.
+__device__ __forceinline__ int64_t latent_first(int64_t cost, int groups, int w) { return quotient(cost * w, groups); }
+__device__ __forceinline__ int latent_owner(int64_t cost, int groups, int64_t at) {
+    return (int)quotient((at + 1) * groups - 1, cost);
 }
 
 // A workgroup's units, of items whose rows it stores, or whose parts.  While one is worked on the next
 // is on its way to LDS, and the one after that is asked for: also over the items' ends, where a walk
 // that began anew for each item spent 5 us a time on loads that followed one another.
 template <int RW, bool kSplit>
-__device__ __forceinline__ void latent_walk(const LatentArgs& a, LatentStream<32 * RW>& stream, int64_t units, int64_t at,
+__device__ __forceinline__ void latent_walk(const LatentArgs& a, LatentStream<32 * RW>& stream, int64_t cost, int groups,
                                             int row_tiles) {
     using W = LatentWalk<RW>;
     __shared__ __attribute__((aligned(1024))) uint8_t st0[kLatStage];
@@ -631,6 +641,7 @@ __device__ __forceinline__ void latent_walk(const LatentArgs& a, LatentStream<32
     w.init();
     bool first = true;
     int turn = 0;                                                // the item that is worked on
+    int64_t at = stream.at;
     // unit 0 is worked on, 1 on its way, 2 asked for
     stream.keep(lds.jobs);
     const LatentJob job0 = stream.job;
@@ -672,7 +683,7 @@ __device__ __forceinline__ void latent_walk(const LatentArgs& a, LatentStream<32
             const int slot = (int)blockIdx.x * 2 + (first ? 0 : 1);
             if (kSplit && w.from == 0 && threadIdx.x == 0)
                 latent_info(a, W::ROWS)[u0.r * row_tiles + u0.rt] =
-                    make_int2(slot, whole ? 0 : latent_owner(units, at - 1 - tile0 + u0.tiles - 1) - (int)blockIdx.x);
+                    make_int2(slot, whole ? 0 : latent_owner(cost, groups, at - 1 + u0.tiles - 1 - tile0) - (int)blockIdx.x);
             w.join(lds);                                         // and all waves are done with st
             if (real1) w.template stage_q<0>(a, u1, st);
             if (whole) w.store(a, u0.it, w.row(u0.rt));
@@ -693,6 +704,7 @@ __device__ __forceinline__ void latent_walk(const LatentArgs& a, LatentStream<32
             }
             w.begin(a, u1, tile1);
             ++turn;
+            at += kLatItemCost;
         }
         tile0 = tile1;
         tile1 = tile2;
@@ -713,23 +725,24 @@ __global__ __launch_bounds__(kLatThreads, 1) void attn_latent_split_kernel(Laten
     const int lane = threadIdx.x & 63;
     LatentStream<32 * RW> stream;
     auto& reqs = stream.reqs;
-    int64_t units = 0;
+    int64_t cost = 0;
     for (int from = 0; from < a.R; from += 64) {
         reqs.load(a, from);
-        units = reqs.scan(units);
+        cost = reqs.scan(cost);
     }
-    const int64_t u = latent_first(units, blockIdx.x), end = latent_first(units, blockIdx.x + 1);
-    if (u >= end) return;
-    if (a.R > 64) {                                              // back to the first unit's requests
+    const int groups = latent_groups(cost, RW);
+    if ((int)blockIdx.x >= groups || cost == 0) return;
+    const int64_t from = latent_first(cost, groups, blockIdx.x), to = latent_first(cost, groups, blockIdx.x + 1);
+    if (a.R > 64) {                                              // back to the requests where it begins
         int64_t next = 0;
-        for (int from = 0; from < a.R && next <= u; from += 64) {
-            reqs.load(a, from);
+        for (int x = 0; x < a.R && next <= from; x += 64) {
+            reqs.load(a, x);
             next = reqs.scan(next);
         }
     }
-    const int in = last_of(reqs.base + lane < a.R && reqs.before <= u);
-    stream.begin(a, __builtin_amdgcn_readfirstlane(reqs.base + in), u - reqs.from_lane(reqs.before, in), end - u);
-    latent_walk<RW, true>(a, stream, units, u, row_tiles);
+    const int in = last_of(reqs.base + lane < a.R && reqs.before <= from);
+    if (stream.begin(a, __builtin_amdgcn_readfirstlane(reqs.base + in), from, to))
+        latent_walk<RW, true>(a, stream, cost, groups, row_tiles);
 }
 
 // One workgroup per item: enough of them to fill the chip, or no workspace.  Request r's items are
@@ -762,6 +775,7 @@ __global__ __launch_bounds__(kLatThreads, 1) void attn_latent_item_kernel(Latent
     }
     stream.job = {r, rt, tiles, it};
     stream.tile = 0;
+    stream.at = 0;
     stream.left = tiles - 1;
     latent_walk<RW, false>(a, stream, 0, 0, 0);
 }
