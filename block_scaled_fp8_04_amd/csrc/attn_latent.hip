@@ -40,7 +40,7 @@ typedef __attribute__((address_space(3))) v2i* lds_v2i;
 
 constexpr int kLatThreads = 256;
 constexpr int kLatGroups = 256;               // most workgroups of a split launch: one a CU (LDS, registers)
-constexpr int kLatItemCost = 2;               // what an item's queries and results cost, in tiles
+constexpr int kLatItemCost = 3;               // what an item's queries and results cost, in tiles
 constexpr int kLatItems = 512;                // most items of a split launch: beyond, they fill the chip
 constexpr int kLatTile = 64;                  // tokens of a tile
 constexpr int kLatCodes = kLatTile * kLatent; // its bytes of codes and of rotated keys
@@ -153,81 +153,57 @@ struct LatentRequests {
 struct LatentJob {
     int r, rt, tiles;
     LatentItem it;
-    __device__ __forceinline__ void put(int4* to) const {
-        if ((threadIdx.x & 63) == 0) {
-            to[0] = make_int4(r, rt, tiles, it.q0);
-            to[1] = make_int4(it.n, it.rows, it.kv_len, 0);
-        }
-    }
-    static __device__ __forceinline__ LatentJob get(const int4* from) {
-        const int4 x = from[0], y = from[1];
-        const auto u = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
-        return {u(x.x), u(x.y), u(x.z), {u(x.w), u(y.x), u(y.y), u(y.z)}};
-    }
 };
 
-// A workgroup's units of work, tiles of its items, one after the other.  It is up to three units ahead of
-// the work: loads are asked for by it.  Its items are left in LDS, four at a time, for the work to find
-// them: held in scalar registers for each unit, they would be most of what these spill.
+// A workgroup's share of the work: runs of tiles, each of one item.
 template <int ROWS>
-struct LatentStream {
+struct LatentShare {
     LatentRequests<ROWS> reqs;
     LatentJob job;
-    int tile;
-    int64_t at, left;                                // cost before this unit; behind it
-    int4* jobs;                                      // this wave's
-    int turn;                                        // number of the item
+    int tile;                                        // the run's first
+    int64_t at, to;                                  // cost before it; at the share's end
 
-    // From cost `from` to `to`, beginning in request r (one of reqs); false: no unit begins there.
-    __device__ __forceinline__ bool begin(const LatentArgs& a, int r, int64_t from, int64_t to) {
-        job.r = r;
-        job.it = reqs.item(a, r);
-        job.tiles = latent_tiles(job.it.kv_len);
+    // From cost `from` on, in request r (one of reqs); false: no tile begins there.
+    __device__ __forceinline__ bool begin(const LatentArgs& a, int r, int64_t from, int64_t end) {
+        take(a, r);
         const int64_t local = from - reqs.from_lane(reqs.before, r - reqs.base);
         const int per = job.tiles + kLatItemCost;
         job.rt = __builtin_amdgcn_readfirstlane((int)quotient(local, per));
         const int x = (int)(local - (int64_t)job.rt * per);
         tile = max(x - kLatItemCost, 0);
         at = from + tile + kLatItemCost - x;
-        left = to - at - 1;
-        return left >= 0;
+        to = end;
+        return at < to;
     }
-    __device__ __forceinline__ void keep(int4* to) {
-        jobs = to;
-        turn = 0;
-        job.put(jobs);
+    __device__ __forceinline__ void take(const LatentArgs& a, int r) {
+        job.r = r;
+        job.rt = 0;
+        job.it = reqs.item(a, r);
+        job.tiles = latent_tiles(job.it.kv_len);
     }
-    // To the next unit; none: stays.
-    __device__ __forceinline__ bool step(const LatentArgs& a) {
-        const int pay = tile + 1 < job.tiles ? 1 : kLatItemCost + 1;
-        if (left < pay) return false;
-        left -= pay;
-        if (++tile < job.tiles) return true;
+    // the tile behind the run's last
+    __device__ __forceinline__ int end() const { return (int)min((int64_t)job.tiles, tile + (to - at)); }
+    // To the next run; false: there is none.
+    __device__ __forceinline__ bool next(const LatentArgs& a) {
+        at += job.tiles - tile + kLatItemCost;
         tile = 0;
-        if (++job.rt * ROWS >= job.it.rows) {
-            job.rt = 0;
-            uint64_t later = __ballot(reqs.cost > 0) & ~((2ull << (job.r - reqs.base)) - 1);
-            while (later == 0 && reqs.base + 64 < a.R) {
-                reqs.load(a, reqs.base + 64);
-                later = __ballot(reqs.cost > 0);
-            }
-            if (later == 0) return false;                        // (not with cost left)
-            job.r = reqs.base + __ffsll((unsigned long long)later) - 1;
-            job.it = reqs.item(a, job.r);
-            job.tiles = latent_tiles(job.it.kv_len);
+        if (at >= to) return false;
+        if (++job.rt * ROWS < job.it.rows) return true;
+        uint64_t later = __ballot(reqs.cost > 0) & ~((2ull << (job.r - reqs.base)) - 1);
+        while (later == 0 && reqs.base + 64 < a.R) {
+            reqs.load(a, reqs.base + 64);
+            later = __ballot(reqs.cost > 0);
         }
-        ++turn;
-        job.put(jobs + (turn & 3) * 2);
+        if (later == 0) return false;                            // (not with cost left)
+        take(a, reqs.base + __ffsll((unsigned long long)later) - 1);
         return true;
     }
 };
 
 struct LatentLds {
-    uint8_t *st0, *st1, *st2;                        // stages, a tile each
     float2* scales;                                  // this wave's [64 tokens] exponents and inverses
     uint4* trade;                                    // [row half][token half][2][64 lanes] weights
     float* refs;                                     // [row half][token half][2][64 lanes] references, norms
-    int4* jobs;                                      // this wave's four items
 };
 
 // One workgroup's way through its units.  Its four waves form weights two by two, each for 32 rows and half tg of a tile's tokens, trade them through LDS, and each sums its rows' values
@@ -353,13 +329,13 @@ struct LatentWalk {
         kv_len = u.it.kv_len;
     }
 
-    // The table entry of the page that holds token `lane` of a unit (of the last page, behind the end).
-    static __device__ __forceinline__ int entry(const LatentArgs& a, const LatentStream<ROWS>& s) {
-        const uint32_t pos = min((uint32_t)s.tile * kLatTile + (threadIdx.x & 63), (uint32_t)s.job.it.kv_len - 1);
-        return (a.block_table + s.job.r * a.width)[pos >> a.log_b];
+    // The table entry of the page that holds token `lane` of a tile (of the last page, behind the end).
+    static __device__ __forceinline__ int entry(const LatentArgs& a, const LatentJob& u, int tile) {
+        const uint32_t pos = min((uint32_t)tile * kLatTile + (threadIdx.x & 63), (uint32_t)u.it.kv_len - 1);
+        return (a.block_table + u.r * a.width)[pos >> a.log_b];
     }
 
-    // A unit's way to LDS: each wave brings 16 of its tokens, by ten loads that bypass the registers.
+    // A tile's way to LDS: each wave brings 16 of its tokens, by ten loads that bypass the registers.
     // not real: the loads lie outside their resource and read nothing.
     struct Fetch {
         __amdgpu_buffer_rsrc_t codes, rope;
@@ -511,7 +487,7 @@ struct LatentWalk {
         barrier_written();
     }
 
-    // One unit, whose tile has landed in st.
+    // One tile, which has landed in st.
     __device__ __forceinline__ void work(const LatentLds& lds, int tile, uint8_t* st, float sc, float c,
                                          const Fetch& fetch, uint8_t* to) {
         const int base = tile * kLatTile;
@@ -620,11 +596,12 @@ __device__ __forceinline__ int latent_owner(int64_t cost, int groups, int64_t at
     return (int)quotient((at + 1) * groups - 1, cost);
 }
 
-// A workgroup's units, of items whose rows it stores, or whose parts.  While one is worked on the next
-// is on its way to LDS, and the one after that is asked for: also over the items' ends, where a walk
-// that began anew for each item spent 5 us a time on loads that followed one another.
+// A workgroup's runs, of items whose rows it stores, or whose parts.  While a tile is worked on the
+// next is on its way to LDS, and the one after that is asked for.  A run begins with all of its first
+// loads at once: its queries, its first tile, whose page the run before asked for; the results of the
+// run before are stored while they come.
 template <int RW, bool kSplit>
-__device__ __forceinline__ void latent_walk(const LatentArgs& a, LatentStream<32 * RW>& stream, int64_t cost, int groups,
+__device__ __forceinline__ void latent_walk(const LatentArgs& a, LatentShare<32 * RW>& share, int64_t cost, int groups,
                                             int row_tiles) {
     using W = LatentWalk<RW>;
     __shared__ __attribute__((aligned(1024))) uint8_t st0[kLatStage];
@@ -633,98 +610,75 @@ __device__ __forceinline__ void latent_walk(const LatentArgs& a, LatentStream<32
     __shared__ __attribute__((aligned(16))) float2 scales[4][kLatTile];
     __shared__ uint4 trade[RW * 256];
     __shared__ float refs[RW * 256];
-    __shared__ int4 jobs[4][8];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const LatentLds lds = {st0, st1, st2, scales[wave], trade, refs, jobs[wave]};
+    const LatentLds lds = {scales[wave], trade, refs};
     const float c = a.scale * kLog2e;
     W w;
     w.init();
-    bool first = true;
-    int turn = 0;                                                // the item that is worked on
-    int64_t at = stream.at;
-    // unit 0 is worked on, 1 on its way, 2 asked for
-    stream.keep(lds.jobs);
-    const LatentJob job0 = stream.job;
-    int tile0 = stream.tile;
-    const int ent0 = w.entry(a, stream);
-    bool real1 = stream.step(a);
-    int tile1 = stream.tile;
-    const int ent1 = w.entry(a, stream);
-    bool real2 = real1 && stream.step(a);
-    int tile2 = stream.tile;
-    int ent2 = w.entry(a, stream);
-    w.template stage_q<0>(a, job0, st1);
-    if constexpr (RW == 2) w.template stage_q<1>(a, job0, st2);
-    const typename W::Fetch f0(a, tile0, ent0, true), f1(a, tile1, ent1, real1);
-    float sc0 = *f0.scale, sc1 = *f1.scale, sc2 = 0.f;
+    LatentJob job = share.job, done;
+    int tile = share.tile, end = share.end(), slot = -1;
+    bool whole = false;
+    int ent0 = w.entry(a, job, tile), ent1 = w.entry(a, job, tile + 1);
+    for (;;) {
+        w.template stage_q<0>(a, job, st1);
+        if constexpr (RW == 2) w.template stage_q<1>(a, job, st2);
+        const typename W::Fetch f0(a, tile, ent0, true), f1(a, tile + 1, ent1, tile + 1 < end);
+        float sc0 = *f0.scale, sc1 = *f1.scale, sc2 = 0.f;
 #pragma unroll
-    for (int k = 0; k < W::FETCHES; ++k) f0.load(st0, k);
-    barrier_all();
-    w.template read_q<0>(st1);
-    if constexpr (RW == 2) w.template read_q<1>(st2);
-    barrier_written();
-    w.begin(a, job0, tile0);
-#pragma unroll
-    for (int k = 0; k < W::FETCHES; ++k) f1.load(st1, k);
-    const auto step = [&](uint8_t* st, uint8_t* ahead, float sc, float& sc_ahead) __attribute__((always_inline)) {
-        wait_vmcnt<W::FETCHES>();                                // all but the next unit's loads
-        barrier_lds();
-        __builtin_amdgcn_sched_barrier(0);
-        const typename W::Fetch fetch(a, tile2, ent2, real2);
-        const bool real3 = real2 && stream.step(a);
-        ent2 = w.entry(a, stream);
-        sc_ahead = *fetch.scale;
-        __builtin_amdgcn_sched_barrier(0);
-        w.work(lds, tile0, st, sc, c, fetch, ahead);
-        ++at;
-        if (!real1 || tile1 == 0) {                              // the run's last unit
-            const LatentJob u0 = LatentJob::get(lds.jobs + (turn & 3) * 2), u1 = LatentJob::get(lds.jobs + (turn + 1 & 3) * 2);
-            const bool whole = !kSplit || (w.from == 0 && tile0 + 1 == u0.tiles);
-            const int slot = (int)blockIdx.x * 2 + (first ? 0 : 1);
-            if (kSplit && w.from == 0 && threadIdx.x == 0)
-                latent_info(a, W::ROWS)[u0.r * row_tiles + u0.rt] =
-                    make_int2(slot, whole ? 0 : latent_owner(cost, groups, at - 1 + u0.tiles - 1 - tile0) - (int)blockIdx.x);
-            w.join(lds);                                         // and all waves are done with st
-            if (real1) w.template stage_q<0>(a, u1, st);
-            if (whole) w.store(a, u0.it, w.row(u0.rt));
+        for (int k = 0; k < W::FETCHES; ++k) f0.load(st0, k);
+        int ent2 = w.entry(a, job, tile + 2);
+        if (slot >= 0) {                                         // the run before
+            if (whole) w.store(a, done.it, w.row(done.rt));
             else w.store_part(a, slot);
-            if (!real1) {
-                wait_vmcnt<0>();                                 // no load outlives its LDS
-                return false;
-            }
-            first = false;
-            barrier_all();
-            w.template read_q<0>(st);
-            barrier_written();
-            if constexpr (RW == 2) {
-                w.template stage_q<1>(a, u1, st);
-                barrier_all();
-                w.template read_q<1>(st);
-                barrier_written();
-            }
-            w.begin(a, u1, tile1);
-            ++turn;
-            at += kLatItemCost;
         }
-        tile0 = tile1;
-        tile1 = tile2;
-        tile2 = stream.tile;
-        real1 = real2;
-        real2 = real3;
-        return true;
-    };
-    while (step(st0, st2, sc0, sc2) && step(st1, st0, sc1, sc0) && step(st2, st1, sc2, sc1)) {
+        barrier_all();
+        w.template read_q<0>(st1);
+        if constexpr (RW == 2) w.template read_q<1>(st2);
+        barrier_written();
+#pragma unroll
+        for (int k = 0; k < W::FETCHES; ++k) f1.load(st1, k);
+        w.begin(a, job, tile);
+        whole = !kSplit || (tile == 0 && end == job.tiles);
+        slot = (int)blockIdx.x * 2 + (slot < 0 ? 0 : 1);
+        if (kSplit && tile == 0 && threadIdx.x == 0)
+            latent_info(a, W::ROWS)[job.r * row_tiles + job.rt] =
+                make_int2(slot, whole ? 0 : latent_owner(cost, groups, share.at + job.tiles - 1) - (int)blockIdx.x);
+        const bool more = kSplit && share.next(a);
+        ent0 = w.entry(a, share.job, 0);
+        ent1 = w.entry(a, share.job, 1);
+        const auto step = [&](uint8_t* st, uint8_t* ahead, float sc, float& sc_ahead) __attribute__((always_inline)) {
+            wait_vmcnt<W::FETCHES>();                            // all but the next tile's loads
+            barrier_lds();
+            __builtin_amdgcn_sched_barrier(0);
+            const typename W::Fetch fetch(a, tile + 2, ent2, tile + 2 < end);
+            ent2 = w.entry(a, job, tile + 3);
+            sc_ahead = *fetch.scale;
+            __builtin_amdgcn_sched_barrier(0);
+            w.work(lds, tile, st, sc, c, fetch, ahead);
+            return ++tile < end;
+        };
+        while (step(st0, st2, sc0, sc2) && step(st1, st0, sc1, sc0) && step(st2, st1, sc2, sc1)) {
+        }
+        wait_vmcnt<0>();                                         // no load outlives its use of LDS
+        w.join(lds);                                             // and all waves are done with their stages
+        done = job;
+        if (!more) break;
+        job = share.job;
+        tile = 0;
+        end = share.end();
     }
+    if (whole) w.store(a, done.it, w.row(done.rt));
+    else w.store_part(a, slot);
 }
 
-// Every workgroup takes an even share of the units of all items, in their order.  Where it begins an
+// Every workgroup takes an even share of the cost of all items, in their order.  Where it begins an
 // item it notes for the join where the item's parts are: its own slot (of the two that a workgroup has:
 // its first run's and its last one's) and how many workgroups follow.
 template <int RW>
 __global__ __launch_bounds__(kLatThreads, 1) void attn_latent_split_kernel(LatentArgs a, int row_tiles) {
     const int lane = threadIdx.x & 63;
-    LatentStream<32 * RW> stream;
-    auto& reqs = stream.reqs;
+    LatentShare<32 * RW> share;
+    auto& reqs = share.reqs;
     int64_t cost = 0;
     for (int from = 0; from < a.R; from += 64) {
         reqs.load(a, from);
@@ -741,8 +695,8 @@ __global__ __launch_bounds__(kLatThreads, 1) void attn_latent_split_kernel(Laten
         }
     }
     const int in = last_of(reqs.base + lane < a.R && reqs.before <= from);
-    if (stream.begin(a, __builtin_amdgcn_readfirstlane(reqs.base + in), from, to))
-        latent_walk<RW, true>(a, stream, cost, groups, row_tiles);
+    if (share.begin(a, __builtin_amdgcn_readfirstlane(reqs.base + in), from, to))
+        latent_walk<RW, true>(a, share, cost, groups, row_tiles);
 }
 
 // One workgroup per item: enough of them to fill the chip, or no workspace.  Request r's items are
@@ -757,10 +711,10 @@ __global__ __launch_bounds__(kLatThreads, 1) void attn_latent_item_kernel(Latent
     };
     const int each64 = a.q_offsets[min(lane * 64, a.R)];
     const int from = last_of(lane * 64 < a.R && start(each64, lane * 64) <= b) * 64;
-    LatentStream<W::ROWS> stream;
-    stream.reqs.load(a, from);
-    const int r = __builtin_amdgcn_readfirstlane(from + last_of(from + lane < a.R && start(stream.reqs.q0, from + lane) <= b));
-    const LatentItem it = stream.reqs.item(a, r);
+    LatentShare<W::ROWS> share;
+    share.reqs.load(a, from);
+    const int r = __builtin_amdgcn_readfirstlane(from + last_of(from + lane < a.R && start(share.reqs.q0, from + lane) <= b));
+    const LatentItem it = share.reqs.item(a, r);
     const int64_t at = b - start((int)it.q0, r);
     if (at < 0 || at * W::ROWS >= it.rows) return;
     const int rt = __builtin_amdgcn_readfirstlane((int)at);
@@ -773,11 +727,11 @@ __global__ __launch_bounds__(kLatThreads, 1) void attn_latent_item_kernel(Latent
         w.store(a, it, w.row(rt));
         return;
     }
-    stream.job = {r, rt, tiles, it};
-    stream.tile = 0;
-    stream.at = 0;
-    stream.left = tiles - 1;
-    latent_walk<RW, false>(a, stream, 0, 0, 0);
+    share.job = {r, rt, tiles, it};
+    share.tile = 0;
+    share.at = 0;
+    share.to = tiles;
+    latent_walk<RW, false>(a, share, 0, 0, 0);
 }
 static_assert(kKvMaxRequests <= 64 * 64, "a request is found in two steps of 64");
 
