@@ -572,8 +572,9 @@ struct LatentWalk {
     }
 
     // Partial results of a slot: [RW][16 dims blocks][4][64 lanes] of four floats, then (m, l) a row.
-    __device__ __forceinline__ void store_part(const LatentArgs& a, int64_t slot) const {
+    __device__ __forceinline__ void store_part(const LatentArgs& a, const LatentJob& u, int64_t slot) const {
         const int lane = threadIdx.x & 63;
+        if (row(u.rt) >= u.it.rows) return;
         v4f* const ws = (v4f*)a.ws + ((slot * RW + rg) * 16 + dw * DT) * 256 + lane;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
@@ -629,7 +630,7 @@ __device__ __forceinline__ void latent_walk(const LatentArgs& a, LatentShare<32 
         int ent2 = w.entry(a, job, tile + 2);
         if (slot >= 0) {                                         // the run before
             if (whole) w.store(a, done.it, w.row(done.rt));
-            else w.store_part(a, slot);
+            else w.store_part(a, done, slot);
         }
         barrier_all();
         w.template read_q<0>(st1);
@@ -668,7 +669,7 @@ __device__ __forceinline__ void latent_walk(const LatentArgs& a, LatentShare<32 
         end = share.end();
     }
     if (whole) w.store(a, done.it, w.row(done.rt));
-    else w.store_part(a, slot);
+    else w.store_part(a, done, slot);
 }
 
 // Every workgroup takes an even share of the cost of all items, in their order.  Where it begins an
@@ -751,8 +752,8 @@ __global__ __launch_bounds__(kLatThreads) void attn_latent_join_kernel(LatentArg
     if (rt * ROWS + rg * 32 >= it.rows) return;
     v4f o[4] = {};
     float m = neg_inf(), l = 0.f;
-    if (it.kv_len > 0) {
-        if (info.y == 0) return;                                 // finished by its workgroup
+    if (it.kv_len > 0 && info.y == 0) return;                    // finished by its workgroup
+    if (it.kv_len > 0 && rt * ROWS + rg * 32 + (lane & 31) < it.rows) {
         const v4f* const ws = (const v4f*)a.ws + (rg * 16 + d) * 256 + lane;
         const float2* const ml = latent_ml(a, ROWS) + rg * 32 + (lane & 31);
 #pragma unroll 2
