@@ -163,6 +163,10 @@ def _stream(stream, device):
     return ctypes.c_void_p(int(stream))
 
 
+def _handle(stream, gpu):
+    return torch._C._cuda_getCurrentRawStream(gpu) if stream is None else _stream(stream, None)
+
+
 def _allocating_on(stream, device):
     """Context in which an allocating call makes its arrays: on the stream that its kernels take.
     Fills then stay in order with them, and what the call drops or the caller frees is handed out
@@ -506,8 +510,7 @@ def kv_plan_buffers(R, T, device) -> KVPlan:
     return KVPlan(*(torch.empty(n, dtype=torch.int32, device=device) for n in sizes))
 
 
-def _need_i32(device, *named):
-    gpu = device.index
+def _need_i32(gpu, *named):
     for name, t, shape in named:
         if t.dtype is not torch.int32 or t.get_device() != gpu or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous int32 tensor on the call's GPU")
@@ -527,13 +530,13 @@ def bfp8_kv_plan(ctx_lens, new_lens, free_pages, block_table, page_size, plan, f
     _need(block_table.dim() == 2 and free_pages.dim() == 1, "block_table [R, W], free_pages [F]")
     R, W = block_table.shape
     T = plan.slot_map.shape[0]
-    _need_i32(dev, ("ctx_lens", ctx_lens, (R,)), ("new_lens", new_lens, (R,)),
+    _need_i32(dev.index, ("ctx_lens", ctx_lens, (R,)), ("new_lens", new_lens, (R,)),
               ("free_pages", free_pages, None), ("block_table", block_table, None),
               ("q_offsets", plan.q_offsets, (R + 1,)), ("kv_lens", plan.kv_lens, (R,)),
               ("tile_offsets", plan.tile_offsets, (R + 1,)), ("slot_map", plan.slot_map, (T,)),
               ("positions", plan.positions, (T,)), ("counts", plan.counts, (4,)))
     if free_head is not None:
-        _need_i32(dev, ("free_head", free_head, (1,)))
+        _need_i32(dev.index, ("free_head", free_head, (1,)))
     _check("bfp8_kv_plan", library().bfp8_kv_plan(
         ctx_lens.data_ptr(), new_lens.data_ptr(), R, free_pages.data_ptr(), free_pages.shape[0],
         free_head.data_ptr() if free_head is not None else None, block_table.data_ptr(), W,
@@ -581,7 +584,7 @@ def bfp8_kv_append(k, v, slot_map, k_cache, k_scales, v_cache, v_scales, stream=
     k_strides, v_strides = k.stride(), v.stride()
     _need(v.get_device() == dev.index and (T == 0 or (k_strides[2] == 1 and v_strides[2] == 1)),
           "k and v must be on one GPU, their rows contiguous")
-    _need_i32(dev, ("slot_map", slot_map, (T,)))
+    _need_i32(dev.index, ("slot_map", slot_map, (T,)))
     _check("bfp8_kv_append", library().bfp8_kv_append(
         k.data_ptr(), k_strides[0], k_strides[1], v.data_ptr(), v_strides[0], v_strides[1],
         slot_map.data_ptr(), T, k_cache.data_ptr(), k_scales.data_ptr(), v_cache.data_ptr(),
@@ -615,7 +618,7 @@ def bfp8_attn_paged(q, k_cache, k_scales, v_cache, v_scales, block_table, q_offs
           "out must be a contiguous [T, Hq, Dv] on q's GPU")
     _need(block_table.dim() == 2, "block_table must be [R, W]")
     R, W = block_table.shape
-    _need_i32(dev, ("block_table", block_table, None), ("q_offsets", q_offsets, (R + 1,)),
+    _need_i32(dev.index, ("block_table", block_table, None), ("q_offsets", q_offsets, (R + 1,)),
               ("kv_lens", kv_lens, (R,)), ("tile_offsets", tile_offsets, (R + 1,)))
     if lse is not None:
         _need(lse.dtype is torch.float32 and lse.shape == (T, Hq) and lse.device == dev and
@@ -657,9 +660,8 @@ def rope_frequencies(dim, base=10000.0, factor=1.0, trained_len=4096, fast=32.0,
     return freq.to(device, torch.float32), 0.1 * math.log(factor) + 1.0
 
 
-def _need_rows(device, *named):
-    """bf16 tensors on the call's GPU, whose last dim is contiguous."""
-    gpu = device.index
+def _need_rows(gpu, *named):
+    """bf16 tensors on this GPU, whose last dim is contiguous."""
     for name, t in named:
         if t.dtype is not torch.bfloat16 or t.get_device() != gpu:
             raise ValueError(f"{name} must be bf16, on the call's GPU")
@@ -670,18 +672,22 @@ def _need_rows(device, *named):
 def bfp8_rope(x, positions, inv_freq, out, interleaved=False, amplitude=1.0, stream=None):
     """out bf16 [T, H, D] = x bf16 [T, H, D] (any token and head strides) turned by positions int32 [T]
     times inv_freq fp32 [D/2]; out may be x itself.  x[..., first:first + D] rotates part of a head."""
-    dev = x.device
-    _need(x.is_cuda, "all tensors must be on the GPU")
-    _need(x.dim() == 3 and out.shape == x.shape, "x and out must be [T, H, D]")
-    T, H, D = x.shape
-    _need_rows(dev, ("x", x), ("out", out))
-    _need_i32(dev, ("positions", positions, (T,)))
-    _need(inv_freq.dtype is torch.float32 and inv_freq.shape == (D // 2,) and inv_freq.device == dev and
-          inv_freq.is_contiguous(), "inv_freq must be a contiguous fp32 [D/2] on x's GPU")
+    gpu, shape = x.get_device(), x.shape
+    _need(gpu >= 0, "all tensors must be on the GPU")
+    _need(len(shape) == 3 and out.shape == shape, "x and out must be [T, H, D]")
+    T, H, D = shape
     xs, ys = x.stride(), out.stride()
-    _check("bfp8_rope", library().bfp8_rope(
+    if not (x.dtype is out.dtype is torch.bfloat16 and out.get_device() == gpu and xs[2] == ys[2] == 1):
+        _need_rows(gpu, ("x", x), ("out", out))
+    _need_i32(gpu, ("positions", positions, (T,)))
+    if not (inv_freq.dtype is torch.float32 and inv_freq.shape == (D // 2,) and inv_freq.get_device() == gpu and
+            inv_freq.is_contiguous()):
+        raise ValueError("inv_freq must be a contiguous fp32 [D/2] on x's GPU")
+    status = library().bfp8_rope(
         x.data_ptr(), xs[0], xs[1], positions.data_ptr(), inv_freq.data_ptr(), out.data_ptr(), ys[0],
-        ys[1], T, H, D, 1 if interleaved else 0, amplitude, _stream(stream, dev)))
+        ys[1], T, H, D, 1 if interleaved else 0, amplitude, _handle(stream, gpu))
+    if status:
+        _check("bfp8_rope", status)
 
 
 def latent_cache_buffers(num_pages, page_size, device):
@@ -691,20 +697,21 @@ def latent_cache_buffers(num_pages, page_size, device):
             torch.empty(num_pages, page_size, LATENT_ROPE, dtype=torch.bfloat16, device=device))
 
 
-def _latent_shape(device, latent_cache, latent_scales, rope_cache):
+def _latent_shape(gpu, latent_cache, latent_scales, rope_cache):
     """(P, B) of a layer's latent cache, checked."""
     if latent_cache.dtype is not torch.uint8 and latent_cache.dtype is not torch.float8_e4m3fn:
         raise TypeError(f"expected e4m3 codes (uint8 or float8_e4m3fn), got {latent_cache.dtype}")
-    _need(latent_cache.dim() == 3 and latent_cache.shape[2] == LATENT, "latent_cache must be [P, B, 512]")
-    P, B, _ = latent_cache.shape
-    _need(latent_scales.dtype is torch.float32 and latent_scales.shape == (P, B),
-          "latent_scales must be fp32 [P, B]")
-    _need(rope_cache.dtype is torch.bfloat16 and rope_cache.shape == (P, B, LATENT_ROPE),
-          "rope_cache must be bf16 [P, B, 64]")
-    gpu = device.index
-    for t in (latent_cache, latent_scales, rope_cache):
-        if t.get_device() != gpu or not t.is_contiguous():
-            raise ValueError("the cache must be contiguous, on the call's GPU")
+    shape = latent_cache.shape
+    if len(shape) != 3 or shape[2] != LATENT:
+        raise ValueError("latent_cache must be [P, B, 512]")
+    P, B, _ = shape
+    if latent_scales.dtype is not torch.float32 or latent_scales.shape != (P, B):
+        raise ValueError("latent_scales must be fp32 [P, B]")
+    if rope_cache.dtype is not torch.bfloat16 or rope_cache.shape != (P, B, LATENT_ROPE):
+        raise ValueError("rope_cache must be bf16 [P, B, 64]")
+    if not (latent_cache.get_device() == latent_scales.get_device() == rope_cache.get_device() == gpu and
+            latent_cache.is_contiguous() and latent_scales.is_contiguous() and rope_cache.is_contiguous()):
+        raise ValueError("the cache must be contiguous, on the call's GPU")
     return P, B
 
 
@@ -713,43 +720,56 @@ def bfp8_latent_append(kv, slot_map, positions, inv_freq, latent_cache, latent_s
     """Rows kv bf16 [T, 576] (any token stride) into the slots of slot_map int32 [T] (in place): the
     first 512 dims normed by norm_weight bf16 [512] (None: as they are) and quantized, the last 64
     rotated as by bfp8_rope at positions int32 [T]."""
-    dev = kv.device
-    _need(kv.is_cuda, "all tensors must be on the GPU")
-    P, B = _latent_shape(dev, latent_cache, latent_scales, rope_cache)
+    gpu = kv.get_device()
+    _need(gpu >= 0, "all tensors must be on the GPU")
+    P, B = _latent_shape(gpu, latent_cache, latent_scales, rope_cache)
     T = slot_map.shape[0]
-    _need(kv.shape == (T, LATENT + LATENT_ROPE), "kv must be [T, 576]")
-    _need_rows(dev, ("kv", kv))
-    _need_i32(dev, ("slot_map", slot_map, (T,)), ("positions", positions, (T,)))
-    _need(inv_freq.dtype is torch.float32 and inv_freq.shape == (LATENT_ROPE // 2,) and inv_freq.device == dev and
-          inv_freq.is_contiguous(), "inv_freq must be a contiguous fp32 [32] on kv's GPU")
+    if kv.shape != (T, LATENT + LATENT_ROPE):
+        raise ValueError("kv must be [T, 576]")
+    kvs = kv.stride()
+    if kv.dtype is not torch.bfloat16 or kvs[1] != 1:
+        _need_rows(gpu, ("kv", kv))
+    _need_i32(gpu, ("slot_map", slot_map, (T,)), ("positions", positions, (T,)))
+    if not (inv_freq.dtype is torch.float32 and inv_freq.shape == (LATENT_ROPE // 2,) and inv_freq.get_device() == gpu and
+            inv_freq.is_contiguous()):
+        raise ValueError("inv_freq must be a contiguous fp32 [32] on kv's GPU")
     if norm_weight is not None:
         _need(norm_weight.shape == (LATENT,) and norm_weight.is_contiguous(), "norm_weight must be a contiguous [512]")
-        _need_rows(dev, ("norm_weight", norm_weight))
-    _check("bfp8_latent_append", library().bfp8_latent_append(
-        kv.data_ptr(), kv.stride(0), norm_weight.data_ptr() if norm_weight is not None else None, eps,
+        _need_rows(gpu, ("norm_weight", norm_weight))
+    status = library().bfp8_latent_append(
+        kv.data_ptr(), kvs[0], norm_weight.data_ptr() if norm_weight is not None else None, eps,
         slot_map.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), 1 if interleaved else 0, amplitude, T,
-        latent_cache.data_ptr(), latent_scales.data_ptr(), rope_cache.data_ptr(), P, B, _stream(stream, dev)))
+        latent_cache.data_ptr(), latent_scales.data_ptr(), rope_cache.data_ptr(), P, B, _handle(stream, gpu))
+    if status:
+        _check("bfp8_latent_append", status)
 
 
 def bfp8_latent_gather(latent_cache, latent_scales, rope_cache, block_table, row_offsets, latent, rope,
                        starts=None, stream=None):
     """Request r's tokens (from starts[r] on) back to rows row_offsets[r] .. row_offsets[r+1] of latent
     bf16 [N, 512] and rope bf16 [N, 64] (any row strides that are multiples of 8)."""
-    dev = latent_cache.device
-    _need(latent_cache.is_cuda, "all tensors must be on the GPU")
-    P, B = _latent_shape(dev, latent_cache, latent_scales, rope_cache)
-    _need(block_table.dim() == 2, "block_table must be [R, W]")
+    gpu = latent_cache.get_device()
+    _need(gpu >= 0, "all tensors must be on the GPU")
+    P, B = _latent_shape(gpu, latent_cache, latent_scales, rope_cache)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [R, W]")
     R, W = block_table.shape
     N = latent.shape[0]
-    _need(latent.shape == (N, LATENT) and rope.shape == (N, LATENT_ROPE), "latent must be [N, 512], rope [N, 64]")
-    _need_rows(dev, ("latent", latent), ("rope", rope))
-    _need_i32(dev, ("block_table", block_table, None), ("row_offsets", row_offsets, (R + 1,)))
+    if latent.shape != (N, LATENT) or rope.shape != (N, LATENT_ROPE):
+        raise ValueError("latent must be [N, 512], rope [N, 64]")
+    ls, rs = latent.stride(), rope.stride()
+    if not (latent.dtype is rope.dtype is torch.bfloat16 and latent.get_device() == rope.get_device() == gpu and
+            ls[1] == rs[1] == 1):
+        _need_rows(gpu, ("latent", latent), ("rope", rope))
+    _need_i32(gpu, ("block_table", block_table, None), ("row_offsets", row_offsets, (R + 1,)))
     if starts is not None:
-        _need_i32(dev, ("starts", starts, (R,)))
-    _check("bfp8_latent_gather", library().bfp8_latent_gather(
+        _need_i32(gpu, ("starts", starts, (R,)))
+    status = library().bfp8_latent_gather(
         latent_cache.data_ptr(), latent_scales.data_ptr(), rope_cache.data_ptr(), P, B, block_table.data_ptr(), W,
         row_offsets.data_ptr(), starts.data_ptr() if starts is not None else None, R, N, latent.data_ptr(),
-        latent.stride(0), rope.data_ptr(), rope.stride(0), _stream(stream, dev)))
+        ls[0], rope.data_ptr(), rs[0], _handle(stream, gpu))
+    if status:
+        _check("bfp8_latent_gather", status)
 
 
 def bfp8_attn_latent_workspace_size(R, max_new, heads) -> int:
@@ -767,32 +787,40 @@ def bfp8_attn_latent(q_latent, q_rope, latent_cache, latent_scales, rope_cache, 
     """out bf16 [T, H, 512] (and lse fp32 [T, H]) = causal attention of each request's new tokens, q_latent
     bf16 [T, H, 512] and q_rope bf16 [T, H, 64], over its latents.  q_offsets and kv_lens come from
     bfp8_kv_plan; max_new bounds the requests' new tokens.  Any token and head strides."""
-    dev = q_latent.device
-    _need(q_latent.is_cuda, "all tensors must be on the GPU")
-    P, B = _latent_shape(dev, latent_cache, latent_scales, rope_cache)
-    _need(q_latent.dim() == 3 and q_latent.shape[2] == LATENT, "q_latent must be [T, H, 512]")
-    T, H, _ = q_latent.shape
-    _need(q_rope.shape == (T, H, LATENT_ROPE) and out.shape == (T, H, LATENT),
-          "q_rope must be [T, H, 64], out [T, H, 512]")
-    _need_rows(dev, ("q_latent", q_latent), ("q_rope", q_rope), ("out", out))
-    _need(block_table.dim() == 2, "block_table must be [R, W]")
+    gpu = q_latent.get_device()
+    _need(gpu >= 0, "all tensors must be on the GPU")
+    P, B = _latent_shape(gpu, latent_cache, latent_scales, rope_cache)
+    shape = q_latent.shape
+    if len(shape) != 3 or shape[2] != LATENT:
+        raise ValueError("q_latent must be [T, H, 512]")
+    T, H, _ = shape
+    if q_rope.shape != (T, H, LATENT_ROPE) or out.shape != shape:
+        raise ValueError("q_rope must be [T, H, 64], out [T, H, 512]")
+    ql, qr, os_ = q_latent.stride(), q_rope.stride(), out.stride()
+    if not (q_latent.dtype is q_rope.dtype is out.dtype is torch.bfloat16 and
+            q_rope.get_device() == out.get_device() == gpu and ql[2] == qr[2] == os_[2] == 1):
+        _need_rows(gpu, ("q_latent", q_latent), ("q_rope", q_rope), ("out", out))
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [R, W]")
     R, W = block_table.shape
-    _need_i32(dev, ("block_table", block_table, None), ("q_offsets", q_offsets, (R + 1,)),
+    _need_i32(gpu, ("block_table", block_table, None), ("q_offsets", q_offsets, (R + 1,)),
               ("kv_lens", kv_lens, (R,)))
-    if lse is not None:
-        _need(lse.dtype is torch.float32 and lse.shape == (T, H) and lse.device == dev and
-              lse.is_contiguous(), "lse must be a contiguous fp32 [T, H] on q_latent's GPU")
+    if lse is not None and not (lse.dtype is torch.float32 and lse.shape == (T, H) and lse.get_device() == gpu and
+                                lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous fp32 [T, H] on q_latent's GPU")
     ws_bytes = 0
     if workspace is not None:
-        _need(workspace.device == dev and workspace.is_contiguous(), "workspace must be on q_latent's GPU")
-        ws_bytes = workspace.numel() * workspace.element_size()
-    ql, qr, os_ = q_latent.stride(), q_rope.stride(), out.stride()
-    _check("bfp8_attn_latent", library().bfp8_attn_latent(
+        if workspace.get_device() != gpu or not workspace.is_contiguous():
+            raise ValueError("workspace must be on q_latent's GPU")
+        ws_bytes = workspace.nbytes
+    status = library().bfp8_attn_latent(
         q_latent.data_ptr(), ql[0], ql[1], q_rope.data_ptr(), qr[0], qr[1], latent_cache.data_ptr(),
         latent_scales.data_ptr(), rope_cache.data_ptr(), P, B, block_table.data_ptr(), W, q_offsets.data_ptr(),
         kv_lens.data_ptr(), R, T, max_new, H, scale, out.data_ptr(), os_[0], os_[1],
         lse.data_ptr() if lse is not None else None, workspace.data_ptr() if workspace is not None else None,
-        ws_bytes, _stream(stream, dev)))
+        ws_bytes, _handle(stream, gpu))
+    if status:
+        _check("bfp8_attn_latent", status)
 
 
 # ------------------------------------------------------- allocating conveniences
