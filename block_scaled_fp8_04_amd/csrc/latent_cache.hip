@@ -9,8 +9,8 @@
 //     s = 2^ceil(log2(max(amax |y|, 1e-4) / 448)),   code = e4m3_rne(y / s)
 // The lower half's lanes each turn one pair of the key.
 //
-// gather: one wave per 16 rows: a row's codes are eight a lane, its key eight elements of eight lanes,
-// four rows on their way at a time.
+// gather: one wave per eight or four rows: a row's codes are eight a lane, its key eight elements of
+// eight lanes.
 #include "attn_common.hpp"
 #include "device_codec.hpp"
 #include "internal.hpp"
@@ -120,8 +120,10 @@ hipError_t launch_latent_append(const void* kv, int64_t kv_ts, const void* norm_
 
 // ------------------------------------------------------------------ gather
 
-constexpr int kGatherRows = 16;               // of a wave
-constexpr int kGatherAhead = 4;               // rows on their way
+// Rows of a wave, whose loads are all on their way at once: eight where there are few, as what counts is
+// latency (16000 rows of 8 requests: 11.0 us, and 18.3 with four), four where there are many, as what
+// counts is how many waves a CU holds (64000 rows of 16 requests: 31 us, and 27 with four).
+constexpr int kGatherFew = 40000;
 
 struct GatherArgs {
     const uint8_t* codes;
@@ -140,17 +142,23 @@ struct GatherArgs {
     int64_t r_ts;
 };
 
+template <int ROWS>
 __global__ __launch_bounds__(kLatentThreads) void latent_gather_kernel(GatherArgs a) {
     const int lane = threadIdx.x & 63;
-    const int64_t row0 = ((int64_t)blockIdx.x * kLatentWaves + (threadIdx.x >> 6)) * kGatherRows;
+    const int64_t row0 = ((int64_t)blockIdx.x * kLatentWaves + (threadIdx.x >> 6)) * ROWS;
     if (row0 >= a.rows) return;
     const int each64 = a.row_offsets[min(lane * 64, a.R)];
+    int ends = a.row_offsets[min(1 + lane, a.R)];                 // of request from + lane
     if (row0 >= a.row_offsets[a.R]) return;
     // the request of the first row, in two steps of 64; those of the others follow
-    int from = last_of(lane * 64 < a.R && each64 <= row0) * 64;
-    int ends = a.row_offsets[min(from + 1 + lane, a.R)];          // of request from + lane
-    int r = a.R;                                                  // lane j < 16: row j's
-    for (int j = 0; j < kGatherRows; ++j) {
+    int from = 0;
+    if (a.R > 64) {
+        from = last_of(lane * 64 < a.R && each64 <= row0) * 64;
+        ends = a.row_offsets[min(from + 1 + lane, a.R)];
+    }
+    int r = a.R;                                                  // lane j < ROWS: row j's
+#pragma unroll
+    for (int j = 0; j < ROWS; ++j) {
         int before = __popcll(__ballot(from + lane < a.R && ends <= row0 + j));
         while (before == 64 && from + 64 < a.R) {
             from += 64;
@@ -169,28 +177,25 @@ __global__ __launch_bounds__(kLatentThreads) void latent_gather_kernel(GatherArg
         }
     }
     const int64_t mine = max(at, (int64_t)0);
-    const float scale = lane < kGatherRows ? a.scales[mine] : 0.f;
+    const float scale = lane < ROWS ? a.scales[mine] : 0.f;
+    uint2 c[ROWS];
+    uint4 k[ROWS];
+    int64_t slot[ROWS];
 #pragma unroll
-    for (int j0 = 0; j0 < kGatherRows; j0 += kGatherAhead) {
-        uint2 c[kGatherAhead];
-        uint4 k[kGatherAhead];
-        int64_t slot[kGatherAhead];
+    for (int j = 0; j < ROWS; ++j) {
+        slot[j] = (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)at, j) |
+                  (int64_t)__builtin_amdgcn_readlane((int)(at >> 32), j) << 32;
+        const int64_t s = max(slot[j], (int64_t)0);
+        c[j] = *(const uint2*)(a.codes + s * kLatent + 8 * lane);
+        k[j] = *(const uint4*)(a.rope + s * kLatentRope + 8 * (lane & 7));
+    }
 #pragma unroll
-        for (int j = 0; j < kGatherAhead; ++j) {
-            slot[j] = (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)at, j0 + j) |
-                      (int64_t)__builtin_amdgcn_readlane((int)(at >> 32), j0 + j) << 32;
-            const int64_t s = max(slot[j], (int64_t)0);
-            c[j] = *(const uint2*)(a.codes + s * kLatent + 8 * lane);
-            k[j] = *(const uint4*)(a.rope + s * kLatentRope + 8 * (lane & 7));
-        }
-#pragma unroll
-        for (int j = 0; j < kGatherAhead; ++j) {
-            if (slot[j] < 0) continue;
-            const float e = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(scale), j0 + j));
-            *(uint4*)(a.latent + (row0 + j0 + j) * a.l_ts + 8 * lane) =
-                __builtin_bit_cast(uint4, widen8((int)c[j].x, (int)c[j].y, e));
-            if (lane < 8) *(uint4*)(a.rope_out + (row0 + j0 + j) * a.r_ts + 8 * lane) = k[j];
-        }
+    for (int j = 0; j < ROWS; ++j) {
+        if (slot[j] < 0) continue;
+        const float e = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(scale), j));
+        *(uint4*)(a.latent + (row0 + j) * a.l_ts + 8 * lane) =
+            __builtin_bit_cast(uint4, widen8((int)c[j].x, (int)c[j].y, e));
+        if (lane < 8) *(uint4*)(a.rope_out + (row0 + j) * a.r_ts + 8 * lane) = k[j];
     }
 }
 
@@ -201,9 +206,10 @@ hipError_t launch_latent_gather(const void* codes, const float* scales, const vo
                                 int64_t r_ts, hipStream_t stream) {
     const GatherArgs a = {(const uint8_t*)codes, scales, (const uint16_t*)rope, pages, __builtin_ctz(page), block_table,
                           width, row_offsets, starts, (int)R, rows, (uint16_t*)latent, l_ts, (uint16_t*)rope_out, r_ts};
-    const int64_t waves = (rows + kGatherRows - 1) / kGatherRows;
-    hipLaunchKernelGGL(latent_gather_kernel, dim3((unsigned)((waves + kLatentWaves - 1) / kLatentWaves)),
-                       dim3(kLatentThreads), 0, stream, a);
+    const bool few = rows < kGatherFew;
+    const int64_t each = kLatentWaves * (few ? 8 : 4);
+    hipLaunchKernelGGL(few ? latent_gather_kernel<8> : latent_gather_kernel<4>,
+                       dim3((unsigned)((rows + each - 1) / each)), dim3(kLatentThreads), 0, stream, a);
     return hipGetLastError();
 }
 
