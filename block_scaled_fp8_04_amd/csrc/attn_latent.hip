@@ -149,6 +149,14 @@ struct LatentRequests {
     }
 };
 
+// The lane, in a form that keeps what is computed from it at a run's ends from being held in registers
+// over its tiles.
+__device__ __forceinline__ int fresh_lane() {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
 // An item, that is a request's row tile, and its tiles.  Uniform.
 struct LatentJob {
     int r, rt, tiles;
@@ -246,7 +254,7 @@ struct LatentWalk {
     template <int X>
     static __device__ __forceinline__ void stage_q(const LatentArgs& a, const LatentJob& u, uint8_t* st) {
         constexpr int MINE = ROWS / 4, C = QROW / 16;            // rows of a wave; chunks of a row
-        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int lane = fresh_lane(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         const int first = u.rt * ROWS + wave * MINE, last = u.it.rows - 1;
         if (!a.q_near) {                                         // by elements
             constexpr int N = X == RW - 1 ? C + 8 : C;
@@ -300,7 +308,7 @@ struct LatentWalk {
     }
     template <int X>
     __device__ __forceinline__ void read_q(const uint8_t* st) {
-        const int h = (threadIdx.x & 63) >> 5, r = rg * 32 + (threadIdx.x & 31);
+        const int lane = fresh_lane(), h = lane >> 5, r = rg * 32 + (lane & 31);
         // operand s: dims 32 (s / 2) + 16 h + 8 (s % 2) .., as a 16-byte read of codes feeds two
 #pragma unroll
         for (int s = X * 16; s < X * 16 + 32 / RW; ++s) {
@@ -387,30 +395,26 @@ struct LatentWalk {
         for (int p = 0; p < AHEAD; ++p) w[p] = read(p);
         __builtin_amdgcn_sched_barrier(0);
         bf8v lo = widen8((int)w[0].x, (int)w[0].y, scale), hi = widen8((int)w[0].z, (int)w[0].w, scale);
-#pragma unroll
-        for (int p = 0; p < N; ++p) {
-            bf8v next_lo = lo, next_hi = hi;
-            if (p + 1 < 16) {
-                next_lo = widen8((int)w[p + 1].x, (int)w[p + 1].y, scale);
-                next_hi = widen8((int)w[p + 1].z, (int)w[p + 1].w, scale);
-            }
-            if (p + AHEAD < N) w[p + AHEAD] = read(p + AHEAD);
-            if (p % 2 == 1) fetch.load(to, p / 2);
-            if (p == 16) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) tokens[i] = *(const v4f*)(scales + 8 * (i >> 1) + 4 * h + 2 * (i & 1));
-            }
+        const auto mfma = [&](bf8v x, int k) __attribute__((always_inline)) {
             __builtin_amdgcn_sched_barrier(0);
-            if (p < 16) {
-                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(lo, q[2 * p], s, 0, 0, 0);
-                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(hi, q[2 * p + 1], s, 0, 0, 0);
-            } else {
-                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8v, w[p]), q[16 + p], s, 0, 0, 0);
-            }
+            s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, q[k], s, 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
-            lo = next_lo;
-            hi = next_hi;
+        };
+#pragma unroll
+        for (int p = 0; p < 16; ++p) {
+            bf8v next = lo;
+            mfma(lo, 2 * p);
+            if (p + 1 < 16) next = widen8((int)w[p + 1].x, (int)w[p + 1].y, scale);
+            w[p + AHEAD] = read(p + AHEAD);
+            mfma(hi, 2 * p + 1);
+            if (p + 1 < 16) hi = widen8((int)w[p + 1].z, (int)w[p + 1].w, scale);
+            if (p < FETCHES) fetch.load(to, p);
+            lo = next;
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) tokens[i] = *(const v4f*)(scales + 8 * (i >> 1) + 4 * h + 2 * (i & 1));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mfma(__builtin_bit_cast(bf8v, w[16 + k]), 32 + k);
         return s;
     }
 
@@ -450,7 +454,7 @@ struct LatentWalk {
         l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
 
-    // O^T += C^T P^T over a tile's tokens, 16 at a time; read and widened ahead as in logits().
+    // O^T += C^T P^T over a tile's tokens, 16 at a time; read ahead, and widened two ahead.
     __device__ __forceinline__ void values(const uint8_t* st, const h8v (&w)[4]) {
         const int lane = threadIdx.x & 63, h = lane >> 5, g = lane >> 4 & 1, i = lane >> 1 & 7;
         // this lane's address is that of token T, 8 of 16 dims; it gets 8 tokens of dim lane & 31
@@ -466,16 +470,17 @@ struct LatentWalk {
 #pragma unroll
         for (int n = 0; n < AHEAD; ++n) x[n] = read(n);
         __builtin_amdgcn_sched_barrier(0);
-        h8v f = widen8_f16(x[0][0], x[0][1]);
+        h8v f = widen8_f16(x[0][0], x[0][1]), next = widen8_f16(x[1][0], x[1][1]);
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            h8v next = f;
-            if (n + 1 < N) next = widen8_f16(x[n + 1][0], x[n + 1][1]);
+            h8v last = next;
+            if (n + 2 < N) last = widen8_f16(x[n + 2][0], x[n + 2][1]);
             if (n + AHEAD < N) x[n + AHEAD] = read(n + AHEAD);
             __builtin_amdgcn_sched_barrier(0);
             o[n % DT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, w[n / DT], o[n % DT], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
             f = next;
+            next = last;
         }
     }
 
@@ -573,7 +578,7 @@ struct LatentWalk {
 
     // Partial results of a slot: [RW][16 dims blocks][4][64 lanes] of four floats, then (m, l) a row.
     __device__ __forceinline__ void store_part(const LatentArgs& a, const LatentJob& u, int64_t slot) const {
-        const int lane = threadIdx.x & 63;
+        const int lane = fresh_lane();
         if (row(u.rt) >= u.it.rows) return;
         v4f* const ws = (v4f*)a.ws + ((slot * RW + rg) * 16 + dw * DT) * 256 + lane;
 #pragma unroll
