@@ -18,7 +18,7 @@
 // Precision.  As keys, codes are widened to bf16 with their token's scale, exactly, and q is bf16 as
 // it comes.  As values they are widened to fp16 without it, exactly as well, and the scale goes into
 // the weight: the maximum is taken over x_t + e_t (in units of log 2), w_t = 2^(x_t + e_t - max) is
-// rounded to fp16 once (2^-12 of it, where a bf16 weight would lose 2^-9, as much as the rounding of
+// rounded to fp16 once (2^-11 of it, where a bf16 weight would lose 2^-8, as much as the rounding of
 // the output), and the norm sums w_t 2^-e_t before that rounding.  So a weight's size is that of the
 // token's contribution, and fp16's range is enough: what it drops is 2^-25 of the largest
 // contribution.  Logits, maxima, norms and sums are fp32; maxima are rounded up to integers, so that
@@ -842,7 +842,10 @@ static hipError_t latent_launch(const LatentArgs& a, const LatentPlan& p, hipStr
 }
 
 hipError_t launch_attn_latent(LatentArgs a, hipStream_t stream) {
-    const LatentPlan p = latent_plan(a.R, a.max_new, a.heads);
+    LatentPlan p = latent_plan(a.R, a.max_new, a.heads);
+    // costs that quotient() takes: a split launch's are below 2^31
+    const int64_t tiles = ((a.width << a.log_b) + kLatTile - 1) / kLatTile;
+    p.split = p.split && a.R * p.row_tiles * (tiles + kLatItemCost) < (int64_t)1 << 31;
     // sixteen rows of queries, in memory, span at most so many tokens
     const auto near = [&](int64_t ts, int64_t hs) {
         return ts < (1 << 26) && hs < ((int64_t)1 << 30) / a.heads && (ts | hs) % 8 == 0;

@@ -589,7 +589,7 @@ int bfp8_latent_gather(const void* latent_cache, const float* latent_scales,
  *     out = bf16_rne( sum_t p_t c_t / sum_t p_t ),  p_t = exp(x_t - max),  lse = log sum_t exp(x_t)
  * with c_t the token's 512 latent values and k_t its 64 rotated dims.  A row that
  * sees nothing gets zeros, and -infinity.  Logits, sums and statistics are fp32; p_t
- * enters its product with eleven significant bits (2^-12 of it at most is lost).
+ * enters its product with eleven significant bits (2^-11 of it at most is lost).
  *   q_latent_bf16 : bf16, element (t, j, d) at t * ql_token_stride + j * ql_head_stride + d,
  *              d < 512, rows 0 .. T-1; q_rope_bf16 likewise, d < 64
  *   block_table : DEVICE int32 [R, table_width]; entries up to kv_len are read,
