@@ -129,15 +129,21 @@ struct LatentRequests {
     }
     // sums up the costs, with `start` before the 64 requests; returns what comes before the next
     __device__ __forceinline__ int64_t scan(int64_t start) {
-        const int lane = threadIdx.x & 63;
         int64_t sum = cost;
-#pragma unroll
-        for (int step = 1; step < 64; step <<= 1) {
-            const int64_t x = __shfl_up((long long)sum, step);
-            if (lane >= step) sum += x;
-        }
+        add<0x111, 0xF>(sum);                                    // rows of 16 lanes: from 1, 2, 4, 8 before
+        add<0x112, 0xF>(sum);
+        add<0x114, 0xF>(sum);
+        add<0x118, 0xF>(sum);
+        add<0x142, 0xA>(sum);                                    // row 1, 3: from the last of the one before
+        add<0x143, 0xC>(sum);                                    // row 2, 3: from the last of row 1
         before = start + sum - cost;
         return start + from_lane(sum, 63);
+    }
+    template <int CONTROL, int LANES>
+    static __device__ __forceinline__ void add(int64_t& sum) {
+        const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)sum, CONTROL, LANES, 0xF, false);
+        const int hi = __builtin_amdgcn_update_dpp(0, (int)(sum >> 32), CONTROL, LANES, 0xF, false);
+        sum += (int64_t)hi << 32 | lo;
     }
     static __device__ __forceinline__ int64_t from_lane(int64_t x, int lane) {
         return (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)x, lane) |
@@ -454,28 +460,35 @@ struct LatentWalk {
         l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
 
-    // O^T += C^T P^T over a tile's tokens, 16 at a time; read ahead, and widened two ahead.
-    __device__ __forceinline__ void values(const uint8_t* st, const h8v (&w)[4]) {
-        const int lane = threadIdx.x & 63, h = lane >> 5, g = lane >> 4 & 1, i = lane >> 1 & 7;
-        // this lane's address is that of token T, 8 of 16 dims; it gets 8 tokens of dim lane & 31
-        const int T = (i & 3) + 8 * (i >> 2) + 4 * h;
-        const uint8_t* const c = st + T * kLatent + (lane & 1) * 8;
-        const int cs = lat_swz(T) ^ g;
-        constexpr int N = 4 * DT, AHEAD = 6;                     // reads, those on their way
+    // Codes of a tile as values: read n is of 16 tokens (n / DT) and 32 dims (n % DT), 8 tokens of a dim a
+    // lane; reads are AHEAD of their use, and the first ones are asked for before the weights are there.
+    struct Codes {
+        static constexpr int N = 4 * DT, AHEAD = 6;
         v2i x[N];
-        const auto read = [&](int n) {
+        const uint8_t* c;
+        int cs;
+        __device__ __forceinline__ Codes(const uint8_t* st) {
+            const int lane = threadIdx.x & 63, h = lane >> 5, g = lane >> 4 & 1, i = lane >> 1 & 7;
+            // this lane's address is that of token T, 8 of 16 dims; it gets 8 tokens of dim lane & 31
+            const int T = (i & 3) + 8 * (i >> 2) + 4 * h;
+            c = st + T * kLatent + (lane & 1) * 8;
+            cs = lat_swz(T) ^ g;
+        }
+        __device__ __forceinline__ void read(int n, int dw) {
             const int chunk = 2 * (dw * DT + n % DT) ^ cs;
-            return __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i)(c + n / DT * 16 * kLatent + (chunk << 4)));
-        };
-#pragma unroll
-        for (int n = 0; n < AHEAD; ++n) x[n] = read(n);
+            x[n] = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i)(c + n / DT * 16 * kLatent + (chunk << 4)));
+        }
+    };
+
+    // O^T += C^T P^T over a tile's tokens, 16 at a time; widened two ahead.
+    __device__ __forceinline__ void values(Codes& k, const h8v (&w)[4]) {
         __builtin_amdgcn_sched_barrier(0);
-        h8v f = widen8_f16(x[0][0], x[0][1]), next = widen8_f16(x[1][0], x[1][1]);
+        h8v f = widen8_f16(k.x[0][0], k.x[0][1]), next = widen8_f16(k.x[1][0], k.x[1][1]);
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
+        for (int n = 0; n < k.N; ++n) {
             h8v last = next;
-            if (n + 2 < N) last = widen8_f16(x[n + 2][0], x[n + 2][1]);
-            if (n + AHEAD < N) x[n + AHEAD] = read(n + AHEAD);
+            if (n + 2 < k.N) last = widen8_f16(k.x[n + 2][0], k.x[n + 2][1]);
+            if (n + k.AHEAD < k.N) k.read(n + k.AHEAD, dw);
             __builtin_amdgcn_sched_barrier(0);
             o[n % DT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f, w[n / DT], o[n % DT], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
@@ -519,6 +532,9 @@ struct LatentWalk {
                 lds.refs[pair] = m;
             }
         }
+        Codes codes(st);
+#pragma unroll
+        for (int n = 0; n < codes.AHEAD; ++n) codes.read(n, dw);
         barrier_written();
         const float m0 = lds.refs[first], m1 = lds.refs[first + 128];
 #pragma unroll
@@ -535,7 +551,7 @@ struct LatentWalk {
             l *= m == top ? 1.f : shrink(m, top);
             m = top;
         }
-        values(st, w);
+        values(codes, w);
     }
 
     // The rows' norms, over both halves of the tokens (which have one reference).
