@@ -758,13 +758,13 @@ __global__ __launch_bounds__(kLatThreads, 1) void attn_latent_item_kernel(Latent
 static_assert(kKvMaxRequests <= 64 * 64, "a request is found in two steps of 64");
 
 // Adds the parts of items that several workgroups shared, and gives the rows of a request without
-// tokens their zeros.  A workgroup takes 32 rows x 32 dims; each of its waves takes every fourth part,
-// in token order, then the waves' sums are added in order.
-template <int RW>
-__global__ __launch_bounds__(kLatThreads) void attn_latent_join_kernel(LatentArgs a, int row_tiles) {
+// tokens their zeros.  A workgroup takes 32 rows x 32 dims; each of its WAVES waves takes every
+// WAVES-th part, in token order, then the waves' sums are added in order.
+template <int RW, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void attn_latent_join_kernel(LatentArgs a, int row_tiles) {
     constexpr int ROWS = 32 * RW;
-    __shared__ v4f sums[4][4][64];
-    __shared__ float2 stats[4][32];
+    __shared__ v4f sums[WAVES][4][64];
+    __shared__ float2 stats[WAVES][32];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, d = blockIdx.y;
     const int rg = blockIdx.x % RW, item = blockIdx.x / RW;
     const int r = item / row_tiles, rt = item % row_tiles;
@@ -778,7 +778,7 @@ __global__ __launch_bounds__(kLatThreads) void attn_latent_join_kernel(LatentArg
         const v4f* const ws = (const v4f*)a.ws + (rg * 16 + d) * 256 + lane;
         const float2* const ml = latent_ml(a, ROWS) + rg * 32 + (lane & 31);
 #pragma unroll 2
-        for (int g = wave; g <= info.y; g += 4) {
+        for (int g = wave; g <= info.y; g += WAVES) {
             const int64_t slot = g == 0 ? info.x : (info.x / 2 + g) * 2;
             const float2 part = ml[slot * ROWS];
             v4f x[4];
@@ -797,16 +797,20 @@ __global__ __launch_bounds__(kLatThreads) void attn_latent_join_kernel(LatentArg
     for (int i = 0; i < 4; ++i) sums[wave][i][lane] = o[i];
     if (lane < 32) stats[wave][lane] = make_float2(m, l);
     __syncthreads();
+    if (wave >= 4) return;
     const int i = wave, row = rt * ROWS + rg * 32 + (lane & 31);
     if (row >= it.rows) return;
-    float2 part[4];
+    float2 part[WAVES];
+    m = neg_inf();
 #pragma unroll
-    for (int z = 0; z < 4; ++z) part[z] = stats[z][lane & 31];
-    m = fmaxf(fmaxf(part[0].x, part[1].x), fmaxf(part[2].x, part[3].x));
+    for (int z = 0; z < WAVES; ++z) {
+        part[z] = stats[z][lane & 31];
+        m = fmaxf(m, part[z].x);
+    }
     v4f sum = {0.f, 0.f, 0.f, 0.f};
     l = 0.f;
 #pragma unroll
-    for (int z = 0; z < 4; ++z) {
+    for (int z = 0; z < WAVES; ++z) {
         const float f = part[z].x == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(part[z].x - m);
         sum += sums[z][i][lane] * f;
         l += part[z].y * f;
@@ -853,7 +857,13 @@ static hipError_t latent_launch(const LatentArgs& a, const LatentPlan& p, hipStr
     attn_latent_split_kernel<RW><<<dim3(kLatGroups), dim3(kLatThreads), 0, stream>>>(a, rt);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    attn_latent_join_kernel<RW><<<dim3((unsigned)(a.R * p.row_tiles * RW), 16), dim3(kLatThreads), 0, stream>>>(a, rt);
+    const int64_t joins = a.R * p.row_tiles * RW;
+    // with few items of many parts, eight waves (two long requests of 128 heads 63.8 -> 62.3 us, 24 drafts
+    // 27.0 -> 26.4); with many of few, four (64 requests of 128 heads 75.9 us, and 79.0 with eight)
+    if (joins < 64)
+        attn_latent_join_kernel<RW, 8><<<dim3((unsigned)joins, 16), dim3(512), 0, stream>>>(a, rt);
+    else
+        attn_latent_join_kernel<RW, 4><<<dim3((unsigned)joins, 16), dim3(256), 0, stream>>>(a, rt);
     return hipGetLastError();
 }
 
