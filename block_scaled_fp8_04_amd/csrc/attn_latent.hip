@@ -22,7 +22,16 @@
 // the output), and the norm sums w_t 2^-e_t before that rounding.  So a weight's size is that of the
 // token's contribution, and fp16's range is enough: what it drops is 2^-25 of the largest
 // contribution.  Logits, maxima, norms and sums are fp32; maxima are rounded up to integers, so that
-// rescaling by 2^(old - new) is exact.
+// rescaling by 2^(old - new) is exact.  (The fp8 matrix product would take the codes as they are, but it
+// drops what lies 13 bits below the largest product it adds: 2^-12.3 of the sum of their sizes, measured.)
+//
+// What bounds it.  64 requests of 512 to 8192 tokens: with 16 heads their 118 MB, which the main kernel
+// brings at 3.3 TB/s in 36 us (4.9 is what a large copy reaches), its tiles alone at 5.1; about 5 us are a
+// workgroup's first loads, one behind the other.  With 128 heads their 50 GFLOP, which take 77 us, 0.65
+// PFLOP/s (1.2 is what a large matrix product reaches), and 11 us for the join, at 4.5 TB/s.  The matrix
+// units are busy for 28 % of that: a wave has its SIMD to itself, as accumulators and queries take up its
+// registers, so nothing covers the softmax (800 of a tile's 5000 cycles), the trade of weights (700) and
+// the first reads behind each barrier.
 #include <algorithm>
 
 #include "attn_common.hpp"
@@ -40,8 +49,15 @@ typedef __attribute__((address_space(3))) v2i* lds_v2i;
 
 constexpr int kLatThreads = 256;
 constexpr int kLatGroups = 256;               // most workgroups of a split launch: one a CU (LDS, registers)
-constexpr int kLatItemCost = 3;               // what an item's queries and results cost, in tiles
-constexpr int kLatItems = 512;                // most items of a split launch: beyond, they fill the chip
+// What an item's queries and results cost, in tiles: 64 requests of 128 heads take 80.1 us if shares
+// count 2 for them, 76.8 with 3, 77.8 with 4, and 12 us more with none.
+constexpr int kLatItemCost = 3;
+// Items of a split launch are fewer than this, by the bound that the host knows; as many fill the chip.
+// 600 of 300 requests of 128 heads over 512 to 8192 tokens take 347 us split and 495 if not, 1008 by the
+// bound of 24 requests with 1 to 60 new tokens 59 and 90; but 1600 of 8 requests with 100 new tokens each
+// 239 and 189, as a split item's tiles are all of its request's, also those that its rows do not see, and
+// 700 of a tile or two 30 and 24.
+constexpr int kLatItems = 1024;
 constexpr int kLatTile = 64;                  // tokens of a tile
 constexpr int kLatCodes = kLatTile * kLatent; // its bytes of codes and of rotated keys
 constexpr int kLatStage = kLatCodes + kLatTile * kLatentRope * 2;
@@ -220,13 +236,18 @@ struct LatentLds {
     float* refs;                                     // [row half][token half][2][64 lanes] references, norms
 };
 
-// One workgroup's way through its units.  Its four waves form weights two by two, each for 32 rows and half tg of a tile's tokens, trade them through LDS, and each sums its rows' values
-// over all of the tile's tokens for its share of the dims:
+// One workgroup's way through its tiles.  Its four waves form weights two by two, each for 32 rows and
+// half tg of a tile's tokens, trade them through LDS, and each sums its rows' values over all of the
+// tile's tokens for its share of the dims:
 //   RW == 2 (64 rows): wave (rg, x) has 32 rows, token half x and dim half x.
 //   RW == 1 (32 rows): wave x has all rows, token half x & 1 and dim quarter x; two waves form the
 //     same weights, which is work twice done, but with so few rows the cache's bytes are what counts.
 // (A wave with 32 rows and all dims would keep 256 registers of O next to 144 of q, which the compiler
-// does not manage without spills.)
+// does not manage without spills.  Eight waves of 256 registers, which share the dims of the logits as
+// well and widen each code once for 64 rows, take 87 us where these take 77: a second exchange for each
+// tile, and twice as many waves to read all weights.)
+// A wave alone on its SIMD issues an instruction every five cycles and a matrix instruction takes 32, so
+// the four conversions that each needs stand before it or after it, not eight of them before two.
 template <int RW>
 struct LatentWalk {
     static constexpr int DT = RW == 2 ? 8 : 4;       // blocks of 32 dims of a wave
@@ -824,8 +845,10 @@ __global__ __launch_bounds__(64 * WAVES) void attn_latent_join_kernel(LatentArgs
         a.lse[t * a.heads + j] = l == 0.f ? neg_inf() : (m + __builtin_log2f(l)) * kLn2;
 }
 
-// How a launch divides its rows: the waves of a workgroup that have rows of their own, and the row
-// tiles of a request.
+// How a launch divides its rows: the 32-row groups of a workgroup, and the row tiles of a request.  With
+// one group where a request's rows are no more (64 requests of 16 heads: 39 us, and 47 with two), with two
+// otherwise (128 heads: 84 us, and 117 with one; only where the tokens are few, too, one is ahead: 24
+// requests of 60 rows over 100 to 6000 tokens 24 us, and 26 with two).
 struct LatentPlan {
     int rw;
     int64_t row_tiles;

@@ -92,11 +92,12 @@ def test_more_requests_than_lanes(H):
     _case(41, kv, new, H, 64, workspace=False)
 
 
-def test_more_items_than_a_split_launch_takes():
+@pytest.mark.parametrize("R", [700, 1023, 1024])
+def test_about_as_many_items_as_a_split_launch_takes(R):
     rng = np.random.default_rng(50)
-    new = [int(x) for x in rng.integers(0, 2, 700)]
+    new = [int(x) for x in rng.integers(0, 2, R)]
     kv = [n + int(rng.integers(0, 90)) if n else 0 for n in new]
-    assert bfp8.bfp8_attn_latent_workspace_size(700, 1, 16) == 0
+    assert (bfp8.bfp8_attn_latent_workspace_size(R, 1, 16) == 0) == (R >= 1024)
     _case(50, kv, new, 16, 32)
 
 
