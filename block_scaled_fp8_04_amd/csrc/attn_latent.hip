@@ -630,7 +630,7 @@ struct LatentWalk {
 };
 
 // A split launch's cost is shared evenly by this many workgroups (no share is empty).
-__device__ __forceinline__ int latent_groups(int64_t cost, int rw) {
+__device__ __forceinline__ int latent_groups(int64_t cost) {
     return (int)min(cost, (int64_t)kLatGroups);
 }
 // Where workgroup w's share begins, and the workgroup whose share holds position `at`.
@@ -727,7 +727,7 @@ __global__ __launch_bounds__(kLatThreads, 1) void attn_latent_split_kernel(Laten
         reqs.load(a, from);
         cost = reqs.scan(cost);
     }
-    const int groups = latent_groups(cost, RW);
+    const int groups = latent_groups(cost);
     if ((int)blockIdx.x >= groups || cost == 0) return;
     const int64_t from = latent_first(cost, groups, blockIdx.x), to = latent_first(cost, groups, blockIdx.x + 1);
     if (a.R > 64) {                                              // back to the requests where it begins

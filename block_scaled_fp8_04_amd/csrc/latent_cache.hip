@@ -4,11 +4,13 @@
 // 644 bytes.  The scale is the token's own, so a token is written without a look at its page and
 // never touched again.
 //
-// append: one wave per token, eight latent elements a lane.
+// append: one wave per two tokens, eight latent elements of each a lane.
 //     y = c * rsqrt(mean c^2 + eps) * w        (or y = c), fp32, not rounded in between
 //     s = 2^ceil(log2(max(amax |y|, 1e-4) / 448)),   code = e4m3_rne(y / s)
-// The lower half's lanes each turn one pair of the key.  17312 tokens take 11.8 us, 2.6 TB/s read and
-// written: 17 waves a SIMD in turn, each a load, two sums over the wave and a store behind one another.
+// Each half of the wave turns one token's key, a pair a lane: an angle's sine and cosine take some 60
+// instructions.  17312 tokens take 11.5 us alone, 9.5 among other calls (3.3 TB/s read and written), where a
+// token a wave took 10.8; nine waves a SIMD in turn, each loads, two sums over the wave and stores behind
+// one another.
 //
 // gather: one wave per eight or four rows: a row's codes are eight a lane, its key eight elements of
 // eight lanes.  194700 rows take 82 us, 4.3 TB/s; 1600 take 6.4: offsets, table, row, one behind the other.
@@ -22,16 +24,25 @@ namespace bfp8 {
 constexpr int kLatentThreads = 256;
 constexpr int kLatentWaves = kLatentThreads / 64;
 
-// Over the 64 lanes, to all of them.
+// Over the 64 lanes, to all of them: lanes of four, of eight, of a row of 16, of two rows, of both halves.
+template <typename F>
+__device__ __forceinline__ uint32_t over_wave(uint32_t x, F join) {
+    x = join(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, true));
+    x = join(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, true));
+    x = join(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xF, 0xF, true));
+    x = join(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x140, 0xF, 0xF, true));
+    const auto rows = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    x = join(rows[0], rows[1]);
+    const auto halves = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    return join(halves[0], halves[1]);
+}
 __device__ __forceinline__ float wave_add(float x) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
-    return x;
+    return __uint_as_float(over_wave(__float_as_uint(x), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
 }
 __device__ __forceinline__ uint32_t wave_most(uint32_t x) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) x = max(x, (uint32_t)__shfl_xor((int)x, d));
-    return x;
+    return over_wave(x, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 
 // Eight bf16 (kVec: 16-byte aligned).
@@ -57,51 +68,58 @@ __global__ __launch_bounds__(kLatentThreads) void latent_append_kernel(
     const int32_t* __restrict__ slot_map, const int32_t* __restrict__ positions,
     const float* __restrict__ inv_freq, int interleaved, float amplitude, int64_t T,
     uint8_t* __restrict__ codes, float* __restrict__ scales, uint16_t* __restrict__ rope, int64_t slots) {
-    const int lane = threadIdx.x & 63, pair = lane & 31;
-    const int64_t t = (int64_t)blockIdx.x * kLatentWaves + (threadIdx.x >> 6);
-    if (t >= T) return;
-    const int64_t slot = slot_map[t];
-    if (slot < 0 || slot >= slots) return;
-    const uint16_t* const row = kv + t * kv_ts;
-    float y[8], w[8];
-    widen8_bf16<kVec>(row + 8 * lane, y);
+    const int lane = threadIdx.x & 63, pair = lane & 31, half = lane >> 5;
+    const int64_t t0 = ((int64_t)blockIdx.x * kLatentWaves + (threadIdx.x >> 6)) * 2;
+    if (t0 >= T) return;
+    const int64_t t[2] = {t0, min(t0 + 1, T - 1)}, slot[2] = {slot_map[t0], t0 + 1 < T ? slot_map[t0 + 1] : -1};
+    float y[2][8], w[8];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) widen8_bf16<kVec>(kv + t[j] * kv_ts + 8 * lane, y[j]);
     if (norm_weight) widen8_bf16<kVec>(norm_weight + 8 * lane, w);
-    // both halves of the wave turn the key, the lower one stores it
+    // each half of the wave turns a token's key
+    const uint16_t* const key = kv + (half ? t[1] : t[0]) * kv_ts + kLatent;
     const int i0 = interleaved ? 2 * pair : pair, i1 = interleaved ? 2 * pair + 1 : pair + kLatentRope / 2;
-    const float a = bf16_lo(row[kLatent + i0]), b = bf16_lo(row[kLatent + i1]);
-    const float2 cs = rotary(positions[t], inv_freq[pair], amplitude);
+    const float a = bf16_lo(key[i0]), b = bf16_lo(key[i1]);
+    const float2 cs = rotary(positions[half ? t[1] : t[0]], inv_freq[pair], amplitude);
     const float r0 = __builtin_fmaf(a, cs.x, -b * cs.y), r1 = __builtin_fmaf(a, cs.y, b * cs.x);
-    if (norm_weight) {
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(y[i], y[i], sum);
-        const float f = 1.f / __builtin_sqrtf(wave_add(sum) * (1.f / kLatent) + eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = y[i] * f * w[i];
-    }
-    // by bit patterns: infinities and NaN are the largest
-    uint32_t most = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(y[i]) & 0x7FFFFFFFu);
-    most = wave_most(most);
     const uint32_t rot = pack_bf16x2(r0, r1);
-    const bool odd = (rot & 0x7F80u) == 0x7F80u || (rot >> 16 & 0x7F80u) == 0x7F80u;
-    // not finite, or 2^127 and more: codes times the scale would pass bf16
-    const bool bad = most >= 0x7F000000u || __any(odd);
-    const float s = pow2_scale(__uint_as_float(most));
-    const float inv = __uint_as_float((254u << 23) - __float_as_uint(s));
-    uint2 q = make_uint2(e4m3_encode4<true>(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                         e4m3_encode4<true>(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
-    if (bad) q = make_uint2(0, 0);
-    *(uint2*)(codes + slot * kLatent + 8 * lane) = q;
-    if (lane == 0) scales[slot] = bad ? __uint_as_float(0x7FC00000u) : s;
-    if (lane < 32) {
-        uint16_t* const to = rope + slot * kLatentRope;
+    const uint64_t odd = __ballot((rot & 0x7F80u) == 0x7F80u || (rot >> 16 & 0x7F80u) == 0x7F80u);
+    bool bad[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if (norm_weight) {
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(y[j][i], y[j][i], sum);
+            const float f = 1.f / __builtin_sqrtf(wave_add(sum) * (1.f / kLatent) + eps);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[j][i] = y[j][i] * f * w[i];
+        }
+        // by bit patterns: infinities and NaN are the largest
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(y[j][i]) & 0x7FFFFFFFu);
+        most = wave_most(most);
+        // not finite, or 2^127 and more: codes times the scale would pass bf16
+        bad[j] = most >= 0x7F000000u || (uint32_t)(odd >> 32 * j) != 0;
+        if (slot[j] < 0 || slot[j] >= slots) continue;
+        const float s = pow2_scale(__uint_as_float(most));
+        const float inv = __uint_as_float((254u << 23) - __float_as_uint(s));
+        uint2 q = make_uint2(e4m3_encode4<true>(y[j][0] * inv, y[j][1] * inv, y[j][2] * inv, y[j][3] * inv),
+                             e4m3_encode4<true>(y[j][4] * inv, y[j][5] * inv, y[j][6] * inv, y[j][7] * inv));
+        if (bad[j]) q = make_uint2(0, 0);
+        *(uint2*)(codes + slot[j] * kLatent + 8 * lane) = q;
+        if (lane == 0) scales[slot[j]] = bad[j] ? __uint_as_float(0x7FC00000u) : s;
+    }
+    const int64_t mine = half ? slot[1] : slot[0];
+    if (mine >= 0 && mine < slots) {
+        const bool none = half ? bad[1] : bad[0];
+        uint16_t* const to = rope + mine * kLatentRope;
         if (interleaved) {
-            *(uint32_t*)(to + i0) = bad ? 0u : rot;
+            *(uint32_t*)(to + i0) = none ? 0u : rot;
         } else {
-            to[i0] = bad ? 0 : (uint16_t)rot;
-            to[i1] = bad ? 0 : (uint16_t)(rot >> 16);
+            to[i0] = none ? 0 : (uint16_t)rot;
+            to[i1] = none ? 0 : (uint16_t)(rot >> 16);
         }
     }
 }
@@ -112,7 +130,7 @@ hipError_t launch_latent_append(const void* kv, int64_t kv_ts, const void* norm_
                                 void* codes, float* scales, void* rope, int64_t slots,
                                 hipStream_t stream) {
     const bool vec = ((uintptr_t)kv | (uintptr_t)norm_weight) % 16 == 0 && kv_ts % 8 == 0;
-    const unsigned grid = (unsigned)((T + kLatentWaves - 1) / kLatentWaves);
+    const unsigned grid = (unsigned)((T + 2 * kLatentWaves - 1) / (2 * kLatentWaves));
     hipLaunchKernelGGL(vec ? latent_append_kernel<true> : latent_append_kernel<false>, dim3(grid), dim3(kLatentThreads),
                        0, stream, (const uint16_t*)kv, kv_ts, (const uint16_t*)norm_weight, eps, slot_map, positions,
                        inv_freq, (int)interleaved, amplitude, T, (uint8_t*)codes, scales, (uint16_t*)rope, slots);
