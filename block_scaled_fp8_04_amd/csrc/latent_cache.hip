@@ -186,11 +186,11 @@ __global__ __launch_bounds__(kLatentThreads) void latent_gather_kernel(GatherArg
         }
         if (lane == j) r = from + before;
     }
-    // where it lies in the pool, -1 for nowhere
+    // where it lies in the pool, -1 for nowhere: rows in front of the first request have its number, too
     int64_t at = -1;
     if (r < a.R && row0 + lane < a.rows) {
-        const int64_t pos = row0 + lane - a.row_offsets[r] + (a.starts ? a.starts[r] : 0);
-        if (pos >= 0 && pos < a.width << a.log_b) {
+        const int64_t in = row0 + lane - a.row_offsets[r], pos = in + (a.starts ? a.starts[r] : 0);
+        if (in >= 0 && pos >= 0 && pos < a.width << a.log_b) {
             const int64_t page = a.block_table[r * a.width + (pos >> a.log_b)];
             at = min(max(page, (int64_t)0), a.pages - 1) << a.log_b | (pos & ((1 << a.log_b) - 1));
         }

@@ -566,8 +566,8 @@ int bfp8_latent_append(const void* kv_bf16, int64_t kv_token_stride, const void*
  * prompt's chunks: rows row_offsets[r] .. row_offsets[r+1] - 1 are request r's tokens
  * from starts[r] on (from its first one if starts is NULL),
  *     latent_out[row] = bf16(code * scale)   (exact),   rope_out[row] = the rotated dims
- *   row_offsets : DEVICE int32 [R+1], ascending; rows past `rows` or past
- *                 row_offsets[R], and of tokens past the table's width, are not written
+ *   row_offsets : DEVICE int32 [R+1], ascending; rows before row_offsets[0], past `rows` or
+ *                 past row_offsets[R], and of tokens past the table's width, are not written
  *   starts      : DEVICE int32 [R], or NULL
  *   latent_out  : bf16 [rows, 512] at a row stride, 16-byte aligned; rope_out likewise [rows, 64]
  * Table entries are clamped into the pool.  A token stored as not finite gives NaN latents.
