@@ -640,10 +640,10 @@ def bfp8_attn_paged(q, k_cache, k_scales, v_cache, v_scales, block_table, q_offs
 def rope_frequencies(dim, base=10000.0, factor=1.0, trained_len=4096, fast=32.0, slow=1.0, device="cuda"):
     """Inverse frequencies fp32 [dim / 2] of rotary positions, and the amplitude that goes with them.
 
-    factor > 1 stretches a model trained on trained_len tokens to factor times as many: a pair that
-    makes fewer than `slow` turns in trained_len has its frequency divided by factor, one that makes
-    more than `fast` keeps it, in between they are mixed linearly over the pair's number; the
-    amplitude is 0.1 ln(factor) + 1 (1 without scaling)."""
+    factor > 1 stretches a model trained on trained_len tokens to factor times as many, by the YaRN
+    method: a pair that makes fewer than `slow` turns in trained_len has its frequency divided by
+    factor, one that makes more than `fast` keeps it, in between they are mixed linearly over the
+    pair's number; the amplitude is 0.1 ln(factor) + 1 (1 without scaling)."""
     _need(dim >= 2 and dim % 2 == 0, "dim must be even")
     _need(factor >= 1.0 and trained_len > 0 and fast >= slow > 0 and base > 1.0,
           "factor >= 1, trained_len > 0, fast >= slow > 0 and base > 1")
@@ -654,8 +654,10 @@ def rope_frequencies(dim, base=10000.0, factor=1.0, trained_len=4096, fast=32.0,
 
     def pair_with(turns):                  # the pair that makes this many turns, as a real number
         return dim * math.log(trained_len / (turns * 2 * math.pi)) / (2 * math.log(base))
-    lo, hi = max(math.floor(pair_with(fast)), 0), min(math.ceil(pair_with(slow)), dim // 2 - 1)
-    stretched = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+    # the ends of the mixed pairs, as the method has them; below 0, every pair is divided
+    lo, hi = max(math.floor(pair_with(fast)), 0), min(math.ceil(pair_with(slow)), dim - 1)
+    lo = min(lo, hi - 1)
+    stretched = ((i - lo) / (hi - lo)).clamp(0, 1)
     freq = freq / factor * stretched + freq * (1 - stretched)
     return freq.to(device, torch.float32), 0.1 * math.log(factor) + 1.0
 
