@@ -91,7 +91,23 @@ __global__ __launch_bounds__(kLatentThreads) void latent_append_kernel(
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(y[j][i], y[j][i], sum);
-            const float f = 1.f / __builtin_sqrtf(wave_add(sum) * (1.f / kLatent) + eps);
+            float mean = wave_add(sum) * (1.f / kLatent) + eps;
+            // squares that may have left fp32's range: those of the row over a power of two near its largest
+            // element, or near eps's root.  (of all lanes, like the sum; NaN stays NaN, infinity becomes it)
+            if (!(mean >= 0x1p-90f && mean <= 0x1p120f)) {
+                uint32_t top = __float_as_uint(__builtin_sqrtf(eps));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(y[j][i]) & 0x7FFFFFFFu);
+                const int down = 127 - (int)(wave_most(top) >> 23);
+                sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    y[j][i] = __builtin_ldexpf(y[j][i], down);
+                    sum = __builtin_fmaf(y[j][i], y[j][i], sum);
+                }
+                mean = wave_add(sum) * (1.f / kLatent) + __builtin_ldexpf(eps, 2 * down);
+            }
+            const float f = 1.f / __builtin_sqrtf(mean);
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[j][i] = y[j][i] * f * w[i];
         }
