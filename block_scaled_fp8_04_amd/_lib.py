@@ -721,7 +721,7 @@ def bfp8_latent_append(kv, slot_map, positions, inv_freq, latent_cache, latent_s
                        norm_weight=None, eps=1e-6, interleaved=True, amplitude=1.0, stream=None):
     """Rows kv bf16 [T, 576] (any token stride) into the slots of slot_map int32 [T] (in place): the
     first 512 dims normed by norm_weight bf16 [512] (None: as they are) and quantized, the last 64
-    rotated as by bfp8_rope at positions int32 [T]."""
+    rotated as by bfp8_rope at positions int32 [T] (negative: the token is skipped)."""
     gpu = kv.get_device()
     _need(gpu >= 0, "all tensors must be on the GPU")
     P, B = _latent_shape(gpu, latent_cache, latent_scales, rope_cache)

@@ -71,7 +71,10 @@ __global__ __launch_bounds__(kLatentThreads) void latent_append_kernel(
     const int lane = threadIdx.x & 63, pair = lane & 31, half = lane >> 5;
     const int64_t t0 = ((int64_t)blockIdx.x * kLatentWaves + (threadIdx.x >> 6)) * 2;
     if (t0 >= T) return;
-    const int64_t t[2] = {t0, min(t0 + 1, T - 1)}, slot[2] = {slot_map[t0], t0 + 1 < T ? slot_map[t0 + 1] : -1};
+    const int64_t t[2] = {t0, min(t0 + 1, T - 1)};
+    const int at[2] = {positions[t[0]], positions[t[1]]};
+    // a token without a position is skipped, as one without a slot
+    const int64_t slot[2] = {at[0] < 0 ? -1 : slot_map[t0], t0 + 1 == T || at[1] < 0 ? -1 : slot_map[t[1]]};
     float y[2][8], w[8];
 #pragma unroll
     for (int j = 0; j < 2; ++j) widen8_bf16<kVec>(kv + t[j] * kv_ts + 8 * lane, y[j]);
@@ -80,7 +83,7 @@ __global__ __launch_bounds__(kLatentThreads) void latent_append_kernel(
     const uint16_t* const key = kv + (half ? t[1] : t[0]) * kv_ts + kLatent;
     const int i0 = interleaved ? 2 * pair : pair, i1 = interleaved ? 2 * pair + 1 : pair + kLatentRope / 2;
     const float a = bf16_lo(key[i0]), b = bf16_lo(key[i1]);
-    const float2 cs = rotary(positions[half ? t[1] : t[0]], inv_freq[pair], amplitude);
+    const float2 cs = rotary(half ? at[1] : at[0], inv_freq[pair], amplitude);
     const float r0 = __builtin_fmaf(a, cs.x, -b * cs.y), r1 = __builtin_fmaf(a, cs.y, b * cs.x);
     const uint32_t rot = pack_bf16x2(r0, r1);
     const uint64_t odd = __ballot((rot & 0x7F80u) == 0x7F80u || (rot >> 16 & 0x7F80u) == 0x7F80u);

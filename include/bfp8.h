@@ -550,8 +550,9 @@ int bfp8_rope(const void* x_bf16, int64_t x_token_stride, int64_t x_head_stride,
  *   norm_weight : DEVICE bf16 [512], or NULL
  *   slot_map    : DEVICE int32 [T]; a slot outside [0, num_pages * page_size) is
  *                 skipped, a slot named twice holds either token's parts
- *   positions   : DEVICE int32 [T], inv_freq : DEVICE fp32 [32], interleaved and
- *                 amplitude as for bfp8_rope
+ *   positions   : DEVICE int32 [T]; a token whose position is negative is skipped (its
+ *                 slot keeps what it holds)
+ *   inv_freq    : DEVICE fp32 [32], interleaved and amplitude as for bfp8_rope
  *   latent_cache, rope_cache : 16-byte aligned; latent_scales : 4-byte aligned
  * Errors: BFP8_ERR_SHAPE if T < 0, T >= 2^26, kv_token_stride < 0, num_pages < 0 or
  * num_pages * page_size >= 2^31; BFP8_ERR_ARG if page_size is not 32, 64 or 128, or eps

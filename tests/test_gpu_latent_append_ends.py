@@ -50,3 +50,19 @@ def test_rows_that_are_not_finite_stay_poisoned():
     kv = torch.zeros_like(kv)
     run_append(kv, [1, 2, 3], [0, 0, 0], freq(64), cache, norm_weight=weight, eps=0.0)
     assert torch.isnan(cache[1][0, 1:4]).all() and (cache[0][0, 1:4] == 0).all()
+
+
+@pytest.mark.parametrize("T", [1, 2, 9])
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_tokens_without_a_position_are_skipped(T, interleaved):
+    """As by bfp8_rope; their slots keep what they hold, and their neighbours are stored."""
+    rng = np.random.default_rng(63 + T)
+    for gone in range(min(T, 3)):
+        kv = bf16(rng.standard_normal((T, 576)))
+        slots, pos = rng.permutation(32)[:T], rng.integers(0, 9999, T)
+        pos[gone] = (-1, -2 ** 31, -77)[gone]
+        cache = pool(1, 32, rng)
+        before = [x.clone() for x in cache]
+        run_append(kv, slots, pos, freq(64), cache, interleaved=interleaved)
+        kept = np.where(pos < 0, -1, slots)
+        check_append(kv, kept, pos, freq(64), before, cache, interleaved, 1.0, None, 1e-6)
