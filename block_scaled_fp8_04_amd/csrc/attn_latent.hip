@@ -471,14 +471,15 @@ struct LatentWalk {
     // Weights of 32 tokens against the reference m, and their share of the norm.
     __device__ __forceinline__ void weights(const v16f& s, const v4f (&tokens)[8], h8v (&w)[2]) {
         const float ref = m == neg_inf() ? 0.f : m;
-        float sum[4] = {l, 0.f, 0.f, 0.f};
+        // summed up before they meet l: one by one, weights under its last step would be lost
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const float y = __builtin_amdgcn_exp2f(s[i] - ref);
             sum[i & 3] = __builtin_fmaf(y, tokens[i >> 1][2 * (i & 1) + 1], sum[i & 3]);
             w[i >> 3][i & 7] = (_Float16)y;
         }
-        l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
 
     // Codes of a tile as values: read n is of 16 tokens (n / DT) and 32 dims (n % DT), 8 tokens of a dim a

@@ -1,0 +1,56 @@
+"""Weights of bfp8_attn_latent that lie far below the largest: what they lose is bounded, however many tokens
+there are, and wherever in a tile they stand."""
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_fp8_04_amd as bfp8
+from gpu_helpers import announce, dev
+from kv_helpers import f64, i32
+
+pytestmark = pytest.mark.gpu
+
+ONE, MOST = 0x38, 0x7E                                     # codes of 1 and of 448
+
+
+def attend(x, codes, scales, H, workspace, what):
+    """One query row for H heads whose logits are x (exact in bf16), over tokens whose 512 codes are all
+    codes[t]; returns the output as one number, and lse, of heads that are all alike."""
+    n, B = len(x), 128
+    pages = -(-n // B)
+    cache = bfp8.latent_cache_buffers(pages, B, dev())
+    cache[0].fill_(0x7F)
+    cache[1].fill_(float("nan"))
+    cache[2].fill_(float("nan"))
+    cache[0].flatten(0, 1)[:n] = torch.from_numpy(np.asarray(codes, np.uint8)).to(dev())[:, None]
+    cache[1].flatten()[:n] = torch.from_numpy(np.asarray(scales, np.float32)).to(dev())
+    cache[2].flatten(0, 1)[:n] = 0
+    cache[2].flatten(0, 1)[:n, 0] = torch.from_numpy(np.asarray(x, np.float32)).to(dev()).bfloat16()
+    assert np.array_equal(f64(cache[2].flatten(0, 1)[:n, 0]), x)
+    ql = torch.zeros(1, H, 512, dtype=torch.bfloat16, device=dev())
+    qr = torch.zeros(1, H, 64, dtype=torch.bfloat16, device=dev())
+    qr[..., 0] = 1
+    out, lse = torch.empty_like(ql), torch.empty(1, H, device=dev())
+    ws = bfp8.attn_latent_workspace(1, 1, H, dev()) if workspace else None
+    announce(f"latent weights {what} n={n} H={H} ws={workspace}")
+    bfp8.bfp8_attn_latent(ql, qr, *cache, i32([range(pages)]), i32([0, 1]), i32([n]), 1, 1.0, out, lse, ws)
+    torch.cuda.synchronize()
+    assert (out == out[0, 0, 0]).all() and (lse == lse[0, 0]).all()
+    return float(out[0, 0, 0]), float(lse[0, 0])
+
+
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("workspace", [False, True])
+@pytest.mark.parametrize("top", [16.0, 16.75, 17.25])
+def test_lse_of_one_token_above_a_long_tail(H, workspace, top):
+    """131071 tokens at 2^-23 to 2^-24.9 of the largest.  The fp32 exponent and its power are off by 2^-22 of
+    their size, top log2 e and one, together, the logarithm by 2^-23 of the result; 2048 tiles' sums are added
+    one after another, each rounded by 2^-25 at most of a sum that is between 1/2 and 1: 2^-13 of it."""
+    n = 131072
+    x = np.zeros(n)
+    x[70] = top
+    _, lse = attend(x, [ONE] * n, [1.0] * n, H, workspace, f"norm, top {top}")
+    want = top + np.log1p((n - 1) * np.exp(-top))
+    bound = 2.0 ** -22 * (top * 1.5 + 1) + 2.0 ** -23 * want + 2.0 ** -13
+    announce(f"lse {lse:.8g} want {want:.8g} bound {bound:.3g}")
+    assert abs(lse - want) <= bound
