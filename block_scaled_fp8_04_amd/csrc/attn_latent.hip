@@ -460,7 +460,7 @@ struct LatentWalk {
 #pragma unroll
         for (int i = 0; i < 4; ++i) top[i] = fmaxf(fmaxf(s[i], s[i + 4]), fmaxf(s[i + 8], s[i + 12]));
         const float x = __builtin_ceilf(half_max(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]))));
-        return x > m + kLatSlack ? x : m;
+        return x - m > kLatSlack ? x : m;                        // (m + slack may be rounded up)
     }
 
     // 2^(from - to) for references; 0 where there was none.

@@ -6,7 +6,7 @@ import torch
 
 import block_scaled_fp8_04_amd as bfp8
 from gpu_helpers import announce, dev
-from kv_helpers import f64, i32
+from kv_helpers import i32
 
 pytestmark = pytest.mark.gpu
 
@@ -14,8 +14,8 @@ ONE, MOST = 0x38, 0x7E                                     # codes of 1 and of 4
 
 
 def attend(x, codes, scales, H, workspace, what):
-    """One query row for H heads whose logits are x (exact in bf16), over tokens whose 512 codes are all
-    codes[t]; returns the output as one number, and lse, of heads that are all alike."""
+    """One query row for H heads whose logits are x (sums of three bf16 at most), over tokens whose 512 codes
+    are all codes[t]; returns the output as one number, and lse, of heads that are all alike."""
     n, B = len(x), 128
     pages = -(-n // B)
     cache = bfp8.latent_cache_buffers(pages, B, dev())
@@ -25,11 +25,15 @@ def attend(x, codes, scales, H, workspace, what):
     cache[0].flatten(0, 1)[:n] = torch.from_numpy(np.asarray(codes, np.uint8)).to(dev())[:, None]
     cache[1].flatten()[:n] = torch.from_numpy(np.asarray(scales, np.float32)).to(dev())
     cache[2].flatten(0, 1)[:n] = 0
-    cache[2].flatten(0, 1)[:n, 0] = torch.from_numpy(np.asarray(x, np.float32)).to(dev()).bfloat16()
-    assert np.array_equal(f64(cache[2].flatten(0, 1)[:n, 0]), x)
+    left = torch.from_numpy(np.asarray(x, np.float64))
+    for d in range(3):
+        part = left.bfloat16()
+        cache[2].flatten(0, 1)[:n, d] = part.to(dev())
+        left = left - part.double()
+    assert (left == 0).all()
     ql = torch.zeros(1, H, 512, dtype=torch.bfloat16, device=dev())
     qr = torch.zeros(1, H, 64, dtype=torch.bfloat16, device=dev())
-    qr[..., 0] = 1
+    qr[..., :3] = 1
     out, lse = torch.empty_like(ql), torch.empty(1, H, device=dev())
     ws = bfp8.attn_latent_workspace(1, 1, H, dev()) if workspace else None
     announce(f"latent weights {what} n={n} H={H} ws={workspace}")
@@ -54,3 +58,21 @@ def test_lse_of_one_token_above_a_long_tail(H, workspace, top):
     bound = 2.0 ** -22 * (top * 1.5 + 1) + 2.0 ** -23 * want + 2.0 ** -13
     announce(f"lse {lse:.8g} want {want:.8g} bound {bound:.3g}")
     assert abs(lse - want) <= bound
+
+
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("exponent", [23, 24, 25, 26, 27, 28, 30, 40, 100])
+def test_far_logits_that_grow(H, exponent):
+    """Logits whose steps are 1 and more: neighbours are 2^16 and more apart, whatever the reference is rounded
+    to.  All values are 1, so the output is 1 but for its own rounding, and lse off by the rounding of the
+    logits' product and power, 2^-22 of their size."""
+    rng = np.random.default_rng(exponent)
+    step = 2.0 ** (exponent - 23)                           # fp32's there
+    for sign in (1, -1):
+        for _ in range(4):
+            # a few steps up from tile to tile, and within one
+            x = sign * 2.0 ** exponent + step * (np.repeat(np.cumsum(rng.integers(0, 4, 10)), 64) + rng.integers(0, 3, 640))
+            x = x[:rng.integers(1, 640)]
+            out, lse = attend(x, [ONE] * len(x), [1.0] * len(x), H, False, f"far {sign} 2^{exponent}")
+            assert out == 1.0
+            assert abs(lse - x.max()) <= 2.0 ** -22 * 1.5 * np.abs(x).max() + np.log(len(x))
