@@ -17,10 +17,11 @@
 //
 // Precision.  As keys, codes are widened to bf16 with their token's scale, exactly, and q is bf16 as
 // it comes.  As values they are widened to fp16 without it, exactly as well, and the scale goes into
-// the weight: the maximum is taken over x_t + e_t (in units of log 2), w_t = 2^(x_t + e_t - max) is
+// the weight: the maximum is taken over x_t + e_t (in units of log 2), w_t = 2^(x_t + e_t - reference) is
 // rounded to fp16 once (2^-11 of it, where a bf16 weight would lose 2^-8, as much as the rounding of
 // the output), and the norm sums w_t 2^-e_t before that rounding.  So a weight's size is that of the
-// token's contribution, and fp16's range is enough: what it drops is 2^-25 of the largest
+// token's contribution, and as the reference lies 2^7 below the largest, all of fp16's range is used: below
+// its normal numbers a weight loses 2^-31 of the largest
 // contribution.  Logits, maxima, norms and sums are fp32; maxima are rounded up to integers, so that
 // rescaling by 2^(old - new) is exact.  (The fp8 matrix product would take the codes as they are, but it
 // drops what lies 13 bits below the largest product it adds: 2^-12.3 of the sum of their sizes, measured.)
@@ -61,9 +62,12 @@ constexpr int kLatItems = 1024;
 constexpr int kLatTile = 64;                  // tokens of a tile
 constexpr int kLatCodes = kLatTile * kLatent; // its bytes of codes and of rotated keys
 constexpr int kLatStage = kLatCodes + kLatTile * kLatentRope * 2;
-// A maximum is followed only where it would be passed by more than this (in units of log 2): weights
-// reach 2^8, far inside fp16's range.
-constexpr float kLatSlack = 8.f;
+// A row's reference is the largest exponent of two that it met, rounded up, less kLatRise, and follows a
+// larger one only where that is more than kLatSlack away.  So weights reach 2^14, and the largest is 2^6 or
+// more: fp16's last step, 2^-24, is 2^-30 of it or less.  (Where fp32's steps are 2 or 4, the difference may
+// come out as 8, or nothing: 2^15, which fp16 holds.)
+constexpr float kLatRise = 7.f;
+constexpr float kLatSlack = 7.f;
 
 // The permutation of a row's 16-byte chunks in LDS: chunk c of row r lies at c ^ lat_swz(r).  Key
 // reads take the same chunk of 16 rows, all different here; transposing reads take two neighbouring
@@ -459,7 +463,7 @@ struct LatentWalk {
         float top[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) top[i] = fmaxf(fmaxf(s[i], s[i + 4]), fmaxf(s[i + 8], s[i + 12]));
-        const float x = __builtin_ceilf(half_max(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]))));
+        const float x = __builtin_ceilf(half_max(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])))) - kLatRise;
         return x - m > kLatSlack ? x : m;                        // (m + slack may be rounded up)
     }
 

@@ -7,6 +7,7 @@ import torch
 import block_scaled_fp8_04_amd as bfp8
 from gpu_helpers import announce, dev
 from kv_helpers import i32
+from kv_reference import VALUES
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +77,43 @@ def test_far_logits_that_grow(H, exponent):
             out, lse = attend(x, [ONE] * len(x), [1.0] * len(x), H, False, f"far {sign} 2^{exponent}")
             assert out == 1.0
             assert abs(lse - x.max()) <= 2.0 ** -22 * 1.5 * np.abs(x).max() + np.log(len(x))
+
+
+def check(x, codes, scales, H, workspace, what):
+    """Against 64 bits.  Counted: the output's rounding, 2^-8 of it; a weight's rounding to fp16, 2^-11 of
+    it; a logit's x log2 e + e_t and its power in fp32, 2^-22 of their size and 2^-22; and three halves of
+    fp16's last step, 2^-24, below its normal range (a weight's rounding, and twice when two halves of a
+    tile are brought to one reference), where the largest weight is 2^6 or more: 2^-29 of the largest
+    contribution for a token's code."""
+    x, v, s = np.asarray(x, np.float64), VALUES[np.asarray(codes)], np.asarray(scales, np.float64)
+    p = np.exp(x - x.max())
+    norm = p.sum()
+    want, want_lse = (p * v * s).sum() / norm, x.max() + np.log(norm)
+    slack = 2.0 ** -22 * (1.5 * np.abs(x).max() + 33)
+    bound = 2.0 ** -8 * abs(want) + (2.0 ** -11 + 2 * slack) * (p * np.abs(v) * s).sum() / norm + \
+        2.0 ** -29 * (p * s).max() * np.abs(v).sum() / norm
+    out, lse = attend(x, codes, scales, H, workspace, what)
+    announce(f"got {out:.6g} want {want:.6g} bound {bound:.3g}, lse {lse:.7g} want {want_lse:.7g}")
+    assert abs(out - want) <= bound, (out, want, bound)
+    # a sum of n fp32 in chains of n / 32 and less, and the logarithm
+    assert abs(lse - want_lse) <= slack + 2.0 ** -21 * (1 + abs(want_lse)) + 2.0 ** -24 * np.sqrt(len(x))
+
+
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("workspace", [False, True])
+def test_one_token_above_a_long_tail(H, workspace):
+    """131071 tokens at 2^-24.2 of the largest hold 0.7 % of the sum."""
+    n = 131072
+    x = np.zeros(n)
+    x[70] = 16.75
+    check(x, [ONE] * n, [1.0] * n, H, workspace, "tail")
+
+
+@pytest.mark.parametrize("H", [16, 64])
+def test_a_tail_of_many_sizes(H):
+    """Weights from 2^-20 to 2^-27 of the largest, values of one sign."""
+    rng = np.random.default_rng(71)
+    n = 100003
+    x = rng.integers(-150, -110, n) / 8.0
+    x[n // 2] = 0
+    check(x, rng.integers(ONE, MOST, n), 2.0 ** rng.integers(-1, 2, n), H, False, "sizes")
