@@ -472,6 +472,16 @@ struct LatentWalk {
         return from == neg_inf() ? 0.f : __builtin_amdgcn_exp2f(from - to);
     }
 
+    // Weights against `from` as weights against `to`, in two steps: one fp16 factor ends at 2^-24, where a
+    // weight of 2^14 still is 2^-10.
+    static __device__ __forceinline__ void lower(h8v& x, h8v& y, float from, float to) {
+        const float d = from == neg_inf() ? -64.f : from - to;   // (or all is 0)
+        const _Float16 a = (_Float16)__builtin_amdgcn_exp2f(fmaxf(d, -14.f));
+        const _Float16 b = (_Float16)__builtin_amdgcn_exp2f(fminf(d + 14.f, 0.f));
+        x = x * a * b;
+        y = y * a * b;
+    }
+
     // Weights of 32 tokens against the reference m, and their share of the norm.
     __device__ __forceinline__ void weights(const v16f& s, const v4f (&tokens)[8], h8v (&w)[2]) {
         const float ref = m == neg_inf() ? 0.f : m;
@@ -567,11 +577,9 @@ struct LatentWalk {
         for (int x = 0; x < 4; ++x) w[x] = __builtin_bit_cast(h8v, lds.trade[first + 64 * x]);
         // the rows' reference is that of O in all waves: the larger of the two
         if (__any(m0 != m1 || m0 != before)) {
-            const float top = fmaxf(m0, m1), f0 = shrink(m0, top), f1 = shrink(m1, top), alpha = shrink(before, top);
-            w[0] *= (_Float16)f0;
-            w[1] *= (_Float16)f0;
-            w[2] *= (_Float16)f1;
-            w[3] *= (_Float16)f1;
+            const float top = fmaxf(m0, m1), alpha = shrink(before, top);
+            lower(w[0], w[1], m0, top);
+            lower(w[2], w[3], m1, top);
 #pragma unroll
             for (int d = 0; d < DT; ++d) o[d] *= alpha;
             l *= m == top ? 1.f : shrink(m, top);

@@ -117,3 +117,18 @@ def test_a_tail_of_many_sizes(H):
     x = rng.integers(-150, -110, n) / 8.0
     x[n // 2] = 0
     check(x, rng.integers(ONE, MOST, n), 2.0 ** rng.integers(-1, 2, n), H, False, "sizes")
+
+
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("leap", [5.5, 15.5, 16.5, 18.5, 22.0, 26.0, 31.0])
+@pytest.mark.parametrize("tall", [0, 1])
+def test_one_half_of_a_tile_leaps(H, leap, tall):
+    """A tile's half leaps up; the other half's tokens, 2^7.94 above the reference so far, keep their
+    share of a sum in which their values are 448 times the tallest token's."""
+    x = np.zeros(192)
+    half = np.arange(64, 128) if tall else np.arange(64, 128)[::-1]
+    x[half[:32]] = 5.5
+    x[half[63]] = leap
+    codes = np.full(192, MOST)
+    codes[half[63]] = ONE
+    check(x, codes, np.ones(192), H, False, f"leap {leap}")
