@@ -547,7 +547,9 @@ struct LatentWalk {
         const int base = tile * kLatTile;
         const int lane = threadIdx.x & 63, pair = (rg * 2 + tg) * 128 + lane, first = rg * 256 + lane;
         clear_tail(st, base);
-        const uint32_t ex = __float_as_uint(sc) >> 23 & 255;     // 255: a token that is not finite
+        // 255: a token that is not finite.  A scale of zero would pass fp32 in the norm: of scales below 2^-90
+        // the values, nothing next to any other, count as if it were that.
+        const uint32_t ex = max(__float_as_uint(sc) >> 23 & 255, 127u - 90u);
         lds.scales[lane] = make_float2(ex == 255 ? __uint_as_float(0x7FC00000u) : (float)((int)ex - 127),
                                        ex == 255 ? 0.f : __uint_as_float((254 - ex) << 23));
         __builtin_amdgcn_wave_barrier();

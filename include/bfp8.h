@@ -506,7 +506,8 @@ size_t bfp8_attn_paged_workspace_size(int64_t R, int64_t max_new, int32_t heads_
  *   latent_cache  : e4m3 [num_pages, B, 512]
  *   latent_scales : fp32 [num_pages, B], a power of two per token
  *   rope_cache    : bf16 [num_pages, B, 64], the rotated dims
- * value = e4m3(code) * scale; of any other scale only the exponent is used.
+ * value = e4m3(code) * scale; of any other scale only the exponent is used (zero
+ * is the smallest one; attention counts those below 2^-90 as 2^-90 for values).
  * Slots behind a request's last token, and pages that no request holds, may
  * hold anything, NaN included.
  * ---------------------------------------------------------------------- */

@@ -132,3 +132,24 @@ def test_one_half_of_a_tile_leaps(H, leap, tall):
     codes = np.full(192, MOST)
     codes[half[63]] = ONE
     check(x, codes, np.ones(192), H, False, f"leap {leap}")
+
+
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("workspace", [False, True])
+@pytest.mark.parametrize("n", [1, 2, 63, 200, 9000])
+def test_a_cache_of_zeros(H, workspace, n):
+    """Scales of zero: values of nothing, and every token counts."""
+    out, lse = attend(np.zeros(n), [0] * n, [0.0] * n, H, workspace, "zeros")
+    assert out == 0 and abs(lse - np.log(n)) <= 2.0 ** -20 * (1 + np.log(n))
+
+
+@pytest.mark.parametrize("H", [16, 64])
+@pytest.mark.parametrize("exponent", [-22, 0, 8, 30])
+def test_zeros_beside_others(H, exponent):
+    """Tokens of scale zero next to one of another scale: they halve, or thin, its share."""
+    for n in (2, 64, 300):
+        scales = np.zeros(n)
+        scales[n - 1] = 2.0 ** exponent
+        codes = np.full(n, 0)
+        codes[n - 1] = ONE
+        check(np.zeros(n), codes, scales, H, False, f"2^{exponent} beside zeros")
