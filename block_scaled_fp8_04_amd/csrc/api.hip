@@ -479,7 +479,7 @@ int bfp8_latent_gather(const void* latent_cache, const float* latent_scales,
 
 static bool latent_sizes_ok(int64_t R, int64_t max_new, int32_t heads) {
     return R >= 0 && max_new >= 0 && heads >= 1 && heads <= 65535 &&
-           max_new < ((int64_t)1 << 31) / heads;
+           max_new < (int64_t)1 << 31 && max_new * heads < (int64_t)1 << 31;
 }
 
 size_t bfp8_attn_latent_workspace_size(int64_t R, int64_t max_new, int32_t heads) {
@@ -497,7 +497,8 @@ int bfp8_attn_latent(const void* q_latent_bf16, int64_t ql_token_stride, int64_t
                      void* out_bf16, int64_t out_token_stride, int64_t out_head_stride, float* lse,
                      void* workspace, size_t workspace_bytes, void* stream) {
     if (!kv_page_ok(page_size) || !finite_f(scale)) return BFP8_ERR_ARG;
-    if (!latent_sizes_ok(R, max_new, heads) || T < 0 || T >= ((int64_t)1 << 29) / heads ||
+    if (!latent_sizes_ok(R, max_new, heads) || T < 0 || T >= (int64_t)1 << 29 ||
+        T * heads >= (int64_t)1 << 29 ||
         ql_token_stride < 0 || ql_head_stride < 0 || qr_token_stride < 0 || qr_head_stride < 0 ||
         out_token_stride < 0 || out_head_stride < 0 || !kv_slots_ok(num_pages, page_size) ||
         !kv_slots_ok(table_width, page_size))
