@@ -643,7 +643,11 @@ def rope_frequencies(dim, base=10000.0, factor=1.0, trained_len=4096, fast=32.0,
     factor > 1 stretches a model trained on trained_len tokens to factor times as many, by the YaRN
     method: a pair that makes fewer than `slow` turns in trained_len has its frequency divided by
     factor, one that makes more than `fast` keeps it, in between they are mixed linearly over the
-    pair's number; the amplitude is 0.1 ln(factor) + 1 (1 without scaling)."""
+    pair's number; the amplitude is 0.1 ln(factor) + 1 (1 without scaling).
+
+    It belongs to queries and keys that are rotated as a whole: their logits grow by its square.  In
+    attention over a shared latent only a part of the logit is rotated: there, rotate with an
+    amplitude of 1 and multiply attn_latent's scale by its square."""
     _need(dim >= 2 and dim % 2 == 0, "dim must be even")
     _need(factor >= 1.0 and trained_len > 0 and fast >= slow > 0 and base > 1.0,
           "factor >= 1, trained_len > 0, fast >= slow > 0 and base > 1")

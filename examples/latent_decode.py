@@ -1,6 +1,6 @@
 """One layer of latent attention serving a batch, in the absorbed form.
 
-    python examples/latent_decode.py [--requests 16] [--steps 8]
+    python examples/latent_decode.py [--requests 16] [--steps 8] [--factor 1]
 
 Every step plans its pages (bfp8_kv_plan), projects the new tokens' hidden states to queries and to
 the shared latent (bfp8_linear_fp8), rotates the queries (bfp8_rope), brings the latents into the
@@ -9,6 +9,10 @@ paged cache, normed, rotated and quantized (bfp8_latent_append), and attends ove
 outputs.  The first step takes the requests' prompts, the later ones a token each; these are one
 captured graph that carries lengths and the free list along by itself.  At the end the last step's
 attention is compared with float64 over the latents that bfp8_latent_gather reads back.
+
+With --factor, positions are stretched (bfp8.rope_frequencies).  The amplitude that belongs to them
+is one of the whole logit: the rotated dims are only a part of it, so they are turned as they are, and
+its square goes into the scale.
 """
 import argparse
 import os
@@ -31,14 +35,15 @@ SCALE = (NOPE + ROPE) ** -0.5
 class Layer:
     """The layer's weights, its cache, and the buffers of a step of T tokens (of R requests)."""
 
-    def __init__(self, R, max_len, dev):
+    def __init__(self, R, max_len, factor, dev):
         self.w_in = [t.to(dev) for t in synth.weight(Q + KV_ROWS, DIM, 1, 2, -10.0, -4.0)]
         self.w_out = [t.to(dev) for t in synth.weight(DIM, HEADS * VALUE, 3, 4, -10.0, -4.0)]
         # keys and values of a head from the latent: [H, 128, 512], and [H, 512, 128]
         self.w_k = (torch.randn(HEADS, NOPE, LATENT, device=dev) * LATENT ** -0.5).bfloat16()
         self.w_v = (torch.randn(HEADS, LATENT, VALUE, device=dev) * LATENT ** -0.5).bfloat16()
         self.norm = torch.ones(LATENT, dtype=torch.bfloat16, device=dev)
-        self.freq, self.amplitude = bfp8.rope_frequencies(ROPE, device=dev)
+        self.freq, amplitude = bfp8.rope_frequencies(ROPE, factor=factor, device=dev)
+        self.scale = SCALE * amplitude ** 2
         pages = R * -(-max_len // PAGE)
         self.cache = bfp8.latent_cache_buffers(pages, PAGE, dev)
         self.table = torch.zeros(R, -(-max_len // PAGE), dtype=torch.int32, device=dev)
@@ -62,12 +67,12 @@ class Layer:
         bfp8.bfp8_kv_plan(self.ctx, new_lens, self.free, self.table, PAGE, plan, self.free_head)
         bfp8.bfp8_linear_fp8(x, *self.w_in, b["qkv"], b["ws_in"])
         q = b["qkv"][:, :Q].unflatten(1, (HEADS, NOPE + ROPE))
-        bfp8.bfp8_rope(q[..., NOPE:], plan.positions, self.freq, b["q_rope"], True, self.amplitude)
+        bfp8.bfp8_rope(q[..., NOPE:], plan.positions, self.freq, b["q_rope"], True)
         bfp8.bfp8_latent_append(b["qkv"][:, Q:Q + KV], plan.slot_map, plan.positions, self.freq, *self.cache,
-                                norm_weight=self.norm, interleaved=True, amplitude=self.amplitude)
+                                norm_weight=self.norm, interleaved=True)
         b["q_latent"] = (q[..., :NOPE].transpose(0, 1).contiguous() @ self.w_k).transpose(0, 1)     # [T, H, 512]
         bfp8.bfp8_attn_latent(b["q_latent"], b["q_rope"], *self.cache, self.table, plan.q_offsets, plan.kv_lens,
-                              b["max_new"], SCALE, b["out"], None, b["ws"])
+                              b["max_new"], self.scale, b["out"], None, b["ws"])
         values = (b["out"].transpose(0, 1).contiguous() @ self.w_v).transpose(0, 1)                 # [T, H, 128]
         bfp8.bfp8_linear_fp8(values.flatten(1), *self.w_out, b["y"], b["ws_out"])
         # an idle or refused request has a kv_len of 0 and keeps what it has
@@ -82,7 +87,7 @@ class Layer:
         out = []
         for r in range(self.R):
             c, k = latent[ends[r]:ends[r + 1]], rope[ends[r]:ends[r + 1]]
-            s = (b["q_latent"][r].double() @ c.T + b["q_rope"][r].double() @ k.T) * SCALE
+            s = (b["q_latent"][r].double() @ c.T + b["q_rope"][r].double() @ k.T) * self.scale
             out.append(s.softmax(-1) @ c)
         return torch.stack(out)
 
@@ -91,6 +96,7 @@ def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--requests", type=int, default=16)
     ap.add_argument("--steps", type=int, default=8)
+    ap.add_argument("--factor", type=float, default=1.0)
     args = ap.parse_args(argv)
     dev = torch.device("cuda:0")
     torch.cuda.set_device(dev)
@@ -98,7 +104,7 @@ def main(argv=None):
     R = args.requests
     prompts = torch.randint(1, 400, (R,))
     T = int(prompts.sum())
-    layer = Layer(R, 400 + args.steps + 1, dev)
+    layer = Layer(R, 400 + args.steps + 1, args.factor, dev)
 
     layer.step(torch.randn(T, DIM, dtype=torch.bfloat16, device=dev), prompts.to(dev, torch.int32),
                layer.buffers(T, int(prompts.max())))

@@ -521,9 +521,11 @@ size_t bfp8_attn_paged_workspace_size(int64_t R, int64_t max_new, int32_t heads_
  *     (a, b) -> amplitude * (a cos w - b sin w, a sin w + b cos w),  w = positions[t] * inv_freq[p]
  * with (a, b) = (x[2p], x[2p + 1]) if interleaved, (x[p], x[p + dim/2]) if not.
  * Angles are formed in 64 bits, products in fp32, results rounded to bf16 once.
- * Scaled positions for long contexts are a matter of inv_freq and amplitude.  A
- * part of a head is rotated by giving that part alone (a pointer to its first
- * dim, its length as dim).
+ * Scaled positions for long contexts are a matter of inv_freq and amplitude: of
+ * a head that is rotated as a whole, its logits grow by amplitude^2.  Where only a
+ * part is rotated (latent attention), amplitude is 1 and the square belongs to
+ * attention's scale.  A part of a head is rotated by giving that part alone (a
+ * pointer to its first dim, its length as dim).
  *   x_bf16    : bf16, element (t, h, d) at t * x_token_stride + h * x_head_stride + d
  *   out_bf16  : bf16, likewise; x itself with its strides, or no overlap with it
  *   positions : DEVICE int32 [T]; a token whose position is negative is skipped
