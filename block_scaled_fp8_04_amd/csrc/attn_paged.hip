@@ -757,7 +757,6 @@ constexpr int kBlockMaxSplits = 16;
 constexpr int kPartTokens = 256;
 constexpr float kSlack = 8.f;
 
-// x of the two halves of the wave: their maximum, their sum
 // Sum and maximum of the wave's values, in scalar registers.
 template <int kCtrl, int kRows>
 __device__ __forceinline__ int dpp(int x) { return __builtin_amdgcn_update_dpp(0, x, kCtrl, kRows, 0xF, false); }

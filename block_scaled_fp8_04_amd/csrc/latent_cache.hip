@@ -82,10 +82,10 @@ __global__ __launch_bounds__(kLatentThreads) void latent_append_kernel(
     // each half of the wave turns a token's key
     const uint16_t* const key = kv + (half ? t[1] : t[0]) * kv_ts + kLatent;
     const int i0 = interleaved ? 2 * pair : pair, i1 = interleaved ? 2 * pair + 1 : pair + kLatentRope / 2;
-    const float a = bf16_lo(key[i0]), b = bf16_lo(key[i1]);
+    float a = bf16_lo(key[i0]), b = bf16_lo(key[i1]);
     const float2 cs = rotary(half ? at[1] : at[0], inv_freq[pair], amplitude);
-    const float r0 = __builtin_fmaf(a, cs.x, -b * cs.y), r1 = __builtin_fmaf(a, cs.y, b * cs.x);
-    const uint32_t rot = pack_bf16x2(r0, r1);
+    turn(a, b, cs);
+    const uint32_t rot = pack_bf16x2(a, b);
     const uint64_t odd = __ballot((rot & 0x7F80u) == 0x7F80u || (rot >> 16 & 0x7F80u) == 0x7F80u);
     bool bad[2];
 #pragma unroll

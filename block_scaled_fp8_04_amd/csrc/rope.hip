@@ -33,13 +33,6 @@ struct RopeArgs {
     Divisor by_pairs, by_groups, by_heads;   // pairs; groups of a head; heads of a workgroup
 };
 
-// (a, b) packed in w, or a in the low and b in the other word.
-__device__ __forceinline__ void turn(float& a, float& b, const float2 cs) {
-    const float x = a;
-    a = __builtin_fmaf(x, cs.x, -b * cs.y);
-    b = __builtin_fmaf(x, cs.y, b * cs.x);
-}
-
 // kVec: a thread's group is eight elements (interleaved) or twice eight (half layout), 16-byte loads
 // and stores; otherwise it is a pair.
 template <bool kInterleaved, bool kVec>
