@@ -87,33 +87,43 @@ __global__ __launch_bounds__(kLatentThreads) void latent_append_kernel(
     turn(a, b, cs);
     const uint32_t rot = pack_bf16x2(a, b);
     const uint64_t odd = __ballot((rot & 0x7F80u) == 0x7F80u || (rot >> 16 & 0x7F80u) == 0x7F80u);
-    bool bad[2];
+    if (norm_weight) {
+        float mean[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        if (norm_weight) {
+        for (int j = 0; j < 2; ++j) {
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(y[j][i], y[j][i], sum);
-            float mean = wave_add(sum) * (1.f / kLatent) + eps;
-            // squares that may have left fp32's range: those of the row over a power of two near its largest
-            // element, or near eps's root.  (of all lanes, like the sum; NaN stays NaN, infinity becomes it)
-            if (!(mean >= 0x1p-90f && mean <= 0x1p120f)) {
+            mean[j] = wave_add(sum) * (1.f / kLatent) + eps;
+        }
+        // squares that may have left fp32's range: those of the rows over a power of two near the largest
+        // element, or near eps's root.  (Means are those of all lanes; NaN stays NaN, infinity becomes it.)
+        if (!(fminf(mean[0], mean[1]) >= 0x1p-90f && fmaxf(mean[0], mean[1]) <= 0x1p120f)) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
                 uint32_t top = __float_as_uint(__builtin_sqrtf(eps));
 #pragma unroll
                 for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(y[j][i]) & 0x7FFFFFFFu);
                 const int down = 127 - (int)(wave_most(top) >> 23);
-                sum = 0.f;
+                float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     y[j][i] = __builtin_ldexpf(y[j][i], down);
                     sum = __builtin_fmaf(y[j][i], y[j][i], sum);
                 }
-                mean = wave_add(sum) * (1.f / kLatent) + __builtin_ldexpf(eps, 2 * down);
+                mean[j] = wave_add(sum) * (1.f / kLatent) + __builtin_ldexpf(eps, 2 * down);
             }
-            const float f = 1.f / __builtin_sqrtf(mean);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float f = 1.f / __builtin_sqrtf(mean[j]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[j][i] = y[j][i] * f * w[i];
         }
+    }
+    bool bad[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
         // by bit patterns: infinities and NaN are the largest
         uint32_t most = 0;
 #pragma unroll
