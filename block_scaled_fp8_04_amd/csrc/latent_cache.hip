@@ -8,9 +8,9 @@
 //     y = c * rsqrt(mean c^2 + eps) * w        (or y = c), fp32, not rounded in between
 //     s = 2^ceil(log2(max(amax |y|, 1e-4) / 448)),   code = e4m3_rne(y / s)
 // Each half of the wave turns one token's key, a pair a lane: an angle's sine and cosine take some 60
-// instructions.  17312 tokens take 11.5 us alone, 9.5 among other calls (3.3 TB/s read and written), where a
-// token a wave took 10.8; nine waves a SIMD in turn, each loads, two sums over the wave and stores behind
-// one another.
+// instructions.  17312 tokens take 11.6 us alone, 10.6 among other calls (2.9 TB/s read and written), of
+// which a launch that fills no SIMD twice, 64 tokens, takes 3.8: 8656 waves are little more than the eight a SIMD
+// that are resident at once, so nearly all of them load, sum twice over the wave and store at the same time.
 //
 // gather: one wave per eight or four rows: a row's codes are eight a lane, its key eight elements of
 // eight lanes.  194700 rows take 82 us, 4.3 TB/s; 1600 take 6.4: offsets, table, row, one behind the other.

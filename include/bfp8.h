@@ -592,8 +592,10 @@ int bfp8_latent_gather(const void* latent_cache, const float* latent_scales,
  *     x_t = scale * (q_latent . c_t + q_rope . k_t)
  *     out = bf16_rne( sum_t p_t c_t / sum_t p_t ),  p_t = exp(x_t - max),  lse = log sum_t exp(x_t)
  * with c_t the token's 512 latent values and k_t its 64 rotated dims.  A row that
- * sees nothing gets zeros, and -infinity.  Logits, sums and statistics are fp32; p_t
- * enters its product with eleven significant bits (2^-11 of it at most is lost).
+ * sees nothing gets zeros, and -infinity.  Logits, sums and statistics are fp32.  p_t
+ * scale_t enters its product with the token's codes rounded to fp16, against a power of
+ * two near the row's largest: it loses 2^-11 of itself at most, or 2^-29 of that largest if
+ * this is more.  A token 2^-132 below the largest counts for nothing, in the norm as well.
  *   q_latent_bf16 : bf16, element (t, j, d) at t * ql_token_stride + j * ql_head_stride + d,
  *              d < 512, rows 0 .. T-1; q_rope_bf16 likewise, d < 64
  *   block_table : DEVICE int32 [R, table_width]; entries up to kv_len are read,
@@ -601,7 +603,10 @@ int bfp8_latent_gather(const void* latent_cache, const float* latent_scales,
  *   q_offsets : DEVICE int32 [R+1], kv_lens : DEVICE int32 [R], as bfp8_kv_plan
  *              writes them (any values stay inside the buffers)
  *   max_new  : host upper bound of the requests' new tokens; rows of a request
- *              past it are not written
+ *              past it are not written.  From R * ceil(max_new * heads / 64) = 1024 on
+ *              (/ 32 with up to 32 rows a request) no request's tokens are shared by
+ *              workgroups: a batch of one long chunk and long caches that decode takes
+ *              less time as two calls, each with its rows of block_table, q_offsets, kv_lens
  *   out_bf16 : bf16, element (t, j, d) at t * out_token_stride + j * out_head_stride + d,
  *              16-byte aligned, strides multiples of 8, rows not overlapping; rows of
  *              no request are not written
@@ -609,8 +614,8 @@ int bfp8_latent_gather(const void* latent_cache, const float* latent_scales,
  *   workspace: DEVICE, at least bfp8_attn_latent_workspace_size(...) bytes, 16-byte
  *              aligned, any contents: partial results of token ranges; NULL lets every
  *              row's tokens be walked in one piece
- * Sums are fp32 and p may reach 2^8 in them: latents beyond 2^100 may overflow in the
- * rows that see them.  Deterministic.
+ * A logit past fp32's range (latents of 2^100 against queries of 2^28) may make its row NaN.
+ * Deterministic.
  * Errors: BFP8_ERR_SHAPE if a size or stride is negative, T * heads >= 2^29, max_new < 1 (with
  * R, T > 0), heads < 1, heads > 65535, max_new * heads >= 2^31, or num_pages or table_width
  * times page_size >= 2^31; BFP8_ERR_GROUPS if R > BFP8_KV_MAX_REQUESTS; BFP8_ERR_ARG for a
